@@ -70,6 +70,11 @@ typedef enum { LMH_F32 = 0, LMH_BF16 = 1, LMH_F16 = 2 } lmh_dtype_t;
                                     the row was treated as ignored          */
 #define LMH_DEV_PIPE_TIMEOUT 0x2 /* a pipeline wait gave up (bounded spin);
                                     the output of that call is not valid    */
+#define LMH_DEV_BAD_LOGIT 0x4    /* beam_select met a logit that is NaN or not
+                                    below 1e38, or a score of NaN or +inf; each
+                                    was taken as -inf                       */
+#define LMH_DEV_BAD_PARENT 0x10  /* beam_reorder met a parent outside [0, W);
+                                    that beam's state was left as it was    */
 
 /* Same type as cudaStream_t. */
 typedef struct CUstream_st *lmh_stream_t;
@@ -253,6 +258,62 @@ LMH_API lmh_status_t lmhead_bwd_dw(const void *dlogits, const void *X, void *dW,
  *   Requirements as lmhead_bwd_dw. */
 LMH_API lmh_status_t lmhead_bwd_dw_acc(const void *dlogits, const void *X, float *dW, int64_t M,
                                        int64_t K, int64_t V, int32_t *status, lmh_stream_t stream);
+
+/* One step of beam search over the logits: of all continuations of the W beams
+ * of each of N batch entries, the C best, and the W beams that go on (no
+ * counterpart on the pages; the log-softmax is that of ce_fwd).
+ *   logits  [N,W,V] FP32 or BF16 (logits_dtype), as lmhead_fwd or
+ *           lmhead_fwd_lora store them.   scores [N,W] FP32, log-probability
+ *           of each beam so far.
+ *   total[w,v] = scores[w] + logits[w,v] - log sum_v exp(logits[w,v]).
+ *   done    [N] int32 or NULL: an entry with done != 0 is not read and keeps
+ *           its beams (next_score = scores, next_beam = w); its candidates are
+ *           (-inf, -1, -1).
+ *   cand_score / cand_beam / cand_token [N,C] (FP32, int32, int64): the C best
+ *           continuations, best first, compared by the FP64 value of total and,
+ *           where equal, by the lower w * V + v.  A logit or score of -inf
+ *           forbids a continuation: where fewer than C are possible the rest is
+ *           (-inf, -1, -1).
+ *   next_score / next_beam / next_token [N,W], all three or none (NULL): the
+ *           first W candidates whose token is not eos (eos = -1: none is), in
+ *           order.  Places that no candidate fills get (-inf, w, eos, or 0 for
+ *           eos = -1), w being the place itself.
+ *   workspace: device scratch of beam_select_workspace_bytes(N, W, V, C) bytes,
+ *           16-byte aligned; its contents do not matter before or after.
+ *   Limits: W <= 64, C <= 128, and with next_*: C >= 2 W (C >= W for eos = -1),
+ *   so that W candidates go on however many end; -1 <= eos < V.  Any V >= 1;
+ *   logits aligned to its element.  Deterministic.  Logits that are NaN or not
+ *   below 1e38 set LMH_DEV_BAD_LOGIT and count as -inf. */
+LMH_API lmh_status_t beam_select(const void *logits, int32_t logits_dtype, const float *scores,
+                                 const int32_t *done, float *cand_score, int32_t *cand_beam,
+                                 int64_t *cand_token, float *next_score, int32_t *next_beam,
+                                 int64_t *next_token, void *workspace, int64_t workspace_bytes,
+                                 int64_t N, int64_t W, int64_t V, int64_t C, int64_t eos,
+                                 int32_t *status, lmh_stream_t stream);
+
+/* Scratch bytes beam_select needs: per beam and 8192 logits 16 + 8 C bytes.  -1
+ * for sizes out of range. */
+LMH_API int64_t beam_select_workspace_bytes(int64_t N, int64_t W, int64_t V, int64_t C);
+
+/* Puts the beams' states (caches, token histories) in the order of their
+ * parents, in place: state[.., n, w, ..] = old state[.., n, parents[n,w], ..].
+ * Beams whose parent is their own place are not touched.
+ *   states   HOST array of num_states (1..128) device pointers to states of one
+ *            geometry: element (o, n, w) starts at
+ *            sum_i o_i outer_stride[i] + n entry_stride + w beam_stride and has
+ *            run_bytes contiguous bytes; outer and outer_stride are HOST arrays
+ *            of num_outer (0..3) extents and strides.  All strides in bytes.
+ *            Elements of a state must not overlap (checked from the strides);
+ *            different states must not either (equal pointers are refused).
+ *   parents  [N,W] int32 (beam_select's next_beam).  A parent outside [0, W)
+ *            sets LMH_DEV_BAD_PARENT and leaves that beam's state as it was.
+ *   Limits: N <= 65535, W <= 64.  Any alignment: 16-byte copies where the
+ *   pointers, strides and run_bytes allow them, narrower ones otherwise. */
+LMH_API lmh_status_t beam_reorder(void *const *states, int64_t num_states, const int32_t *parents,
+                                  int64_t N, int64_t W, int64_t entry_stride, int64_t beam_stride,
+                                  int64_t run_bytes, const int64_t *outer,
+                                  const int64_t *outer_stride, int64_t num_outer, int32_t *status,
+                                  lmh_stream_t stream);
 
 /* Static, NUL-terminated description of a status value. */
 LMH_API const char *lmh_status_string(lmh_status_t s);

@@ -1,0 +1,597 @@
+// beam_kernels.cuh -- beam search over the LM head's logits: the best
+// continuations over beams and vocabulary, and the beams' states put in the
+// order of their parents.
+//
+// Selection.  A continuation of beam w by token v scores
+//     total(w, v) = score_w + x_wv - lse_w,   lse_w = log sum_v exp(x_wv).
+// Within a row the order is that of the logits, so the best C of a row are
+// among the best C logits of each of its chunks, and one pass over the logits
+// gives both those and the chunk's share of lse_w:
+//   beam_scan_kernel   one CTA per 8192-logit chunk, held in registers: maximum,
+//                      sum of exponentials, best C logits
+//   beam_merge_kernel  one CTA per batch entry: lse of every beam, the best C
+//                      of all beams' candidates, the beams that go on
+// Continuations are compared by the FP64 value of total, ties by the lower
+// w * V + v: an FP32 total has a step of 1e-6 at -15, which the gaps between
+// candidates of a large batch do meet.
+#pragma once
+#include <cstdint>
+#include <cuda_bf16.h>
+
+#include "ptx.cuh"
+
+namespace lmh {
+
+constexpr int kBeamThreads = 256;
+constexpr int kBeamWarps = kBeamThreads / 32;
+constexpr int kBeamPerThread = 32;                              // logits a thread holds
+constexpr int kBeamChunk = kBeamThreads * kBeamPerThread;       // logits of one CTA
+constexpr int kBeamBuf = 1024;        // candidates at or above the threshold a CTA can hold
+constexpr int kBeamMaxCand = 128;
+constexpr int kBeamMaxWidth = 64;
+constexpr float kBeamMaxLogit = 1e38f;
+constexpr int kBeamDevBadLogit = 0x4;   // LMH_DEV_BAD_LOGIT
+constexpr int kBeamDevBadParent = 0x10; // LMH_DEV_BAD_PARENT
+
+// One logit chunk's share of its row.
+struct BeamPartial {
+    double sum;     // sum of 2^(x log2(e) - ref)
+    float ref;      // integer-valued: rint(max * log2(e)); -inf if no finite logit
+    int32_t count;  // candidates in the chunk's list
+};
+
+struct BeamCand {
+    float x;      // the logit
+    int32_t tok;  // its token
+};
+
+// Order-preserving map of a float to an unsigned integer (-inf lowest).
+__device__ __forceinline__ uint32_t ordered(float x)
+{
+    const uint32_t u = __float_as_uint(x);
+    return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+}
+
+__device__ __forceinline__ float from_ordered(uint32_t k)
+{
+    return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
+}
+
+__device__ __forceinline__ double warp_sum(double v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// A value that at least `want` of the block's per-thread maxima reach, found
+// from the q-th largest maximum of each warp: the h-th largest of those, with
+// h warps x q lanes >= want.  h = 4 of the 8 warps: near the median warp the
+// threshold lets about twice `want` values through (h = 1 about six times as
+// many, h = 8 three times).  -inf when too few threads hold a finite value.
+// `red` has kBeamWarps entries.
+__device__ __forceinline__ float block_threshold(float best, int want, uint32_t *red)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int h = want > 4 * 32 ? 8 : 4;
+    const int q = (want + h - 1) / h;
+    uint32_t key = ordered(best), kth = 0;
+    for (int i = 0; i < q; ++i) {
+        kth = __reduce_max_sync(0xffffffffu, key);
+        const unsigned at = __ballot_sync(0xffffffffu, key == kth);
+        if (lane == __ffs(at) - 1)
+            key = 0;
+    }
+    if (lane == 0)
+        red[warp] = kth;
+    __syncthreads();
+    uint32_t t = 0;
+#pragma unroll
+    for (int i = 0; i < kBeamWarps; ++i) {
+        int above = 0;  // warps ahead of warp i (ties by warp number)
+#pragma unroll
+        for (int j = 0; j < kBeamWarps; ++j)
+            above += red[j] > red[i] || (red[j] == red[i] && j < i);
+        if (above == h - 1)
+            t = red[i];
+    }
+    return t ? from_ordered(t) : -INFINITY;
+}
+
+__device__ __forceinline__ uint4 ldg_vec(const void *p)
+{
+    uint4 u;
+    asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                 : "l"(p));
+    return u;
+}
+
+template <typename T>
+struct BeamVec;
+template <>
+struct BeamVec<float> {
+    static constexpr int N = 4;
+    static __device__ __forceinline__ void unpack(const uint32_t (&u)[4], float *x)
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            x[i] = __uint_as_float(u[i]);
+    }
+    static __device__ __forceinline__ float one(const float *p) { return *p; }
+};
+template <>
+struct BeamVec<__nv_bfloat16> {
+    static constexpr int N = 8;
+    static __device__ __forceinline__ void unpack(const uint32_t (&u)[4], float *x)
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(u[i] << 16);
+            x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        }
+    }
+    static __device__ __forceinline__ float one(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
+};
+
+// The 16 bytes that begin `bytes` (0 <= bytes < 16, a multiple of 2) past the
+// 16-byte boundary p, out of the vectors they lie in (one where bytes is 0).
+__device__ __forceinline__ void ldg_straddle(const void *p, int bytes, uint32_t (&u)[4])
+{
+    const uint4 a = ldg_vec(p);
+    uint4 b = a;
+    if (bytes)
+        b = ldg_vec(static_cast<const uint4 *>(p) + 1);
+    uint32_t w[5];  // the words from the one that holds the first byte on
+    switch (bytes >> 2) {
+    case 0: w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x; break;
+    case 1: w[0] = a.y, w[1] = a.z, w[2] = a.w, w[3] = b.x, w[4] = b.y; break;
+    case 2: w[0] = a.z, w[1] = a.w, w[2] = b.x, w[3] = b.y, w[4] = b.z; break;
+    default: w[0] = a.w, w[1] = b.x, w[2] = b.y, w[3] = b.z, w[4] = b.w; break;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        u[i] = __funnelshift_r(w[i], w[i + 1], (bytes & 2) * 8);
+}
+
+__device__ __forceinline__ bool beam_live(float score) { return score > -INFINITY && score < INFINITY; }
+
+// One CTA per chunk of a row.  A logit's thread and place go by its column alone,
+// so that equal rows give equal sums and their ties fall by beam number wherever
+// the rows start (V may be odd).  A row that does not start on 16 bytes is read
+// in the aligned vectors around each 16 bytes (the second of the two is the
+// neighbour's first, an L1 hit), and its first and last elements one by one.
+// Rows of beams that cannot go on (score -inf) and of entries that are done are
+// not read.
+template <typename T>
+__global__ void __launch_bounds__(kBeamThreads, 4)
+    beam_scan_kernel(const T *__restrict__ logits, const float *__restrict__ scores,
+                     const int32_t *__restrict__ done, BeamPartial *__restrict__ part,
+                     BeamCand *__restrict__ cand, int32_t W, int64_t V, int32_t C, int32_t chunks,
+                     int32_t *status)
+{
+    constexpr int VN = BeamVec<T>::N;
+    __shared__ uint32_t red[kBeamWarps];
+    __shared__ double red_sum[kBeamWarps];
+    __shared__ uint64_t buf[kBeamBuf];
+    __shared__ int count;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t row = blockIdx.x / chunks;
+    const int chunk = static_cast<int>(blockIdx.x - row * chunks);
+    if ((done && done[row / W]) || !beam_live(scores[row]))
+        return;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const T *x0 = logits + row * V;
+    const int64_t base = static_cast<int64_t>(chunk) * kBeamChunk;  // column of the chunk's start
+    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(x0) & 15);  // bytes past a boundary
+    const int offe = off / static_cast<int>(sizeof(T));
+
+    float x[kBeamPerThread];
+    bool bad = false;
+    if (off == 0 && base + kBeamChunk <= V) {  // every load in flight at once
+        uint4 q[kBeamPerThread / VN];
+#pragma unroll
+        for (int i = 0; i < kBeamPerThread / VN; ++i)
+            q[i] = ldg_vec(x0 + base + (i * kBeamThreads + tid) * VN);
+#pragma unroll
+        for (int i = 0; i < kBeamPerThread / VN; ++i) {
+            const uint32_t u[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+            BeamVec<T>::unpack(u, x + i * VN);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kBeamPerThread / VN; ++i) {
+            const int64_t v = base + (i * kBeamThreads + tid) * VN;
+            if (v >= offe && v - offe + (off ? 2 : 1) * VN <= V) {
+                uint32_t u[4];
+                ldg_straddle(x0 + v - offe, off, u);
+                BeamVec<T>::unpack(u, x + i * VN);
+            } else {
+#pragma unroll
+                for (int e = 0; e < VN; ++e)
+                    x[i * VN + e] = v + e < V ? BeamVec<T>::one(x0 + v + e) : -INFINITY;
+            }
+        }
+    }
+    if (tid == 0)
+        count = 0;
+    float best = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kBeamPerThread; ++i) {
+        const bool ok = x[i] < kBeamMaxLogit;  // NaN, +inf and what log2(e) times would be: -inf
+        bad |= !ok;
+        x[i] = ok ? x[i] : -INFINITY;
+        best = fmaxf(best, x[i]);
+    }
+    if (__any_sync(0xffffffffu, bad) && lane == 0 && status)
+        atomicOr(status, kBeamDevBadLogit);
+
+    const uint32_t wmax = __reduce_max_sync(0xffffffffu, ordered(best));
+    // the block's maximum comes with the threshold: both go through `red`
+    if (lane == 0)
+        red[warp] = wmax;
+    __syncthreads();
+    uint32_t bmax = red[0];
+#pragma unroll
+    for (int i = 1; i < kBeamWarps; ++i)
+        bmax = max(bmax, red[i]);
+    const float top = from_ordered(bmax);
+    __syncthreads();
+    BeamPartial *pp = part + row * chunks + chunk;
+    if (top == -INFINITY) {  // the same for the whole block
+        if (tid == 0)
+            *pp = BeamPartial{0.0, -INFINITY, 0};
+        return;
+    }
+    const float thr = block_threshold(best, C, red);
+
+    // Sum of exponentials against an integer power of two: x log2(e) - ref is
+    // then rounded once per term, near its own size (log2(e) as two floats, so
+    // that large logits keep their last places); short FP32 sums, joined in
+    // FP64, leave lse good to about 1e-8.
+    constexpr float kLh = 1.44269502162933349609f, kLl = 1.92596303e-8f;
+    const float ref = rintf(top * kLh);
+    float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < kBeamPerThread; ++i) {
+        const float t = fmaf(x[i], kLl, fmaf(x[i], kLh, -ref));
+        float y;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(t));
+        s4[i & 3] += y;
+    }
+    const double ws = warp_sum(static_cast<double>((s4[0] + s4[1]) + (s4[2] + s4[3])));
+    if (lane == 0)
+        red_sum[warp] = ws;
+
+    if (best >= thr) {
+#pragma unroll
+        for (int i = 0; i < kBeamPerThread; ++i)
+            if (x[i] >= thr && x[i] > -INFINITY) {
+                const int at = atomicAdd(&count, 1);
+                const int64_t v = base + ((i / VN) * kBeamThreads + tid) * VN + i % VN;
+                // higher is better: logit first, then the lower token
+                if (at < kBeamBuf)
+                    buf[at] = (static_cast<uint64_t>(ordered(x[i])) << 32) | (0xffffffffu - static_cast<uint32_t>(v));
+            }
+    }
+    __syncthreads();
+    const int n = count;
+    BeamCand *out = cand + (row * chunks + chunk) * C;
+    int kept;
+    if (n <= kBeamBuf) {
+        kept = n < C ? n : C;
+        for (int i = tid; i < n; i += kBeamThreads) {
+            const uint64_t k = buf[i];
+            int rank = 0;
+            for (int j = 0; j < n; ++j)
+                rank += buf[j] > k;
+            if (rank < C)
+                out[rank] = BeamCand{from_ordered(static_cast<uint32_t>(k >> 32)),
+                                     static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(k))};
+        }
+    } else {
+        // more values at the threshold than fit (many equal logits): the best
+        // one below the last, C times
+        __shared__ uint64_t win[kBeamWarps];
+        uint64_t last = ~0ull;
+        for (kept = 0; kept < C; ++kept) {
+            uint64_t b = 0;
+#pragma unroll
+            for (int i = 0; i < kBeamPerThread; ++i) {
+                const int64_t v = base + ((i / VN) * kBeamThreads + tid) * VN + i % VN;
+                const uint64_t k = (static_cast<uint64_t>(ordered(x[i])) << 32) | (0xffffffffu - static_cast<uint32_t>(v));
+                if (x[i] > -INFINITY && k < last && k > b)
+                    b = k;
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                const uint64_t c = __shfl_xor_sync(0xffffffffu, b, o);
+                b = c > b ? c : b;
+            }
+            if (lane == 0)
+                win[warp] = b;
+            __syncthreads();
+            b = win[0];
+#pragma unroll
+            for (int i = 1; i < kBeamWarps; ++i)
+                b = win[i] > b ? win[i] : b;
+            __syncthreads();
+            if (b == 0)
+                break;
+            last = b;
+            if (tid == 0)
+                out[kept] = BeamCand{from_ordered(static_cast<uint32_t>(b >> 32)),
+                                     static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(b))};
+        }
+    }
+    if (tid == 0) {
+        double s = 0.0;
+#pragma unroll
+        for (int i = 0; i < kBeamWarps; ++i)
+            s += red_sum[i];
+        *pp = BeamPartial{s, ref, kept};
+    }
+}
+
+struct BeamOut {
+    float *cand_score;
+    int32_t *cand_beam;
+    int64_t *cand_token;
+    float *next_score;
+    int32_t *next_beam;
+    int64_t *next_token;
+};
+
+// A candidate of the merge: the FP64 total and the place w * V + v.
+struct BeamKey {
+    double total;
+    int64_t at;
+};
+
+__device__ __forceinline__ bool ahead(const BeamKey &a, const BeamKey &b)
+{
+    return a.total > b.total || (a.total == b.total && a.at < b.at);
+}
+
+// One CTA per batch entry.  The candidates of all chunks of all beams are read
+// twice from L2 (a few KB): once for a threshold, once for those that reach it.
+__global__ void __launch_bounds__(kBeamThreads)
+    beam_merge_kernel(const float *__restrict__ scores, const int32_t *__restrict__ done,
+                      const BeamPartial *part, const BeamCand *cand, BeamOut o, int32_t W, int64_t V,
+                      int32_t C, int32_t chunks, int64_t eos, int32_t *status)
+{
+    __shared__ double off[kBeamMaxWidth];   // score - lse; -inf for a beam with no continuation
+    __shared__ uint32_t red[kBeamWarps];
+    __shared__ BeamKey buf[kBeamBuf];
+    __shared__ BeamKey win[kBeamWarps];
+    __shared__ BeamKey sorted[kBeamMaxCand];
+    __shared__ int count;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t n = blockIdx.x;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (done && done[n]) {
+        // nothing is chosen: every beam stays where it is
+        for (int i = tid; i < C; i += kBeamThreads) {
+            o.cand_score[n * C + i] = -INFINITY;
+            o.cand_beam[n * C + i] = -1;
+            o.cand_token[n * C + i] = -1;
+        }
+        if (o.next_score)
+            for (int w = tid; w < W; w += kBeamThreads) {
+                o.next_score[n * W + w] = scores[n * W + w];
+                o.next_beam[n * W + w] = w;
+                o.next_token[n * W + w] = eos < 0 ? 0 : eos;
+            }
+        return;
+    }
+    if (tid == 0)
+        count = 0;
+    for (int w = warp; w < W; w += kBeamWarps) {
+        const float sc = scores[n * W + w];
+        double r = -INFINITY;
+        if (beam_live(sc)) {
+            const BeamPartial *pp = part + (n * W + w) * chunks;
+            float c = -INFINITY;
+            for (int k = lane; k < chunks; k += 32)
+                c = fmaxf(c, pp[k].ref);
+            c = from_ordered(__reduce_max_sync(0xffffffffu, ordered(c)));
+            if (c > -INFINITY) {
+                double s = 0.0;
+                for (int k = lane; k < chunks; k += 32)
+                    if (pp[k].ref > -INFINITY)
+                        s += pp[k].sum * exp2(static_cast<double>(pp[k].ref) - static_cast<double>(c));
+                s = warp_sum(s);
+                constexpr double kLn2 = 0.69314718055994530942;
+                r = static_cast<double>(sc) - (static_cast<double>(c) + log2(s)) * kLn2;
+            }
+        } else if (lane == 0 && status && !(sc < INFINITY)) {
+            atomicOr(status, kBeamDevBadLogit);  // a score of NaN or +inf
+        }
+        if (lane == 0)
+            off[w] = r;
+    }
+    __syncthreads();
+
+    const int per_row = chunks * C;
+    const int items = W * per_row;
+    // item i: rank i % C of chunk (i / C) % chunks of beam i / per_row
+    auto load = [&](int i, BeamKey &k) -> bool {
+        const int w = i / per_row, rest = i - w * per_row;
+        if (off[w] == -INFINITY)
+            return false;
+        const int64_t rc = (n * W + w) * chunks + rest / C;
+        if (rest % C >= part[rc].count)
+            return false;
+        const BeamCand c = cand[rc * C + rest % C];
+        k.total = off[w] + static_cast<double>(c.x);
+        k.at = w * V + c.tok;
+        return true;
+    };
+    // rounded down, so that a thread's maximum is a bound its candidate reaches
+    float best = -INFINITY;
+    for (int i = tid; i < items; i += kBeamThreads) {
+        BeamKey k;
+        if (load(i, k))
+            best = fmaxf(best, __double2float_rd(k.total));
+    }
+    const float thr = block_threshold(best, C, red);
+    if (best >= thr && best > -INFINITY)
+        for (int i = tid; i < items; i += kBeamThreads) {
+            BeamKey k;
+            if (load(i, k) && k.total >= static_cast<double>(thr)) {
+                const int at = atomicAdd(&count, 1);
+                if (at < kBeamBuf)
+                    buf[at] = k;
+            }
+        }
+    __syncthreads();
+    const int m = count;
+    int kept;
+    if (m <= kBeamBuf) {
+        kept = m < C ? m : C;
+        for (int i = tid; i < m; i += kBeamThreads) {
+            const BeamKey k = buf[i];
+            int rank = 0;
+            for (int j = 0; j < m; ++j)
+                rank += ahead(buf[j], k);
+            if (rank < C)
+                sorted[rank] = k;
+        }
+        __syncthreads();
+    } else {
+        BeamKey last{INFINITY, -1};
+        for (kept = 0; kept < C; ++kept) {
+            BeamKey b{-INFINITY, INT64_MAX};
+            for (int i = tid; i < items; i += kBeamThreads) {
+                BeamKey k;
+                if (load(i, k) && ahead(last, k) && ahead(k, b))
+                    b = k;
+            }
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1) {
+                const BeamKey c{__shfl_xor_sync(0xffffffffu, b.total, s),
+                                __shfl_xor_sync(0xffffffffu, b.at, s)};
+                if (ahead(c, b))
+                    b = c;
+            }
+            if (lane == 0)
+                win[warp] = b;
+            __syncthreads();
+            b = win[0];
+            for (int i = 1; i < kBeamWarps; ++i)
+                if (ahead(win[i], b))
+                    b = win[i];
+            __syncthreads();
+            if (b.total == -INFINITY)
+                break;
+            last = b;
+            if (tid == 0)
+                sorted[kept] = b;
+        }
+        __syncthreads();
+    }
+    int gone_on = 0;  // candidates before this one that do not end their sequence
+    for (int i = tid; i < C; i += kBeamThreads) {
+        const bool have = i < kept;
+        const int32_t beam = have ? static_cast<int32_t>(sorted[i].at / V) : -1;
+        const int64_t tok = have ? sorted[i].at - beam * V : -1;
+        const float sc = have ? static_cast<float>(sorted[i].total) : -INFINITY;
+        o.cand_score[n * C + i] = sc;
+        o.cand_beam[n * C + i] = beam;
+        o.cand_token[n * C + i] = tok;
+        if (o.next_score && have && tok != eos) {
+            gone_on = 0;
+            for (int j = 0; j < i; ++j)
+                gone_on += sorted[j].at % V != eos;
+            if (gone_on < W) {
+                o.next_score[n * W + gone_on] = sc;
+                o.next_beam[n * W + gone_on] = beam;
+                o.next_token[n * W + gone_on] = tok;
+            }
+        }
+    }
+    if (o.next_score && warp == 0) {
+        // places that no candidate fills: a dead beam that stays where it is
+        int live = 0;
+        for (int i = lane; i < kept; i += 32)
+            live += sorted[i].at % V != eos;
+        live = __reduce_add_sync(0xffffffffu, live);
+        for (int w = live + lane; w < W; w += 32) {
+            o.next_score[n * W + w] = -INFINITY;
+            o.next_beam[n * W + w] = w;
+            o.next_token[n * W + w] = eos < 0 ? 0 : eos;
+        }
+    }
+}
+
+// ---------------------------------------------------------------- reorder
+
+constexpr int kReorderMaxStates = 128;
+constexpr int kReorderThreads = 256;
+
+struct ReorderParams {
+    uint8_t *state[kReorderMaxStates];
+    int64_t entry_stride, beam_stride;  // bytes
+    int64_t outer_stride[3];
+    uint32_t outer[3];                  // extents (1 where unused)
+    uint32_t run_vecs;                  // vectors in the contiguous run
+    uint32_t columns;                   // outer[0] * outer[1] * outer[2] * run_vecs
+    int32_t W;
+    const int32_t *parents;
+    int32_t *status;
+};
+
+// state[.., n, w, ..] = old state[.., n, parents[n][w], ..], in place: a thread
+// owns one vector-wide column of an entry, reads what every beam whose parent
+// is another takes over, and only then writes.  No row that stays is touched,
+// and a row that several beams take is read from memory once (L1 serves the
+// rest), so the traffic is the rows wanted plus the rows changed.
+// MAXW bounds W at compile time, so that the column's values stay in registers:
+// vectors of 16 bytes up to 16 beams, 8 up to 32, 4 up to 64.
+template <typename VecT, int MAXW>
+__global__ void __launch_bounds__(kReorderThreads)
+    beam_reorder_kernel(const __grid_constant__ ReorderParams p)
+{
+    __shared__ int32_t from[kBeamMaxWidth];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t n = blockIdx.y;
+    bool moves = false;
+    if (threadIdx.x < p.W) {
+        const int w = threadIdx.x;
+        int q = p.parents[n * p.W + w];
+        if (q < 0 || q >= p.W) {
+            if (p.status && blockIdx.x == 0 && blockIdx.z == 0)
+                atomicOr(p.status, kBeamDevBadParent);
+            q = w;  // the row is left as it is
+        }
+        from[w] = q;
+        moves = q != w;
+    }
+    if (!__syncthreads_or(moves))
+        return;
+    uint8_t *base = p.state[blockIdx.z] + n * p.entry_stride;
+    for (uint32_t c = blockIdx.x * kReorderThreads + threadIdx.x; c < p.columns;
+         c += gridDim.x * kReorderThreads) {
+        uint32_t r = c / p.run_vecs;
+        const uint32_t v = c - r * p.run_vecs;
+        const uint32_t r1 = r / p.outer[0], i0 = r - r1 * p.outer[0];
+        const uint32_t i2 = r1 / p.outer[1], i1 = r1 - i2 * p.outer[1];
+        uint8_t *col = base + i0 * p.outer_stride[0] + i1 * p.outer_stride[1] + i2 * p.outer_stride[2] +
+                       static_cast<int64_t>(v) * sizeof(VecT);
+        VecT x[MAXW];
+#pragma unroll
+        for (int w = 0; w < MAXW; ++w)
+            if (w < p.W && from[w] != w)
+                x[w] = *reinterpret_cast<const VecT *>(col + from[w] * p.beam_stride);
+#pragma unroll
+        for (int w = 0; w < MAXW; ++w)
+            if (w < p.W && from[w] != w)
+                *reinterpret_cast<VecT *>(col + w * p.beam_stride) = x[w];
+    }
+}
+
+}  // namespace lmh

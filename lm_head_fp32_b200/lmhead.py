@@ -20,13 +20,16 @@ LMH_OK, LMH_ERR_INVALID_ARG, LMH_ERR_MISALIGNED, LMH_ERR_UNSUPPORTED, LMH_ERR_CU
 F32, BF16, F16 = 0, 1, 2
 DEV_BAD_TARGET = 0x1
 DEV_PIPE_TIMEOUT = 0x2
+DEV_BAD_LOGIT = 0x4
+DEV_BAD_PARENT = 0x10
 IGNORE_INDEX = -100
 
 EXPORTS = ("lmhead_fwd", "ce_fwd", "ce_bwd", "lmhead_bwd_dx", "lmhead_bwd_dw",
            "lmhead_fwd_ce", "lmhead_fwd_ce_workspace_bytes", "lmhead_fwd_ce_noalloc",
            "lmhead_bwd_dw_acc", "ce_fwd_shard", "ce_merge_shards", "ce_bwd_shard",
            "lmh_status_string", "lmh_version", "lmh_watchdog_selftest",
-           "lmh_gemm_watchdog_selftest")
+           "lmh_gemm_watchdog_selftest", "beam_select", "beam_select_workspace_bytes",
+           "beam_reorder")
 
 _lib = None
 
@@ -73,6 +76,12 @@ def lib() -> ctypes.CDLL:
         L.lmh_watchdog_selftest.restype = ctypes.c_int
         L.lmh_gemm_watchdog_selftest.argtypes = [P, P, P, I64, I64, I64, I64, P, P]
         L.lmh_gemm_watchdog_selftest.restype = ctypes.c_int
+        L.beam_select.argtypes = [P, I32, P, P, P, P, P, P, P, P, P, I64, I64, I64, I64, I64, I64, P, P]
+        L.beam_select_workspace_bytes.argtypes = [I64, I64, I64, I64]
+        L.beam_select_workspace_bytes.restype = I64
+        L.beam_reorder.argtypes = [P, I64, P, I64, I64, I64, I64, I64, P, P, I64, P, P]
+        for f in ("beam_select", "beam_reorder"):
+            getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -235,7 +244,8 @@ def gemm_watchdog_selftest(X: torch.Tensor, W: torch.Tensor, logits: torch.Tenso
     assert W.shape[1] == K and tuple(logits.shape) == (M, V) and logits.dtype == torch.float32
     _check(lib().lmh_gemm_watchdog_selftest(_ptr(X), _ptr(W), _ptr(logits), M, K, V,
                                             int(limit_ns), _ptr(status), _stream(stream)),
-           "lmh_gemm_watchdog_selftest")
+           "lmh_gemm_watchdog_selftest", "beam_select", "beam_select_workspace_bytes",
+           "beam_reorder")
 
 
 def lmhead_bwd_dw_acc(dlogits: torch.Tensor, X: torch.Tensor, dW: torch.Tensor,
@@ -289,3 +299,137 @@ def ce_bwd_shard(logits: torch.Tensor, target: torch.Tensor, stats: torch.Tensor
                               int(vocab_total), int(ignore_index), _ptr(status), _stream(stream)),
            "ce_bwd_shard")
     return dlogits
+
+
+def _take(name: str, t: Optional[torch.Tensor], shape, *dtypes, like: Optional[torch.Tensor] = None):
+    """Check one argument of a call (contiguous, its shape, one of its dtypes, on
+    the device of `like`) and return its address; None passes through."""
+    if t is None:
+        return None
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous (row-major)")
+    if like is not None and t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+    return t.data_ptr()
+
+
+def _workspace(t: torch.Tensor, like: torch.Tensor):
+    """(address, bytes) of a caller's scratch buffer."""
+    if not t.is_contiguous() or t.device != like.device:
+        raise ValueError(f"workspace must be contiguous and on {like.device}")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _status(status: Optional[torch.Tensor], like: torch.Tensor):
+    return _take("status", status, (1,), torch.int32, like=like)
+
+
+def _on(like: torch.Tensor, stream, fn, *args) -> int:
+    """fn(*args, stream) with the device of `like` current; stream None is that
+    device's current stream."""
+    if not like.is_cuda:
+        raise ValueError("expected CUDA tensors (the library has no CPU path)")
+    dev = like.device.index
+    if dev == torch.cuda.current_device():
+        s = torch.cuda.current_stream() if stream is None else stream
+        return fn(*args, s.cuda_stream)
+    with torch.cuda.device(dev):
+        s = torch.cuda.current_stream() if stream is None else stream
+        return fn(*args, s.cuda_stream)
+
+
+def beam_select_workspace_bytes(N: int, W: int, V: int, C: int) -> int:
+    """Scratch bytes beam_select needs for N entries of W beams, a vocabulary of
+    V and C candidates (-1 for sizes out of range)."""
+    return int(lib().beam_select_workspace_bytes(int(N), int(W), int(V), int(C)))
+
+
+def beam_select(logits: torch.Tensor, scores: torch.Tensor, cand_score: torch.Tensor,
+                cand_beam: torch.Tensor, cand_token: torch.Tensor,
+                next_score: Optional[torch.Tensor], next_beam: Optional[torch.Tensor],
+                next_token: Optional[torch.Tensor], workspace: torch.Tensor, eos: int = -1,
+                done: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                stream=None):
+    """One step of beam search: the C best continuations of logits[N,W,V] (FP32 or
+    BF16) with beam scores[N,W] into cand_*[N,C] (score FP32, beam int32, token
+    int64; best first, ties to the lower beam * V + token), and the first W whose
+    token is not `eos` into next_*[N,W] (all three None to skip).  Entries with
+    done[n] != 0 (int32) are not read and keep their beams."""
+    if logits.dim() != 3 or cand_score.dim() != 2:
+        raise ValueError("expected logits [N,W,V] and cand_score [N,C]")
+    N, W, V = logits.shape
+    C = cand_score.shape[1]
+    f32, i32, i64 = torch.float32, torch.int32, torch.int64
+    wp, wn = _workspace(workspace, logits)
+    _check(_on(logits, stream, lib().beam_select,
+               _take("logits", logits, (N, W, V), f32, torch.bfloat16), _dtype_code(logits.dtype),
+               _take("scores", scores, (N, W), f32, like=logits),
+               _take("done", done, (N,), i32, like=logits),
+               _take("cand_score", cand_score, (N, C), f32, like=logits),
+               _take("cand_beam", cand_beam, (N, C), i32, like=logits),
+               _take("cand_token", cand_token, (N, C), i64, like=logits),
+               _take("next_score", next_score, (N, W), f32, like=logits),
+               _take("next_beam", next_beam, (N, W), i32, like=logits),
+               _take("next_token", next_token, (N, W), i64, like=logits),
+               wp, wn, N, W, V, C, int(eos), _status(status, logits)), "beam_select")
+    return cand_score, cand_beam, cand_token, next_score, next_beam, next_token
+
+
+def _state_geometry(t: torch.Tensor, entry_dim: int):
+    """(run_bytes, outer extents, outer strides) of a state seen as elements
+    [.., n, w, ..]: the dimensions that are contiguous below every other one form
+    the run, the others are merged where one steps over the next."""
+    es = t.element_size()
+    dims = sorted((t.stride(d) * es, t.shape[d]) for d in range(t.dim())
+                  if d not in (entry_dim, entry_dim + 1) and t.shape[d] != 1)
+    run = es
+    while dims and dims[0][0] == run:
+        run *= dims.pop(0)[1]
+    merged = []
+    for st, n in dims:
+        if merged and st == merged[-1][0] * merged[-1][1]:
+            merged[-1] = (merged[-1][0], merged[-1][1] * n)
+        else:
+            merged.append((st, n))
+    if len(merged) > 3:
+        raise ValueError("a state may have at most three strided dimensions beside its beams")
+    return run, [n for _, n in merged], [st for st, _ in merged]
+
+
+def beam_reorder(states, parents: torch.Tensor, entry_dim: int = 0,
+                 status: Optional[torch.Tensor] = None, stream=None):
+    """Each state (one tensor or a list, all of one shape and strides, any dtype) is
+    put in the order of its beams' parents, in place: state[.., n, w, ..] becomes the
+    old state[.., n, parents[n, w], ..], with n in dimension entry_dim and w in the
+    next.  parents: [N, W] int32, as beam_select's next_beam.  Strided views (the
+    filled part of a cache) are taken as they are."""
+    states = [states] if isinstance(states, torch.Tensor) else list(states)
+    if parents.dim() != 2 or not states:
+        raise ValueError("expected parents [N,W] and at least one state")
+    N, W = parents.shape
+    first = states[0]
+    if not 0 <= entry_dim <= first.dim() - 2 or tuple(first.shape[entry_dim:entry_dim + 2]) != (N, W):
+        raise ValueError(f"dimensions {entry_dim} and {entry_dim + 1} of a state must be {(N, W)}")
+    for t in states:
+        if t.shape != first.shape or t.stride() != first.stride() or t.dtype != first.dtype:
+            raise ValueError("the states of one call must have one shape, dtype and strides")
+        if t.device != parents.device:
+            raise ValueError(f"a state is on {t.device}, parents on {parents.device}")
+    pp = _take("parents", parents, (N, W), torch.int32)
+    sp = _status(status, parents)
+    if first.numel() == 0:
+        return states
+    run, outer, strides = _state_geometry(first, entry_dim)
+    es, k = first.element_size(), len(outer)
+    I64 = ctypes.c_int64
+    for i in range(0, len(states), 128):
+        part = states[i:i + 128]
+        ptrs = (ctypes.c_void_p * len(part))(*[t.data_ptr() for t in part])
+        _check(_on(parents, stream, lib().beam_reorder, ptrs, len(part), pp, N, W,
+                   first.stride(entry_dim) * es, first.stride(entry_dim + 1) * es, run,
+                   (I64 * k)(*outer), (I64 * k)(*strides), k, sp), "beam_reorder")
+    return states
