@@ -73,6 +73,8 @@ typedef enum { LMH_F32 = 0, LMH_BF16 = 1, LMH_F16 = 2 } lmh_dtype_t;
 #define LMH_DEV_BAD_LOGIT 0x4    /* beam_select met a logit that is NaN or not
                                     below 1e38, or a score of NaN or +inf; each
                                     was taken as -inf                       */
+#define LMH_DEV_BAD_ADAPTER 0x8  /* an adapter id neither -1 nor in [0, N); the
+                                    token was treated as having none        */
 #define LMH_DEV_BAD_PARENT 0x10  /* beam_reorder met a parent outside [0, W);
                                     that beam's state was left as it was    */
 
@@ -259,6 +261,62 @@ LMH_API lmh_status_t lmhead_bwd_dw(const void *dlogits, const void *X, void *dW,
 LMH_API lmh_status_t lmhead_bwd_dw_acc(const void *dlogits, const void *X, float *dW, int64_t M,
                                        int64_t K, int64_t V, int32_t *status, lmh_stream_t stream);
 
+/* The LM head with low-rank adapters, one per token (no counterpart on the
+ * pages): the tokens of many requests share W, and each has its own adapter
+ * (A_a [R,K], B_a [V,R]) beside it, or none.
+ *   u[i,:]      = scale[a] X[i,:] . A_a^T                       a = adapter[i]
+ *   logits[i,:] = X[i,:] . W^T + u[i,:] . B_a^T
+ *   A [N,R,K] BF16, B [N,V,R] BF16, scale [N] FP32, of N adapters of rank R
+ *   (adapters of lower rank padded with zeros).   adapter [M] int32: -1 for a
+ *   token without one; any other value outside [0,N) sets LMH_DEV_BAD_ADAPTER
+ *   and counts as -1.
+ *   u       [M,R] FP32, written (0 for a token without adapter); the backward
+ *           calls take it.   logits as lmhead_fwd.
+ *   One kernel forms both products in the same sums, FP32 rounded to nearest
+ *   every 512 terms of K, so the base part is as lmhead_fwd's but with a smaller
+ *   error and not bitwise equal to it.  u enters the second product as two BF16
+ *   parts (2^-18 of u).  An adapter's values reach the tokens that use it and no
+ *   others, infinities and NaN included.  Any order of the tokens; those of one
+ *   adapter next to each other cost least (each 256-token tile reads the
+ *   adapters that occur in it).
+ *   workspace: device scratch of lmhead_lora_workspace_bytes(M, K, V, R, N)
+ *   bytes, 256-byte aligned; its contents do not matter before or after.
+ *   Requirements: K % 8 == 0, R % 8 == 0, R <= 256, N <= 65535, M <= 4194240;
+ *   X, W, A, B 16-byte aligned; logits aligned to its element.  Deterministic. */
+LMH_API lmh_status_t lmhead_fwd_lora(const void *X, const void *W, const void *A, const void *B,
+                                     const float *scale, const int32_t *adapter, float *u,
+                                     void *logits, int32_t out_dtype, void *workspace,
+                                     int64_t workspace_bytes, int64_t M, int64_t K, int64_t V,
+                                     int64_t R, int64_t N, int32_t *status, lmh_stream_t stream);
+
+/* Scratch bytes each of the three adapter calls needs at most.  -1 for sizes out
+ * of range. */
+LMH_API int64_t lmhead_lora_workspace_bytes(int64_t M, int64_t K, int64_t V, int64_t R, int64_t N);
+
+/* The input gradient of lmhead_fwd_lora:
+ *   g[i,:]  = scale[a] dlogits[i,:] . B_a          (written, [M,R] FP32)
+ *   dX[i,:] = dlogits[i,:] . W + g[i,:] . A_a      (FP32 or BF16)
+ * summed as in lmhead_fwd_lora.  Requirements as there, and V % 8 == 0,
+ * dlogits and dX 16-byte aligned.  Deterministic. */
+LMH_API lmh_status_t lmhead_bwd_dx_lora(const void *dlogits, const void *W, const void *A,
+                                        const void *B, const float *scale, const int32_t *adapter,
+                                        float *g, void *dX, int32_t out_dtype, void *workspace,
+                                        int64_t workspace_bytes, int64_t M, int64_t K, int64_t V,
+                                        int64_t R, int64_t N, int32_t *status, lmh_stream_t stream);
+
+/* The adapters' gradients, from the u of lmhead_fwd_lora and the g of
+ * lmhead_bwd_dx_lora:
+ *   dA_a = sum over its tokens of g[i,:]^T . X[i,:]        [N,R,K] FP32
+ *   dB_a = sum over its tokens of dlogits[i,:]^T . u[i,:]  [N,V,R] FP32
+ * zeros for an adapter without tokens.  u and g enter as three BF16 parts
+ * (FP32's 24 bits).  Requirements as lmhead_bwd_dx_lora; dA and dB 16-byte
+ * aligned.  Deterministic. */
+LMH_API lmh_status_t lmhead_bwd_lora(const void *dlogits, const void *X, const float *u,
+                                     const float *g, const int32_t *adapter, float *dA, float *dB,
+                                     void *workspace, int64_t workspace_bytes, int64_t M, int64_t K,
+                                     int64_t V, int64_t R, int64_t N, int32_t *status,
+                                     lmh_stream_t stream);
+
 /* One step of beam search over the logits: of all continuations of the W beams
  * of each of N batch entries, the C best, and the W beams that go on (no
  * counterpart on the pages; the log-softmax is that of ce_fwd).
@@ -277,7 +335,7 @@ LMH_API lmh_status_t lmhead_bwd_dw_acc(const void *dlogits, const void *X, float
  *   next_score / next_beam / next_token [N,W], all three or none (NULL): the
  *           first W candidates whose token is not eos (eos = -1: none is), in
  *           order.  Places that no candidate fills get (-inf, w, eos, or 0 for
- *           eos = -1), w being the place itself.
+ *           eos = -1), w being the place itself.  next_score may be scores.
  *   workspace: device scratch of beam_select_workspace_bytes(N, W, V, C) bytes,
  *           16-byte aligned; its contents do not matter before or after.
  *   Limits: W <= 64, C <= 128, and with next_*: C >= 2 W (C >= W for eos = -1),

@@ -357,8 +357,9 @@ __device__ __forceinline__ bool ahead(const BeamKey &a, const BeamKey &b)
 
 // One CTA per batch entry.  The candidates of all chunks of all beams are read
 // twice from L2 (a few KB): once for a threshold, once for those that reach it.
+// o.next_score may be `scores`: an entry's are read before any is written.
 __global__ void __launch_bounds__(kBeamThreads)
-    beam_merge_kernel(const float *__restrict__ scores, const int32_t *__restrict__ done,
+    beam_merge_kernel(const float *scores, const int32_t *__restrict__ done,
                       const BeamPartial *part, const BeamCand *cand, BeamOut o, int32_t W, int64_t V,
                       int32_t C, int32_t chunks, int64_t eos, int32_t *status)
 {

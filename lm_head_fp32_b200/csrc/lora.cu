@@ -1,0 +1,428 @@
+// lora.cu -- C ABI of the LM head with low-rank adapters (declared in
+// include/lmhead.h): argument validation, workspace layout, kernel selection
+// and launches of lora_kernels.cuh and lora_gemm.cuh.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cstdint>
+#include <cstring>
+
+#include "lmhead.h"
+#include "host.cuh"
+#include "lora_gemm.cuh"
+#include "lora_kernels.cuh"
+
+namespace {
+
+using namespace lmh::host;
+using lmh::GemmCfg;
+using lmh::GemmParams;
+using lmh::LoraParams;
+
+constexpr int64_t kMaxRank = 256;
+constexpr int64_t kMaxAdapters = 65535;              // a grid dimension
+constexpr int64_t kMaxTokens = 65535ll * lmh::kRowsTokens;  // likewise
+constexpr int64_t kRowsCtas = 592;  // row-kernel CTAs aimed at: four per SM
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
+
+// Token-tile width of the GEMMs: the smallest supported MMA N that covers M, up
+// to 256.
+int pick_bn(int64_t M, int least) { return M <= least ? least : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256; }
+
+// Ranges the columns of a row kernel are cut into: enough CTAs to fill the GPU,
+// and no more, since each range writes a partial result.
+struct RowRanges {
+    int64_t subs, ranges;
+};
+RowRanges row_ranges(int64_t M, int64_t Cdim, int64_t R)
+{
+    const int64_t nsub = ceil_div(Cdim, lmh::kRowsSub);
+    const int64_t base = ceil_div(M, lmh::kRowsTokens) * ceil_div(R, lmh::kRankBlock);
+    int64_t want = kRowsCtas / base;
+    want = want < 1 ? 1 : want > nsub ? nsub : want;
+    const int64_t subs = ceil_div(nsub, want);
+    return {subs, ceil_div(nsub, subs)};
+}
+
+int64_t rank_pad(int64_t R) { return (R + 15) / 16 * 16; }
+
+// Byte offsets in the workspace of lmhead_fwd_lora (Cdim = K) and
+// lmhead_bwd_dx_lora (Cdim = V).
+struct GemmSpace {
+    int64_t partial, ux, nslots, slot_id, slot_mask, bytes;
+    int64_t tiles, stages, max_slots, slot_stride;
+};
+GemmSpace gemm_space(int64_t M, int64_t Cdim, int64_t R, int64_t N, int bn)
+{
+    GemmSpace g;
+    g.tiles = ceil_div(M, bn);
+    g.stages = R <= 32 ? 1 : 2 * ceil_div(R, 64);
+    g.max_slots = N < bn ? N : bn;
+    g.slot_stride = (g.max_slots + 3) / 4 * 4;
+    g.partial = 0;
+    g.ux = align256(row_ranges(M, Cdim, R).ranges * M * rank_pad(R) * 4);
+    g.nslots = g.ux + align256(g.tiles * g.stages * bn * 128);
+    g.slot_id = g.nslots + align256(g.tiles * 4);
+    g.slot_mask = g.slot_id + align256(g.tiles * g.slot_stride * 4);
+    g.bytes = g.slot_mask + align256(g.tiles * g.max_slots * lmh::kSlotMaskWords * 4);
+    return g;
+}
+
+// Byte offsets in the workspace of lmhead_bwd_lora.
+struct GradSpace {
+    int64_t start, order, u_parts, g_parts, bytes;
+};
+GradSpace grad_space(int64_t M, int64_t R, int64_t N)
+{
+    GradSpace g;
+    g.start = 0;
+    g.order = align256((N + 1) * 4);
+    g.u_parts = g.order + align256(M * 4);
+    const int64_t parts = align256(M * 3 * rank_pad(R) * 2);
+    g.g_parts = g.u_parts + parts;
+    g.bytes = g.g_parts + parts;
+    return g;
+}
+
+bool lora_dims_ok(int64_t M, int64_t K, int64_t V, int64_t R, int64_t N)
+{
+    return dims_ok(M, K, V) && M <= kMaxTokens && R >= 1 && R <= kMaxRank && N >= 1 && N <= kMaxAdapters;
+}
+
+// 3-D BF16 tensor [outer][mid][inner] (contiguous), 128-byte swizzled boxes of
+// 64 x box_mid; out-of-range elements read as zero.
+bool make_map3(CUtensorMap *map, const void *base, uint64_t inner, uint64_t mid, uint64_t outer, uint32_t box_mid)
+{
+    EncodeTiledFn enc = encode_fn();
+    if (!enc)
+        return false;
+    const cuuint64_t dims[3] = {inner, mid, outer};
+    const cuuint64_t strides[2] = {inner * 2, inner * mid * 2};
+    const cuuint32_t box[3] = {64, box_mid, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Shared memory above 48 KB, once per kernel and device.
+template <typename K>
+lmh_status_t allow_smem(K kern, int bytes, std::atomic<uint64_t> &set)
+{
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const uint64_t bit = 1ull << (dev & 63);
+    if (set.load() & bit)
+        return LMH_OK;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess ||
+        cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100) != cudaSuccess)
+        return LMH_ERR_CUDA;
+    set.fetch_or(bit);
+    return LMH_OK;
+}
+
+struct AdapterOperands {
+    const void *base;         // [N][mid][inner] BF16
+    uint64_t inner, mid, N;
+    const void *ux;           // the split u of every token tile
+    uint64_t ux_rows;
+};
+
+template <int BN, bool A_MN, typename OutT, bool TMA_STORE, bool PAIR, int RES>
+lmh_status_t launch_impl(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &tc, const CUtensorMap &ts,
+                         const CUtensorMap &tu, GemmParams p, const LoraParams &q, cudaStream_t stream)
+{
+    constexpr int EW = lmh::lora_epi_warps(BN);
+    using C = GemmCfg<BN, A_MN, false, PAIR, RES, EW>;
+    auto kern = lmh::lora_gemm_kernel<BN, A_MN, OutT, TMA_STORE, PAIR, RES, EW>;
+    static std::atomic<uint64_t> set{0};
+    if (const lmh_status_t r = allow_smem(kern, C::SMEM_BYTES, set); r != LMH_OK)
+        return r;
+    p.wait_limit_ns = lmh::kWaitLimitNs;
+    p.num_m_tiles = static_cast<int32_t>(ceil_div(p.Mdim, C::TILE_M));
+    p.num_n_tiles = static_cast<int32_t>(ceil_div(p.Ndim, BN));
+    const int64_t tiles = static_cast<int64_t>(p.num_m_tiles) * p.num_n_tiles;
+    if (tiles > kMaxDim)
+        return LMH_ERR_INVALID_ARG;
+    const int64_t units = RES == 1 ? num_sms() / C::CTAS : tiles;
+    const int grid = static_cast<int>((tiles < units ? tiles : units) * C::CTAS);
+    return launch_ex(kern, dim3(grid), dim3(C::THREADS), C::SMEM_BYTES, stream, PAIR ? 2u : 1u, ta, tb, tc, ts,
+                     tu, p, q);
+}
+
+// A: the shared weights [outer][inner], MN-major (dX) or K-major; B: [Ndim][Kdim].
+template <int BN, bool A_MN, typename OutT, bool PAIR, int RES = 1>
+lmh_status_t launch_lora(const void *a, uint64_t a_inner, uint64_t a_outer, const void *b, const AdapterOperands &ad,
+                         const GemmParams &p, const LoraParams &q, cudaStream_t stream)
+{
+    using C = GemmCfg<BN, A_MN, false, PAIR, RES, lmh::lora_epi_warps(BN)>;
+    CUtensorMap ta, tb, tc, ts, tu;
+    if (!make_map(&ta, a, a_inner, a_outer, 64, A_MN ? lmh::kBlockK : lmh::kBlockM) ||
+        !make_map(&tb, b, static_cast<uint64_t>(p.Kdim), static_cast<uint64_t>(p.Ndim), lmh::kBlockK, C::BN_CTA) ||
+        !make_map3(&ts, ad.base, ad.inner, ad.mid, ad.N, A_MN ? lmh::kBlockK : lmh::kBlockM) ||
+        !make_map(&tu, ad.ux, 64, ad.ux_rows, 64, C::BN_CTA))
+        return LMH_ERR_CUDA;
+    if (make_out_map(&tc, p.out, sizeof(OutT) == 2, static_cast<uint64_t>(p.Mdim), static_cast<uint64_t>(p.Ndim),
+                     static_cast<uint64_t>(p.ldo), C::EPI_CHUNK))
+        return launch_impl<BN, A_MN, OutT, true, PAIR, RES>(ta, tb, tc, ts, tu, p, q, stream);
+    if constexpr (A_MN)
+        return LMH_ERR_MISALIGNED;  // dX rows are multiples of 16 bytes and its base is checked
+    std::memset(&tc, 0, sizeof tc);
+    return launch_impl<BN, A_MN, OutT, A_MN, PAIR, RES>(ta, tb, tc, ts, tu, p, q, stream);
+}
+
+template <bool P_MN, int NT>
+lmh_status_t launch_rows(const void *Y, const void *P, const int32_t *adapter, float *partial, int64_t M, int64_t Cdim,
+                         int64_t R, int64_t N, const RowRanges &rr, cudaStream_t s)
+{
+    using G = lmh::RowsCfg<P_MN, NT>;
+    auto kern = lmh::lora_rows_kernel<P_MN, NT>;
+    static std::atomic<uint64_t> set{0};
+    if (const lmh_status_t r = allow_smem(kern, G::SMEM, set); r != LMH_OK)
+        return r;
+    return launch_ex(kern,
+                     dim3(static_cast<unsigned>(rr.ranges), static_cast<unsigned>(ceil_div(M, lmh::kRowsTokens)),
+                          static_cast<unsigned>(ceil_div(R, lmh::kRankBlock))),
+                     dim3(lmh::kRowsThreads), G::SMEM, s, 1u, static_cast<const __nv_bfloat16 *>(Y),
+                     static_cast<const __nv_bfloat16 *>(P), adapter, partial, M, Cdim, static_cast<int32_t>(R),
+                     static_cast<int32_t>(rank_pad(R)), static_cast<int32_t>(N), static_cast<int32_t>(rr.subs));
+}
+
+// t = s Y P_a over Cdim, its split and the slots of the token tiles, into the
+// workspace and t_out.
+template <bool P_MN>
+lmh_status_t run_rows(const void *Y, const void *P, const float *scale, const int32_t *adapter, float *t_out,
+                      uint8_t *ws, const GemmSpace &g, int bn, int64_t M, int64_t Cdim, int64_t R, int64_t N,
+                      int32_t *status, cudaStream_t s)
+{
+    const RowRanges rr = row_ranges(M, Cdim, R);
+    float *partial = reinterpret_cast<float *>(ws + g.partial);
+    const int64_t nt = R > 48 ? 4 : rank_pad(R) / 16;
+    lmh_status_t r;
+    switch (nt) {
+    case 1: r = launch_rows<P_MN, 1>(Y, P, adapter, partial, M, Cdim, R, N, rr, s); break;
+    case 2: r = launch_rows<P_MN, 2>(Y, P, adapter, partial, M, Cdim, R, N, rr, s); break;
+    case 3: r = launch_rows<P_MN, 3>(Y, P, adapter, partial, M, Cdim, R, N, rr, s); break;
+    default: r = launch_rows<P_MN, 4>(Y, P, adapter, partial, M, Cdim, R, N, rr, s); break;
+    }
+    if (r != LMH_OK)
+        return r;
+    return launch_ex(lmh::lora_expand_kernel,
+                     dim3(static_cast<unsigned>(g.tiles), static_cast<unsigned>(ceil_div(bn, lmh::kExpandTokens))),
+                     dim3(256), lmh::kExpandTokens * rank_pad(R) * sizeof(float), s, 1u,
+                     static_cast<const float *>(partial), static_cast<int32_t>(rr.ranges), adapter, scale, t_out,
+                     reinterpret_cast<__nv_bfloat16 *>(ws + g.ux), reinterpret_cast<int32_t *>(ws + g.nslots),
+                     reinterpret_cast<int32_t *>(ws + g.slot_id), reinterpret_cast<uint32_t *>(ws + g.slot_mask),
+                     static_cast<int32_t>(bn), static_cast<int32_t>(g.slot_stride), static_cast<int32_t>(g.max_slots),
+                     static_cast<int32_t>(g.stages), M, static_cast<int32_t>(R), static_cast<int32_t>(rank_pad(R)),
+                     static_cast<int32_t>(N), status);
+}
+
+LoraParams lora_params(uint8_t *ws, const GemmSpace &g, int64_t R)
+{
+    LoraParams q{};
+    q.nslots = reinterpret_cast<const int32_t *>(ws + g.nslots);
+    q.slot_id = reinterpret_cast<const int32_t *>(ws + g.slot_id);
+    q.slot_mask = reinterpret_cast<const uint32_t *>(ws + g.slot_mask);
+    q.slot_stride = static_cast<int32_t>(g.slot_stride);
+    q.max_slots = static_cast<int32_t>(g.max_slots);
+    q.stages_per_slot = static_cast<int32_t>(g.stages);
+    q.rank = static_cast<int32_t>(R);
+    return q;
+}
+
+template <int NT, bool OUT_RC>
+lmh_status_t launch_cols(const void *Y, const __nv_bfloat16 *parts, const int32_t *start, const int32_t *order,
+                         float *out, int64_t Cdim, int64_t R, int64_t N, cudaStream_t s)
+{
+    using G = lmh::ColsCfg<NT>;
+    auto kern = lmh::lora_cols_kernel<NT, OUT_RC>;
+    static std::atomic<uint64_t> set{0};
+    if (const lmh_status_t r = allow_smem(kern, G::SMEM, set); r != LMH_OK)
+        return r;
+    return launch_ex(kern,
+                     dim3(static_cast<unsigned>(ceil_div(Cdim, lmh::kColsTile)), static_cast<unsigned>(N),
+                          static_cast<unsigned>(ceil_div(R, lmh::kRankBlock))),
+                     dim3(lmh::kColsThreads), G::SMEM, s, 1u, static_cast<const __nv_bfloat16 *>(Y), parts, start,
+                     order, out, Cdim, static_cast<int32_t>(R), static_cast<int32_t>(rank_pad(R)));
+}
+
+template <bool OUT_RC>
+lmh_status_t run_cols(const void *Y, const __nv_bfloat16 *parts, const int32_t *start, const int32_t *order,
+                      float *out, int64_t Cdim, int64_t R, int64_t N, cudaStream_t s)
+{
+    switch (R > 48 ? 4 : rank_pad(R) / 16) {
+    case 1: return launch_cols<1, OUT_RC>(Y, parts, start, order, out, Cdim, R, N, s);
+    case 2: return launch_cols<2, OUT_RC>(Y, parts, start, order, out, Cdim, R, N, s);
+    case 3: return launch_cols<3, OUT_RC>(Y, parts, start, order, out, Cdim, R, N, s);
+    default: return launch_cols<4, OUT_RC>(Y, parts, start, order, out, Cdim, R, N, s);
+    }
+}
+
+template <typename OutT>
+lmh_status_t dispatch_fwd(int bn, bool pair, const void *W, uint64_t K, uint64_t V, const void *X,
+                          const AdapterOperands &ad, const GemmParams &p, const LoraParams &q, cudaStream_t s)
+{
+    switch (bn) {
+    // one token tile: bound by W, two CTAs resident per SM
+    case 16: return launch_lora<16, false, OutT, false, 2>(W, K, V, X, ad, p, q, s);
+    case 32: return launch_lora<32, false, OutT, false, 2>(W, K, V, X, ad, p, q, s);
+    case 64: return launch_lora<64, false, OutT, false, 2>(W, K, V, X, ad, p, q, s);
+    case 128: return launch_lora<128, false, OutT, false, 2>(W, K, V, X, ad, p, q, s);
+    default:
+        return pair ? launch_lora<256, false, OutT, true>(W, K, V, X, ad, p, q, s)
+                    : launch_lora<256, false, OutT, false>(W, K, V, X, ad, p, q, s);
+    }
+}
+
+template <typename OutT>
+lmh_status_t dispatch_dx(int bn, bool pair, const void *W, uint64_t K, uint64_t V, const void *dl,
+                         const AdapterOperands &ad, const GemmParams &p, const LoraParams &q, cudaStream_t s)
+{
+    switch (bn) {
+    case 64: return launch_lora<64, true, OutT, false>(W, K, V, dl, ad, p, q, s);
+    case 128: return launch_lora<128, true, OutT, false>(W, K, V, dl, ad, p, q, s);
+    default:
+        return pair ? launch_lora<256, true, OutT, true>(W, K, V, dl, ad, p, q, s)
+                    : launch_lora<256, true, OutT, false>(W, K, V, dl, ad, p, q, s);
+    }
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t lmhead_lora_workspace_bytes(int64_t M, int64_t K, int64_t V, int64_t R, int64_t N)
+{
+    if (!lora_dims_ok(M, K, V, R, N))
+        return -1;
+    const int64_t f = gemm_space(M, K, R, N, pick_bn(M, 16)).bytes;
+    const int64_t d = gemm_space(M, V, R, N, pick_bn(M, 64)).bytes;
+    const int64_t w = grad_space(M, R, N).bytes;
+    const int64_t fd = f > d ? f : d;
+    return fd > w ? fd : w;
+}
+
+lmh_status_t lmhead_fwd_lora(const void *X, const void *W, const void *A, const void *B, const float *scale,
+                             const int32_t *adapter, float *u, void *logits, int32_t out_dtype, void *workspace,
+                             int64_t workspace_bytes, int64_t M, int64_t K, int64_t V, int64_t R, int64_t N,
+                             int32_t *status, lmh_stream_t stream)
+{
+    if (!X || !W || !A || !B || !scale || !adapter || !u || !logits || !workspace || !lora_dims_ok(M, K, V, R, N))
+        return LMH_ERR_INVALID_ARG;
+    if (bad_dtype(out_dtype))
+        return LMH_ERR_UNSUPPORTED;
+    if (K % 8 || R % 8 || !aligned(X, 16) || !aligned(W, 16) || !aligned(A, 16) || !aligned(B, 16) ||
+        !aligned(scale, 4) || !aligned(adapter, 4) || !aligned(u, 4) || !aligned(workspace, 256) ||
+        !aligned(logits, out_dtype == LMH_F32 ? 4 : 2))
+        return LMH_ERR_MISALIGNED;
+    const int bn = pick_bn(M, 16);
+    const GemmSpace g = gemm_space(M, K, R, N, bn);
+    if (workspace_bytes < g.bytes)
+        return LMH_ERR_INVALID_ARG;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    const lmh_status_t r = run_rows<false>(X, A, scale, adapter, u, ws, g, bn, M, K, R, N, status, s);
+    if (r != LMH_OK)
+        return r;
+    GemmParams p{};
+    p.out = logits;
+    p.ldo = V;
+    p.Mdim = static_cast<int32_t>(V);
+    p.Ndim = static_cast<int32_t>(M);
+    p.Kdim = static_cast<int32_t>(K);
+    p.m_fastest = 0;             // consecutive tiles share one W panel
+    p.l2_a = M <= bn ? 1 : 0;    // as lmhead_fwd: streamed once with one token tile
+    p.l2_b = 2;
+    p.l2_out = 1;
+    p.status = status;
+    const AdapterOperands ad{B, static_cast<uint64_t>(R), static_cast<uint64_t>(V), static_cast<uint64_t>(N),
+                             ws + g.ux, static_cast<uint64_t>(g.tiles * g.stages * bn)};
+    const LoraParams q = lora_params(ws, g, R);
+    const bool pair = V >= 256;
+    const uint64_t k = static_cast<uint64_t>(K), v = static_cast<uint64_t>(V);
+    return out_dtype == LMH_F32 ? dispatch_fwd<float>(bn, pair, W, k, v, X, ad, p, q, s)
+                                : dispatch_fwd<__nv_bfloat16>(bn, pair, W, k, v, X, ad, p, q, s);
+}
+
+lmh_status_t lmhead_bwd_dx_lora(const void *dlogits, const void *W, const void *A, const void *B, const float *scale,
+                                const int32_t *adapter, float *g_out, void *dX, int32_t out_dtype, void *workspace,
+                                int64_t workspace_bytes, int64_t M, int64_t K, int64_t V, int64_t R, int64_t N,
+                                int32_t *status, lmh_stream_t stream)
+{
+    if (!dlogits || !W || !A || !B || !scale || !adapter || !g_out || !dX || !workspace ||
+        !lora_dims_ok(M, K, V, R, N))
+        return LMH_ERR_INVALID_ARG;
+    if (bad_dtype(out_dtype))
+        return LMH_ERR_UNSUPPORTED;
+    if (K % 8 || V % 8 || R % 8 || !aligned(dlogits, 16) || !aligned(W, 16) || !aligned(A, 16) || !aligned(B, 16) ||
+        !aligned(scale, 4) || !aligned(adapter, 4) || !aligned(g_out, 4) || !aligned(dX, 16) ||
+        !aligned(workspace, 256))
+        return LMH_ERR_MISALIGNED;
+    const int bn = pick_bn(M, 64);
+    const GemmSpace g = gemm_space(M, V, R, N, bn);
+    if (workspace_bytes < g.bytes)
+        return LMH_ERR_INVALID_ARG;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    const lmh_status_t r = run_rows<true>(dlogits, B, scale, adapter, g_out, ws, g, bn, M, V, R, N, status, s);
+    if (r != LMH_OK)
+        return r;
+    GemmParams p{};
+    p.out = dX;
+    p.ldo = K;
+    p.Mdim = static_cast<int32_t>(K);
+    p.Ndim = static_cast<int32_t>(M);
+    p.Kdim = static_cast<int32_t>(V);
+    p.m_fastest = 1;
+    p.l2_a = 2;  // as lmhead_bwd_dx
+    p.l2_b = 2;
+    p.status = status;
+    const AdapterOperands ad{A, static_cast<uint64_t>(K), static_cast<uint64_t>(R), static_cast<uint64_t>(N),
+                             ws + g.ux, static_cast<uint64_t>(g.tiles * g.stages * bn)};
+    const LoraParams q = lora_params(ws, g, R);
+    const bool pair = K >= 256;
+    const uint64_t k = static_cast<uint64_t>(K), v = static_cast<uint64_t>(V);
+    return out_dtype == LMH_F32 ? dispatch_dx<float>(bn, pair, W, k, v, dlogits, ad, p, q, s)
+                                : dispatch_dx<__nv_bfloat16>(bn, pair, W, k, v, dlogits, ad, p, q, s);
+}
+
+lmh_status_t lmhead_bwd_lora(const void *dlogits, const void *X, const float *u, const float *g_in,
+                             const int32_t *adapter, float *dA, float *dB, void *workspace, int64_t workspace_bytes,
+                             int64_t M, int64_t K, int64_t V, int64_t R, int64_t N, int32_t *status,
+                             lmh_stream_t stream)
+{
+    if (!dlogits || !X || !u || !g_in || !adapter || !dA || !dB || !workspace || !lora_dims_ok(M, K, V, R, N))
+        return LMH_ERR_INVALID_ARG;
+    if (K % 8 || V % 8 || R % 8 || !aligned(dlogits, 16) || !aligned(X, 16) || !aligned(u, 4) || !aligned(g_in, 4) ||
+        !aligned(adapter, 4) || !aligned(dA, 16) || !aligned(dB, 16) || !aligned(workspace, 256))
+        return LMH_ERR_MISALIGNED;
+    const GradSpace g = grad_space(M, R, N);
+    if (workspace_bytes < g.bytes)
+        return LMH_ERR_INVALID_ARG;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    int32_t *start = reinterpret_cast<int32_t *>(ws + g.start), *order = reinterpret_cast<int32_t *>(ws + g.order);
+    __nv_bfloat16 *up = reinterpret_cast<__nv_bfloat16 *>(ws + g.u_parts);
+    __nv_bfloat16 *gp = reinterpret_cast<__nv_bfloat16 *>(ws + g.g_parts);
+    const int32_t r32 = static_cast<int32_t>(R), pad = static_cast<int32_t>(rank_pad(R)), n32 = static_cast<int32_t>(N);
+    lmh_status_t r = launch_ex(lmh::lora_group_kernel, dim3(static_cast<unsigned>(N)), dim3(1024), 0, s, 1u, adapter,
+                               start, order, M, n32, status);
+    const int64_t blocks = ceil_div(M * pad, 256);
+    const dim3 grid(static_cast<unsigned>(blocks < 1184 ? blocks : 1184));
+    for (int i = 0; i < 2 && r == LMH_OK; ++i)
+        r = launch_ex(lmh::lora_split_kernel, grid, dim3(256), 0, s, 1u, i ? g_in : u,
+                      static_cast<const int32_t *>(start), static_cast<const int32_t *>(order), i ? gp : up, n32, r32,
+                      pad);
+    if (r == LMH_OK)
+        r = run_cols<true>(X, gp, start, order, dA, K, R, N, s);
+    if (r == LMH_OK)
+        r = run_cols<false>(dlogits, up, start, order, dB, V, R, N, s);
+    return r;
+}
+
+}  // extern "C"

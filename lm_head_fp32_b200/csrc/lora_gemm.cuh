@@ -1,0 +1,487 @@
+// lora_gemm.cuh -- the LM head's products with low-rank adapters beside the
+// shared weights, as one tcgen05 kernel:
+//
+//   logits[i, v] = sum_k X[i,k] W[v,k]  + sum_r u[i,r] B_a[v,r]      (A = W,   K-major)
+//   dX[i, k]     = sum_v dl[i,v] W[v,k] + sum_r g[i,r] A_a[r,k]      (A = W^T, MN-major)
+//
+// with a = the token's adapter.  The adapters' term goes into the same sums:
+// after the k-blocks of the shared product, each output tile takes one more
+// k-block (two per 64 ranks above 32) per adapter that occurs among its tokens
+// ("slot"), each into a tensor-memory accumulator of its own, of which the
+// epilogue adds only the columns of that adapter's tokens.  So the delta never
+// travels to memory and back: separate from the product it would read and
+// write all logits once more (4.2 GB at 4096 x 128256), and an adapter that
+// holds infinities or NaN reaches no other request's tokens.  u is FP32, the
+// tensor cores take BF16: it is split into u_hi + u_lo (2^-18 relative), B_a
+// entering twice.
+//
+// The sum over the reduction is kept in FP32 as FP32 should be: the tensor
+// cores' own accumulation loses about 2^-24 of the running sum at each MMA,
+// always towards zero, which grows with the length (4e-6 relative at K = 4096,
+// 1e-4 at K = 128256).  Here a tensor-memory accumulator takes kPromote k-blocks
+// and the epilogue warps add it, rounded to nearest, to sums they hold in
+// registers, while the MMAs fill the other accumulator.
+//
+// Roles, ring, tile order, TMA epilogue and the unwinding after a timeout are
+// those of gemm_tc.cuh.
+#pragma once
+#include "gemm_tc.cuh"
+
+namespace lmh {
+
+constexpr int kPromote = 8;  // k-blocks (512 of the reduction) per tensor-memory accumulation
+
+constexpr int kSlotMaskWords = 8;  // one bit per token of a tile of up to 256
+
+struct LoraParams {
+    const int32_t *nslots;     // per token tile: adapters among its tokens
+    const int32_t *slot_id;    // [token tile][slot_stride]: their ids
+    const uint32_t *slot_mask; // [token tile][max_slots][kSlotMaskWords]: their tokens
+    int32_t slot_stride;       // multiple of 4
+    int32_t max_slots;
+    int32_t stages_per_slot;   // ring stages of one slot: 1 up to 32 ranks, then 2 per 64
+    int32_t rank;
+};
+
+// Epilogue warps: sums of a whole tile stay in their registers, 128 per thread
+// with a 256-wide tile and eight warps, at most 64 with the narrower ones.
+constexpr int lora_epi_warps(int bn) { return bn >= 128 ? 8 : 4; }
+
+template <int BN, bool A_MN, typename OutT, bool TMA_STORE, bool PAIR, int RES = 1, int EW = lora_epi_warps(BN)>
+__global__ void __launch_bounds__(64 + 32 * EW, RES)
+    lora_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                     const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmS,
+                     const __grid_constant__ CUtensorMap tmU, const GemmParams p, const LoraParams q)
+{
+    using C = GemmCfg<BN, A_MN, false, PAIR, RES, EW>;
+    constexpr int S = C::STAGES;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t *tiles = smem;
+    uint8_t *epi_smem = smem + S * C::STAGE_BYTES;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(epi_smem + C::EPI_BYTES);
+    uint64_t *full = bars;
+    uint64_t *empty = bars + S;
+    uint64_t *acc_full = bars + 2 * S;
+    uint64_t *acc_empty = bars + 2 * S + 2;
+    uint64_t *drain = bars + 2 * S + 4;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * S + 5);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    volatile uint32_t *issued_sh = tmem_slot + 2;  // k-blocks whose copies this CTA issued
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
+    const bool leader = rank == 0;
+    const int unit = PAIR ? static_cast<int>(blockIdx.x >> 1) : static_cast<int>(blockIdx.x);
+    const int num_units = PAIR ? static_cast<int>(gridDim.x >> 1) : static_cast<int>(gridDim.x);
+    const int num_tiles = p.num_m_tiles * p.num_n_tiles;
+    const int num_kb = (p.Kdim + kBlockK - 1) / kBlockK;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(&acc_full[a], 1);
+            mbar_init(&acc_empty[a], EW * C::CTAS);  // one arrival per epilogue warp
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        *issued_sh = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tmA);
+        tma_prefetch_desc(&tmB);
+        tma_prefetch_desc(&tmS);
+        tma_prefetch_desc(&tmU);
+        if (TMA_STORE)
+            tma_prefetch_desc(&tmC);
+    }
+    if (warp == 1) {
+        if (PAIR)
+            tmem_alloc_pair(tmem_slot, C::TMEM_COLS);
+        else
+            tmem_alloc(tmem_slot, C::TMEM_COLS);
+    }
+    tc_fence_before();
+    if (PAIR)
+        cluster_sync();
+    else
+        __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    pdl_wait();
+    pdl_launch_dependents();
+
+    const uint64_t pol_a = policy_of(p.l2_a);
+    const uint64_t pol_b = policy_of(p.l2_b);
+    const uint64_t pol_n = policy_of(0);
+    // Arms the full barrier of ring slot `stage` (the leader's, which counts the
+    // bytes of both CTAs) and returns where this CTA's copies signal it.  Every
+    // stage, of the shared product or of a slot, has STAGE_BYTES per CTA.
+    auto arm = [&](uint32_t stage) -> uint32_t {
+        if (leader)
+            mbar_arrive_expect_tx(&full[stage], C::STAGE_BYTES * C::CTAS);
+        return PAIR ? mapa_shared(smem_u32(&full[stage]), 0) : 0u;
+    };
+    auto load2 = [&](const CUtensorMap *m, uint32_t stage, uint32_t fb, void *dst, int c0, int c1, uint64_t pol) {
+        if (PAIR)
+            tma_load_2d_pair(m, fb, dst, c0, c1, pol);
+        else
+            tma_load_2d(m, &full[stage], dst, c0, c1, pol);
+    };
+    auto load3 = [&](const CUtensorMap *m, uint32_t stage, uint32_t fb, void *dst, int c0, int c1, int c2) {
+        if (PAIR)
+            tma_load_3d_pair(m, fb, dst, c0, c1, c2, pol_n);
+        else
+            tma_load_3d(m, &full[stage], dst, c0, c1, c2, pol_n);
+    };
+    auto issue_kblock = [&](uint32_t stage, int m0, int nb0, int k0) {
+        uint8_t *sa = tiles + stage * C::STAGE_BYTES;
+        const uint32_t fb = arm(stage);
+        if (A_MN) {
+#pragma unroll
+            for (int j = 0; j < kBlockM / 64; ++j)
+                load2(&tmA, stage, fb, sa + j * 64 * kBlockK * 2, m0 + 64 * j, k0, pol_a);
+        } else {
+            load2(&tmA, stage, fb, sa, k0, m0, pol_a);
+        }
+        load2(&tmB, stage, fb, sa + C::A_BYTES, k0, nb0, pol_b);
+    };
+    // One ring stage of an adapter: its 64 ranks from r0 against the rows m0.. of
+    // the output (ranks past the last read as zero), and BN_CTA rows of the
+    // split u from row urow.
+    auto issue_slot = [&](uint32_t stage, int m0, int id, int r0, int urow) {
+        uint8_t *sa = tiles + stage * C::STAGE_BYTES;
+        const uint32_t fb = arm(stage);
+        if (A_MN) {
+#pragma unroll
+            for (int j = 0; j < kBlockM / 64; ++j)
+                load3(&tmS, stage, fb, sa + j * 64 * kBlockK * 2, m0 + 64 * j, r0, id);
+        } else {
+            load3(&tmS, stage, fb, sa, r0, m0, id);
+        }
+        load2(&tmU, stage, fb, sa + C::A_BYTES, 0, urow, pol_n);
+    };
+    const int sps = q.stages_per_slot;
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer
+        if (lane == 0) {
+            uint32_t stage = 0, phase = 0;
+            uint32_t issued = 0;
+            bool ok = true;
+            for (int t = unit; t < num_tiles && ok; t += num_units) {
+                int mt, nt;
+                tile_coords(t, p, mt, nt);
+                const int m0 = mt * C::TILE_M + static_cast<int>(rank) * kBlockM;
+                const int nb0 = nt * BN + static_cast<int>(rank) * C::BN_CTA;
+                const int ns = q.nslots[nt];
+                for (int kb = 0; kb < num_kb; ++kb) {
+                    if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.wait_limit_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    issue_kblock(stage, m0, nb0, kb * kBlockK);
+                    ++issued;
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+                const int4 *ids = reinterpret_cast<const int4 *>(q.slot_id + static_cast<int64_t>(nt) * q.slot_stride);
+                for (int s4 = 0; s4 < ns && ok; s4 += 4) {
+                    const int4 four = ids[s4 >> 2];
+#pragma unroll 1
+                    for (int s = s4; s < s4 + 4 && s < ns && ok; ++s) {
+                        const int id = (s & 3) == 0 ? four.x : (s & 3) == 1 ? four.y : (s & 3) == 2 ? four.z : four.w;
+#pragma unroll 1
+                        for (int j = 0; j < sps; ++j) {
+                            if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.wait_limit_ns)) {
+                                ok = false;
+                                break;
+                            }
+                            const int urow = (nt * sps + j) * BN + static_cast<int>(rank) * C::BN_CTA;
+                            issue_slot(stage, m0, id, (j >> 1) * 64, urow);
+                            ++issued;
+                            if (++stage == S) {
+                                stage = 0;
+                                phase ^= 1;
+                            }
+                        }
+                    }
+                }
+            }
+            *issued_sh = issued;
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer (pair: leader only)
+        if (lane == 0 && leader) {
+            uint32_t stage = 0, phase = 0;
+            uint32_t acc = 0, acc_phase = 0;
+            bool ok = true;
+            for (int t = unit; t < num_tiles && ok; t += num_units) {
+                int mt, nt;
+                tile_coords(t, p, mt, nt);
+                const int total = num_kb + q.nslots[nt] * sps;
+                int in_chunk = 0;  // k-blocks in the current accumulator
+                for (int kb = 0; kb < total; ++kb) {
+                    if (in_chunk == 0) {
+                        if (!mbar_wait(&acc_empty[acc], acc_phase ^ 1, abort_flag, p.wait_limit_ns)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                    }
+                    const uint32_t d_tmem = tmem_base + acc * BN;
+                    if (!mbar_wait(&full[stage], phase, abort_flag, p.wait_limit_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sa = smem_u32(tiles + stage * C::STAGE_BYTES);
+                    const uint32_t sb = sa + C::A_BYTES;
+                    auto mma = [&](int ka, int kbb, uint32_t accumulate) {
+                        // K-major: 32 bytes along the swizzled row per 16 of the
+                        // reduction.  MN-major: 16 rows of 128 bytes.
+                        const uint64_t da = A_MN ? smem_desc_sw128(sa + ka * 2048, 64 * kBlockK * 2, 1024)
+                                                 : smem_desc_sw128(sa + ka * 32, 16, 1024);
+                        const uint64_t db = smem_desc_sw128(sb + kbb * 32, 16, 1024);
+                        if (PAIR)
+                            mma_bf16_pair(d_tmem, da, db, C::IDESC, accumulate);
+                        else
+                            mma_bf16(d_tmem, da, db, C::IDESC, accumulate);
+                    };
+                    if (kb < num_kb) {
+#pragma unroll
+                        for (int k = 0; k < kBlockK / kUmmaK; ++k)
+                            mma(k, k, (in_chunk != 0 || k != 0) ? 1u : 0u);
+                    } else if (sps == 1) {
+                        // up to 32 ranks: columns 0..31 of u are its high parts,
+                        // 32..63 the low ones, against the same ranks of B_a
+                        mma(0, 0, 0u);
+                        mma(0, 2, 1u);
+                        if (q.rank > 16) {
+                            mma(1, 1, 1u);
+                            mma(1, 3, 1u);
+                        }
+                    } else {
+                        // 64 ranks: the high parts, then the low ones
+                        const int r0 = (in_chunk >> 1) * 64;
+                        const int steps = min(4, (q.rank - r0 + kUmmaK - 1) / kUmmaK);
+                        for (int k = 0; k < steps; ++k)
+                            mma(k, k, (in_chunk != 0 || k != 0) ? 1u : 0u);
+                    }
+                    if (PAIR)
+                        mma_commit_pair(&empty[stage], 0x3);
+                    else
+                        mma_commit(&empty[stage]);
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                    ++in_chunk;
+                    // an accumulator is full after kPromote k-blocks, at the end
+                    // of the shared product, and at the end of each slot
+                    if (kb < num_kb ? (in_chunk == kPromote || kb == num_kb - 1) : in_chunk == sps) {
+                        in_chunk = 0;
+                        if (PAIR)
+                            mma_commit_pair(&acc_full[acc], 0x3);
+                        else
+                            mma_commit(&acc_full[acc]);
+                        if (++acc == 2) {
+                            acc = 0;
+                            acc_phase ^= 1;
+                        }
+                    }
+                }
+            }
+            // wait until every MMA issued by this thread has completed
+            if (PAIR)
+                mma_commit_pair(drain, 0x1);
+            else
+                mma_commit(drain);
+            volatile int no_abort = 0;
+            mbar_wait(drain, 0, &no_abort, kDrainLimitNs);
+        }
+    } else {
+        // ------------------------------------------------ epilogue (warps 2 .. 2 + EW - 1)
+        constexpr int CH = C::EPI_CHUNK;
+        constexpr int COLS = BN / (EW / 4);  // columns this warp's quarter and half hold
+        const int quarter = warp & 3;
+        const int half = (warp - 2) >> 2;
+        OutT *out = static_cast<OutT *>(p.out);
+        const uint64_t pol_out = policy_of(p.l2_out);
+        OutT *slots = reinterpret_cast<OutT *>(epi_smem + (warp - 2) * C::NSLOT * C::EPI_SLOT_BYTES);
+        constexpr int SLOT_ELEMS = C::EPI_SLOT_BYTES / static_cast<int>(sizeof(float));
+        uint32_t slot = 0;
+        const uint32_t empty_addr0 = PAIR ? mapa_shared(smem_u32(&acc_empty[0]), 0) : 0u;
+        uint32_t acc = 0, acc_phase = 0;
+        bool ok = true;
+        for (int t = unit; t < num_tiles && ok; t += num_units) {
+            int mt, nt;
+            tile_coords(t, p, mt, nt);
+            const int chunks = (num_kb + kPromote - 1) / kPromote;
+            const int all = chunks + q.nslots[nt];
+            // this warp's columns of the tile's slot masks, one slot ahead
+            const uint32_t *masks = q.slot_mask + static_cast<int64_t>(nt) * q.max_slots * kSlotMaskWords +
+                                    half * COLS / 32;
+            constexpr int MW = COLS < 32 ? 1 : COLS / 32;
+            uint32_t mask[MW], ahead[MW];
+#pragma unroll
+            for (int i = 0; i < MW; ++i)
+                ahead[i] = all > chunks ? masks[i] : 0u;
+            float sum[COLS];
+#pragma unroll
+            for (int i = 0; i < COLS; ++i)
+                sum[i] = 0.f;
+#pragma unroll 1
+            for (int ch = 0; ch < all; ++ch) {
+                const bool shared = ch < chunks;
+                if (!shared) {
+#pragma unroll
+                    for (int i = 0; i < MW; ++i) {
+                        mask[i] = ahead[i];
+                        ahead[i] = ch + 1 < all ? masks[(ch + 1 - chunks) * kSlotMaskWords + i] : 0u;
+                    }
+                }
+                // every lane waits, then the warp agrees, so the .sync.aligned
+                // tensor-memory loads below always run with the full warp
+                const bool got = mbar_wait(&acc_full[acc], acc_phase, abort_flag, p.wait_limit_ns);
+                if (!__all_sync(0xffffffffu, got)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * BN + half * COLS;
+                if (shared) {
+#pragma unroll
+                    for (int c = 0; c < COLS; c += 16) {
+                        uint32_t r[32];
+                        tmem_ld_chunk<16>(taddr + c, r);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            sum[c + j] += __uint_as_float(r[j]);
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < COLS; c += 16) {
+                        const uint32_t m16 = (mask[c / 32] >> (c & 31)) & 0xffffu;
+                        if (m16 == 0)
+                            continue;
+                        uint32_t r[32];
+                        tmem_ld_chunk<16>(taddr + c, r);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            if (m16 >> j & 1u)
+                                sum[c + j] += __uint_as_float(r[j]);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (PAIR)
+                        mbar_arrive_cluster(empty_addr0 + acc * 8);
+                    else
+                        mbar_arrive(&acc_empty[acc]);
+                }
+                if (++acc == 2) {
+                    acc = 0;
+                    acc_phase ^= 1;
+                }
+            }
+            if (!ok)
+                break;
+            const int mbase = mt * C::TILE_M + static_cast<int>(rank) * kBlockM;
+            const int m = mbase + quarter * 32 + lane;
+            const int n0 = nt * BN + half * COLS;
+#pragma unroll
+            for (int c = 0; c < COLS; c += CH) {
+                if (TMA_STORE) {
+                    if (n0 + c < p.Ndim) {
+                        // the slot is free once the store issued NSLOT sub-tiles
+                        // ago has finished reading it
+                        if (lane == 0)
+                            bulk_wait_read<C::NSLOT - 1>();
+                        __syncwarp();
+                        OutT *buf = slots + slot * SLOT_ELEMS;
+#pragma unroll
+                        for (int j = 0; j < CH; ++j)
+                            stage_out(buf + j * 32 + lane, __float_as_uint(sum[c + j]));
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (p.l2_out)
+                                tma_store_2d_hint(&tmC, buf, mbase + quarter * 32, n0 + c, pol_out);
+                            else
+                                tma_store_2d(&tmC, buf, mbase + quarter * 32, n0 + c);
+                            bulk_commit();
+                        }
+                        slot = slot + 1 == C::NSLOT ? 0 : slot + 1;
+                    }
+                } else if (m < p.Mdim) {
+                    OutT *o = out + static_cast<int64_t>(n0 + c) * p.ldo + m;
+#pragma unroll
+                    for (int j = 0; j < CH; ++j)
+                        if (n0 + c + j < p.Ndim)
+                            store_out(o + static_cast<int64_t>(j) * p.ldo, __float_as_uint(sum[c + j]));
+                }
+            }
+        }
+        if (TMA_STORE && lane == 0)
+            bulk_wait_all();  // every output byte written before the CTA exits
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (PAIR) {
+        // as in gemm_tc_kernel: after a timeout the CTA that is behind issues the
+        // k-blocks it missed (any data: the stages are of one size), so that
+        // every phase a copy belongs to completes before either CTA leaves
+        cluster_sync();
+        const uint32_t peer = rank ^ 1u;
+        const int peer_abort = static_cast<int>(
+            ld_shared_cluster_u32(mapa_shared(smem_u32(const_cast<int *>(abort_flag)), peer)));
+        if (*abort_flag || peer_abort) {
+            if (threadIdx.x == 0) {
+                const uint32_t mine = *issued_sh;
+                const uint32_t theirs = ld_shared_cluster_u32(
+                    mapa_shared(smem_u32(const_cast<uint32_t *>(issued_sh)), peer));
+                const uint32_t all = mine > theirs ? mine : theirs;
+                for (uint32_t i = mine; i < all; ++i)
+                    issue_kblock(i % S, static_cast<int>(rank) * kBlockM,
+                                 static_cast<int>(rank) * C::BN_CTA, 0);
+                if (leader) {
+                    volatile int no_abort = 0;
+                    for (uint32_t i = all > S ? all - S : 0; i < all; ++i)
+                        mbar_wait(&full[i % S], (i / S) & 1u, &no_abort, kDrainLimitNs);
+                }
+            }
+            cluster_sync();
+        }
+        cluster_sync();
+    } else {
+        if (*abort_flag && threadIdx.x == 0) {
+            const uint32_t all = *issued_sh;
+            volatile int no_abort = 0;
+            for (uint32_t i = all > S ? all - S : 0; i < all; ++i)
+                mbar_wait(&full[i % S], (i / S) & 1u, &no_abort, kDrainLimitNs);
+        }
+    }
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        if (PAIR)
+            tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+        else
+            tmem_dealloc(tmem_base, C::TMEM_COLS);
+    }
+    if (threadIdx.x == 0 && *abort_flag && p.status)
+        atomicOr(p.status, 2);
+}
+
+}  // namespace lmh

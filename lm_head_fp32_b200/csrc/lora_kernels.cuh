@@ -1,0 +1,555 @@
+// lora_kernels.cuh -- the skinny products of the low-rank adapters:
+//
+//   rows   t[i, r]      = sum_c Y[i, c] P_a(r, c)      one row per token: u = s X A^T, g = s dl B
+//   cols   D_a[c, r]    = sum_{i of a} Y[i, c] t[i, r] one matrix per adapter: dB = dl^T u, dA = g^T X
+//
+// Both stream Y (dlogits: 1 GB at 4096 x 128256) through shared memory once with
+// cp.async and are bound by that: 2 to 8 MMAs per 512 bytes read, so mma.sync on
+// register fragments keeps up, and nothing needs tensor memory.
+//
+//   lora_rows_kernel    64 tokens x a range of c; a partial t per range.  For
+//                       each adapter among the tokens the product of all 64 is
+//                       formed and the rows of that adapter's tokens are kept.
+//   lora_expand_kernel  sums the partials in a fixed order, scales, and writes
+//                       t (FP32), its split into BF16 high and low parts for the
+//                       GEMM, and the slots of every token tile
+//   lora_group_kernel   the tokens of each adapter, in order
+//   lora_split_kernel   t in that order as three BF16 parts (FP32's 24 bits)
+//   lora_cols_kernel    128 columns of one adapter over its tokens
+//
+// Sums: FP32 in the MMAs over at most 256 terms, then added rounded to nearest
+// (rows: FP64 across ranges).  No atomics on values; every result has one order.
+#pragma once
+#include <cstdint>
+#include <cuda_bf16.h>
+
+#include "lora_gemm.cuh"
+#include "ptx.cuh"
+
+namespace lmh {
+
+constexpr int kRowsTokens = 64;    // tokens of one lora_rows_kernel CTA
+constexpr int kRowsSub = 128;      // columns of Y staged at once
+constexpr int kRowsThreads = 128;
+constexpr int kRankBlock = 64;     // ranks of one CTA (grid.z takes the others)
+constexpr int kColsTile = 128;     // columns of Y of one lora_cols_kernel CTA
+constexpr int kColsTokens = 32;    // tokens staged at once
+constexpr int kColsThreads = 128;
+constexpr int kColsStages = 4;
+constexpr int kColsPromote = 8;    // stages (256 tokens) summed in the MMAs
+constexpr int kExpandTokens = 16;  // tokens of one lora_expand_kernel CTA
+constexpr int kDevBadAdapter = 0x8;  // LMH_DEV_BAD_ADAPTER
+
+// 16 bytes global -> shared; zeros where `in` is false (nothing is read then).
+__device__ __forceinline__ void cp16(void *dst, const void *src, bool in)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+                 "r"(in ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], const void *p)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(smem_u32(p)));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], const void *p)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(smem_u32(p)));
+}
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Rows of shared tiles are padded to an odd number of 16-byte units, so that the
+// eight rows of an ldmatrix lie in different banks.
+constexpr int pad_row(int elems) { return elems * 2 + 16; }
+
+template <bool P_MN, int NT>
+struct RowsCfg {
+    static constexpr int RB = NT * 16;
+    static constexpr int Y_ROW = pad_row(kRowsSub);
+    static constexpr int Y_BYTES = kRowsTokens * Y_ROW;
+    static constexpr int P_ROW = P_MN ? pad_row(RB) : pad_row(kRowsSub);
+    static constexpr int P_BYTES = (P_MN ? kRowsSub : RB) * P_ROW;
+    static constexpr int SMEM = 3 * (Y_BYTES + P_BYTES);
+};
+
+// partial[range][i][r]: the range's share of t.  Y [M][Cdim] BF16; P_MN: P
+// [adapter][Cdim][R] (B), else [adapter][R][Cdim] (A).  Rpad: R rounded up to 16.
+template <bool P_MN, int NT>
+__global__ void __launch_bounds__(kRowsThreads)
+    lora_rows_kernel(const __nv_bfloat16 *__restrict__ Y, const __nv_bfloat16 *__restrict__ P,
+                     const int32_t *__restrict__ adapter, float *__restrict__ partial, int64_t M,
+                     int64_t Cdim, int32_t R, int32_t Rpad, int32_t N, int32_t subs_per_range)
+{
+    using G = RowsCfg<P_MN, NT>;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ int32_t ids[kRowsTokens];
+    __shared__ int32_t list[kRowsTokens];
+    __shared__ int warp_n[2];
+    uint8_t *ybuf = smem, *pbuf = smem + 3 * G::Y_BYTES;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int64_t i0 = static_cast<int64_t>(blockIdx.y) * kRowsTokens;
+    const int r0 = blockIdx.z * kRankBlock;
+    pdl_wait();
+    pdl_launch_dependents();
+    bool first = false;
+    if (tid < kRowsTokens) {
+        int32_t a = i0 + tid < M ? adapter[i0 + tid] : -1;
+        ids[tid] = a < 0 || a >= N ? -1 : a;
+    }
+    __syncthreads();
+    if (tid < kRowsTokens) {
+        const int32_t a = ids[tid];
+        first = a >= 0;
+        for (int j = 0; j < tid && first; ++j)
+            first = ids[j] != a;
+        const unsigned b = __ballot_sync(0xffffffffu, first);
+        if (lane == 0)
+            warp_n[warp] = __popc(b);
+    }
+    __syncthreads();
+    const int nslot = warp_n[0] + warp_n[1];
+    if (tid < kRowsTokens) {
+        const unsigned b = __ballot_sync(0xffffffffu, first);
+        if (first)
+            list[(warp ? warp_n[0] : 0) + __popc(b & ((1u << lane) - 1u))] = ids[tid];
+    }
+    __syncthreads();
+
+    const int64_t nsub_all = (Cdim + kRowsSub - 1) / kRowsSub;
+    const int64_t sub0 = static_cast<int64_t>(blockIdx.x) * subs_per_range;
+    const int nsub = static_cast<int>(nsub_all - sub0 < subs_per_range ? nsub_all - sub0 : subs_per_range);
+    float acc[2 * NT][4];
+#pragma unroll
+    for (int n = 0; n < 2 * NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            acc[n][e] = 0.f;
+    const int steps = nsub * nslot;
+    // step t: columns sub t / nslot against adapter t % nslot
+    auto load = [&](int t) {
+        if (t < steps) {
+            const int sub = t / nslot, j = t - sub * nslot;
+            const int64_t c0 = (sub0 + sub) * kRowsSub;
+            if (j == 0) {
+                uint8_t *y = ybuf + (sub % 3) * G::Y_BYTES;
+                for (int k = tid; k < kRowsTokens * (kRowsSub / 8); k += kRowsThreads) {
+                    const int row = k / (kRowsSub / 8), ch = k % (kRowsSub / 8);
+                    const bool in = i0 + row < M && c0 + ch * 8 < Cdim;
+                    cp16(y + row * G::Y_ROW + ch * 16, in ? Y + (i0 + row) * Cdim + c0 + ch * 8 : Y, in);
+                }
+            }
+            uint8_t *pb = pbuf + (t % 3) * G::P_BYTES;
+            const __nv_bfloat16 *base = P + static_cast<int64_t>(list[j]) * R * Cdim;
+            if (P_MN) {
+                for (int k = tid; k < kRowsSub * (G::RB / 8); k += kRowsThreads) {
+                    const int row = k / (G::RB / 8), ch = k % (G::RB / 8);
+                    const bool in = c0 + row < Cdim && r0 + ch * 8 < R;
+                    cp16(pb + row * G::P_ROW + ch * 16, in ? base + (c0 + row) * R + r0 + ch * 8 : P, in);
+                }
+            } else {
+                for (int k = tid; k < G::RB * (kRowsSub / 8); k += kRowsThreads) {
+                    const int row = k / (kRowsSub / 8), ch = k % (kRowsSub / 8);
+                    const bool in = r0 + row < R && c0 + ch * 8 < Cdim;
+                    cp16(pb + row * G::P_ROW + ch * 16, in ? base + (r0 + row) * Cdim + c0 + ch * 8 : P, in);
+                }
+            }
+        }
+        cp_commit();
+    };
+    const int g = lane >> 2;  // this thread's rows of the warp's 16: g and g + 8
+    const int id0 = ids[warp * 16 + g], id1 = ids[warp * 16 + g + 8];
+    load(0);
+    load(1);
+    for (int t = 0; t < steps; ++t) {
+        cp_wait<1>();
+        __syncthreads();  // step t has landed; the buffers of step t - 1 are free
+        load(t + 2);
+        const int sub = t / nslot, a = list[t - sub * nslot];
+        const bool k0 = id0 == a, k1 = id1 == a;
+        if (!__any_sync(0xffffffffu, k0 || k1))
+            continue;
+        const uint8_t *y = ybuf + (sub % 3) * G::Y_BYTES;
+        const uint8_t *pb = pbuf + (t % 3) * G::P_BYTES;
+        float part[2 * NT][4];
+#pragma unroll
+        for (int n = 0; n < 2 * NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                part[n][e] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < kRowsSub / 16; ++ks) {
+            uint32_t fa[4];
+            ldsm4(fa, y + (warp * 16 + (lane & 15)) * G::Y_ROW + (ks * 16 + (lane >> 4) * 8) * 2);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                uint32_t fb[4];
+                const int mat = lane >> 3, l = lane & 7;
+                if (P_MN)
+                    ldsm4t(fb, pb + (ks * 16 + (mat & 1) * 8 + l) * G::P_ROW + (n * 16 + (mat >> 1) * 8) * 2);
+                else
+                    ldsm4(fb, pb + (n * 16 + (mat >> 1) * 8 + l) * G::P_ROW + (ks * 16 + (mat & 1) * 8) * 2);
+                mma16816(part[2 * n], fa, fb[0], fb[1]);
+                mma16816(part[2 * n + 1], fa, fb[2], fb[3]);
+            }
+        }
+        // only the rows of this adapter's tokens (a select, not a product with
+        // zero: another adapter's infinities stay out)
+#pragma unroll
+        for (int n = 0; n < 2 * NT; ++n) {
+            if (k0) {
+                acc[n][0] += part[n][0];
+                acc[n][1] += part[n][1];
+            }
+            if (k1) {
+                acc[n][2] += part[n][2];
+                acc[n][3] += part[n][3];
+            }
+        }
+    }
+    cp_wait<0>();
+    float *out = partial + static_cast<int64_t>(blockIdx.x) * M * Rpad;
+#pragma unroll
+    for (int n = 0; n < 2 * NT; ++n) {
+        const int r = r0 + n * 8 + (lane & 3) * 2;
+        if (r < Rpad) {
+            const int64_t ia = i0 + warp * 16 + g;
+            if (ia < M)
+                *reinterpret_cast<float2 *>(out + ia * Rpad + r) = make_float2(acc[n][0], acc[n][1]);
+            if (ia + 8 < M)
+                *reinterpret_cast<float2 *>(out + (ia + 8) * Rpad + r) = make_float2(acc[n][2], acc[n][3]);
+        }
+    }
+}
+
+// x as BF16 high part and remainder; an x with no finite remainder has none.
+__device__ __forceinline__ __nv_bfloat16 split_hi(float x, float &rest)
+{
+    const __nv_bfloat16 h = __float2bfloat16_rn(x);
+    const float hf = __bfloat162float(h);
+    rest = fabsf(hf) < INFINITY ? x - hf : 0.f;
+    return h;
+}
+
+// grid (token tiles of the GEMM, parts of kExpandTokens tokens).
+//   t    [M][R] FP32, scaled: u or g (0 for a token without adapter)
+//   ux   [tile][stages][bn][64] BF16: up to 32 ranks one stage {high 0..31, low
+//        0..31}, above that per 64 ranks a stage of high and one of low parts
+//   nslots, slot_id, slot_mask: see LoraParams (written by part 0)
+__global__ void __launch_bounds__(256)
+    lora_expand_kernel(const float *__restrict__ partial, int32_t ranges, const int32_t *__restrict__ adapter,
+                       const float *__restrict__ scale, float *__restrict__ t_out,
+                       __nv_bfloat16 *__restrict__ ux, int32_t *__restrict__ nslots,
+                       int32_t *__restrict__ slot_id, uint32_t *__restrict__ slot_mask, int32_t bn,
+                       int32_t slot_stride, int32_t max_slots, int32_t stages, int64_t M, int32_t R,
+                       int32_t Rpad, int32_t N, int32_t *status)
+{
+    __shared__ int32_t ids[256];
+    __shared__ int32_t warp_n[8];
+    extern __shared__ float val[];  // [kExpandTokens][Rpad]
+    pdl_wait();
+    pdl_launch_dependents();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int64_t tile = blockIdx.x;
+    const int64_t i0 = tile * bn;
+    const int tok0 = blockIdx.y * kExpandTokens;
+    if (tid < bn) {
+        int32_t a = i0 + tid < M ? adapter[i0 + tid] : -1;
+        if (a < -1 || a >= N) {
+            if (status && blockIdx.y == 0)
+                atomicOr(status, kDevBadAdapter);
+            a = -1;
+        }
+        ids[tid] = a;
+    } else if (tid < 256) {
+        ids[tid] = -1;
+    }
+    __syncthreads();
+
+    for (int k = tid; k < kExpandTokens * Rpad; k += 256) {
+        const int tk = tok0 + k / Rpad, r = k % Rpad;
+        float v = 0.f;
+        if (tk < bn && i0 + tk < M && r < R) {
+            const int a = ids[tk];
+            if (a >= 0) {
+                const float *p = partial + (i0 + tk) * Rpad + r;
+                double s = 0.0;
+#pragma unroll 8
+                for (int q = 0; q < ranges; ++q)
+                    s += static_cast<double>(p[static_cast<int64_t>(q) * M * Rpad]);
+                v = static_cast<float>(s * static_cast<double>(scale[a]));
+            }
+            t_out[(i0 + tk) * R + r] = v;
+        }
+        val[k] = v;
+    }
+    __syncthreads();
+    // the split parts of this CTA's tokens, eight columns per store
+    const int per_token = stages * 8;
+    for (int k = tid; k < kExpandTokens * per_token; k += 256) {
+        const int j = k / per_token, rest = k % per_token;
+        const int st = rest >> 3, c0 = (rest & 7) * 8;
+        const int tk = tok0 + j;
+        if (tk >= bn)
+            break;
+        const bool low = stages == 1 ? c0 >= 32 : (st & 1);
+        const int r0 = stages == 1 ? (c0 & 31) : (st >> 1) * 64 + c0;
+        __nv_bfloat16 h[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float v = r0 + e < Rpad ? val[j * Rpad + r0 + e] : 0.f;
+            float low_part;
+            const __nv_bfloat16 hi = split_hi(v, low_part);
+            h[e] = low ? __float2bfloat16_rn(low_part) : hi;
+        }
+        *reinterpret_cast<uint4 *>(ux + ((tile * stages + st) * bn + tk) * 64 + c0) = *reinterpret_cast<uint4 *>(h);
+    }
+    if (blockIdx.y != 0)
+        return;
+    // the tile's slots, in the order in which their adapters occur
+    const int32_t a = ids[tid];
+    bool first = a >= 0;
+    for (int j = 0; j < tid && first; ++j)
+        first = ids[j] != a;
+    const unsigned b = __ballot_sync(0xffffffffu, first);
+    if (lane == 0)
+        warp_n[warp] = __popc(b);
+    __syncthreads();
+    int slot = __popc(b & ((1u << lane) - 1u)), all = 0;
+    for (int w = 0; w < 8; ++w) {
+        if (w < warp)
+            slot += warp_n[w];
+        all += warp_n[w];
+    }
+    if (tid == 0)
+        nslots[tile] = all;
+    if (first) {
+        slot_id[tile * slot_stride + slot] = a;
+        uint32_t *m = slot_mask + (tile * max_slots + slot) * kSlotMaskWords;
+        for (int w = 0; w < kSlotMaskWords; ++w) {
+            uint32_t bits = 0;
+            for (int j = 0; j < 32; ++j)
+                bits |= static_cast<uint32_t>(ids[w * 32 + j] == a) << j;
+            m[w] = bits;
+        }
+    }
+}
+
+// One CTA per adapter: start[a] (tokens of lower adapters) and its tokens in
+// order, order[start[a] ..].  start has N + 1 entries.
+__global__ void __launch_bounds__(1024)
+    lora_group_kernel(const int32_t *__restrict__ adapter, int32_t *__restrict__ start,
+                      int32_t *__restrict__ order, int64_t M, int32_t N, int32_t *status)
+{
+    __shared__ int warp_n[32];
+    __shared__ int below;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int a = blockIdx.x;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0)
+        below = 0;
+    __syncthreads();
+    int n = 0;
+    for (int64_t i = tid; i < M; i += 1024) {
+        const int32_t x = adapter[i];
+        n += x >= 0 && x < a;
+        if (a == 0 && status && (x < -1 || x >= N))
+            atomicOr(status, kDevBadAdapter);
+    }
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (lane == 0)
+        atomicAdd(&below, n);  // whole numbers: any order
+    __syncthreads();
+    int at = below;
+    if (tid == 0)
+        start[a] = at;
+    for (int64_t i0 = 0; i0 < M; i0 += 1024) {
+        const int64_t i = i0 + tid;
+        const bool mine = i < M && adapter[i] == a;
+        const unsigned b = __ballot_sync(0xffffffffu, mine);
+        if (lane == 0)
+            warp_n[warp] = __popc(b);
+        __syncthreads();
+        int place = __popc(b & ((1u << lane) - 1u)), all = 0;
+        for (int w = 0; w < 32; ++w) {
+            if (w < warp)
+                place += warp_n[w];
+            all += warp_n[w];
+        }
+        if (mine)
+            order[at + place] = static_cast<int32_t>(i);
+        at += all;
+        __syncthreads();
+    }
+    if (a == N - 1 && tid == 0)
+        start[N] = at;
+}
+
+// parts[pos][3][Rpad] BF16 of t[order[pos]]: x = high + middle + low, exact to
+// FP32's 24 bits (while the low part stays normal); zeros in the padding.
+__global__ void __launch_bounds__(256)
+    lora_split_kernel(const float *__restrict__ t, const int32_t *__restrict__ start,
+                      const int32_t *__restrict__ order, __nv_bfloat16 *__restrict__ parts, int32_t N,
+                      int32_t R, int32_t Rpad)
+{
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t total = static_cast<int64_t>(start[N]) * Rpad;
+    for (int64_t k = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; k < total;
+         k += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t pos = k / Rpad;
+        const int r = static_cast<int>(k - pos * Rpad);
+        const float x = r < R ? t[static_cast<int64_t>(order[pos]) * R + r] : 0.f;
+        float rest, rest2;
+        const __nv_bfloat16 h = split_hi(x, rest), m = split_hi(rest, rest2);
+        __nv_bfloat16 *o = parts + pos * 3 * Rpad + r;
+        o[0] = h;
+        o[Rpad] = m;
+        o[2 * Rpad] = __float2bfloat16_rn(rest2);
+    }
+}
+
+template <int NT>
+struct ColsCfg {
+    static constexpr int RB = NT * 16;
+    static constexpr int Y_ROW = pad_row(kColsTile);
+    static constexpr int Y_BYTES = kColsTokens * Y_ROW;
+    static constexpr int T_ROW = pad_row(3 * RB);
+    static constexpr int T_BYTES = kColsTokens * T_ROW;
+    static constexpr int SMEM = kColsStages * (Y_BYTES + T_BYTES);
+};
+
+// grid (column tiles, adapters, rank blocks).  out: OUT_RC [adapter][R][Cdim]
+// (dA), else [adapter][Cdim][R] (dB), FP32; zeros for an adapter without tokens.
+template <int NT, bool OUT_RC>
+__global__ void __launch_bounds__(kColsThreads)
+    lora_cols_kernel(const __nv_bfloat16 *__restrict__ Y, const __nv_bfloat16 *__restrict__ parts,
+                     const int32_t *__restrict__ start, const int32_t *__restrict__ order,
+                     float *__restrict__ out, int64_t Cdim, int32_t R, int32_t Rpad)
+{
+    using G = ColsCfg<NT>;
+    extern __shared__ __align__(16) uint8_t smem[];
+    uint8_t *ybuf = smem, *tbuf = smem + kColsStages * G::Y_BYTES;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kColsTile;
+    const int a = blockIdx.y, r0 = blockIdx.z * kRankBlock;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int first = start[a], count = start[a + 1] - first;
+    const int steps = (count + kColsTokens - 1) / kColsTokens;
+    auto load = [&](int t) {
+        if (t < steps) {
+            uint8_t *y = ybuf + (t % kColsStages) * G::Y_BYTES;
+            for (int k = tid; k < kColsTokens * (kColsTile / 8); k += kColsThreads) {
+                const int row = k / (kColsTile / 8), ch = k % (kColsTile / 8);
+                const int pos = t * kColsTokens + row;
+                const bool in = pos < count && c0 + ch * 8 < Cdim;
+                cp16(y + row * G::Y_ROW + ch * 16,
+                     in ? Y + static_cast<int64_t>(order[first + pos]) * Cdim + c0 + ch * 8 : Y, in);
+            }
+            uint8_t *tb = tbuf + (t % kColsStages) * G::T_BYTES;
+            for (int k = tid; k < kColsTokens * 3 * (G::RB / 8); k += kColsThreads) {
+                const int row = k / (3 * (G::RB / 8)), rest = k % (3 * (G::RB / 8));
+                const int part = rest / (G::RB / 8), ch = rest % (G::RB / 8);
+                const int pos = t * kColsTokens + row;
+                const bool in = pos < count && r0 + ch * 8 < Rpad;
+                cp16(tb + row * G::T_ROW + (part * G::RB + ch * 8) * 2,
+                     in ? parts + (static_cast<int64_t>(first + pos) * 3 + part) * Rpad + r0 + ch * 8 : parts, in);
+            }
+        }
+        cp_commit();
+    };
+    float acc[2][2 * NT][4], part[2][2 * NT][4];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int n = 0; n < 2 * NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                acc[m][n][e] = part[m][n][e] = 0.f;
+#pragma unroll
+    for (int t = 0; t < kColsStages - 1; ++t)
+        load(t);
+    const int mat = lane >> 3, l = lane & 7;
+    for (int t = 0; t < steps; ++t) {
+        cp_wait<kColsStages - 2>();
+        __syncthreads();
+        load(t + kColsStages - 1);
+        const uint8_t *y = ybuf + (t % kColsStages) * G::Y_BYTES;
+        const uint8_t *tb = tbuf + (t % kColsStages) * G::T_BYTES;
+#pragma unroll
+        for (int ks = 0; ks < kColsTokens / 16; ++ks) {
+            uint32_t fa[2][4];
+#pragma unroll
+            for (int m = 0; m < 2; ++m)  // 16 columns of Y x 16 tokens, out of token-major rows
+                ldsm4t(fa[m], y + (ks * 16 + (mat >> 1) * 8 + l) * G::Y_ROW + (warp * 32 + m * 16 + (mat & 1) * 8) * 2);
+#pragma unroll
+            for (int s = 2; s >= 0; --s) {  // the small parts first
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    uint32_t fb[4];
+                    ldsm4t(fb, tb + (ks * 16 + (mat & 1) * 8 + l) * G::T_ROW + (s * G::RB + n * 16 + (mat >> 1) * 8) * 2);
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        mma16816(part[m][2 * n], fa[m], fb[0], fb[1]);
+                        mma16816(part[m][2 * n + 1], fa[m], fb[2], fb[3]);
+                    }
+                }
+            }
+        }
+        if (t % kColsPromote == kColsPromote - 1 || t == steps - 1) {
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int n = 0; n < 2 * NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        acc[m][n][e] += part[m][n][e];
+                        part[m][n][e] = 0.f;
+                    }
+        }
+    }
+    cp_wait<0>();
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int e2 = 0; e2 < 2; ++e2) {
+            const int64_t c = c0 + warp * 32 + m * 16 + (lane >> 2) + e2 * 8;
+            if (c >= Cdim)
+                continue;
+#pragma unroll
+            for (int n = 0; n < 2 * NT; ++n) {
+                const int r = r0 + n * 8 + (lane & 3) * 2;
+                if (r >= R)  // R is a multiple of 8: r + 1 < R as well
+                    continue;
+                const float x = acc[m][n][2 * e2], z = acc[m][n][2 * e2 + 1];
+                if (OUT_RC) {
+                    float *o = out + (static_cast<int64_t>(a) * R + r) * Cdim + c;
+                    o[0] = x;
+                    o[Cdim] = z;
+                } else {
+                    *reinterpret_cast<float2 *>(out + (static_cast<int64_t>(a) * Cdim + c) * R + r) = make_float2(x, z);
+                }
+            }
+        }
+}
+
+}  // namespace lmh

@@ -21,6 +21,7 @@ F32, BF16, F16 = 0, 1, 2
 DEV_BAD_TARGET = 0x1
 DEV_PIPE_TIMEOUT = 0x2
 DEV_BAD_LOGIT = 0x4
+DEV_BAD_ADAPTER = 0x8
 DEV_BAD_PARENT = 0x10
 IGNORE_INDEX = -100
 
@@ -29,7 +30,8 @@ EXPORTS = ("lmhead_fwd", "ce_fwd", "ce_bwd", "lmhead_bwd_dx", "lmhead_bwd_dw",
            "lmhead_bwd_dw_acc", "ce_fwd_shard", "ce_merge_shards", "ce_bwd_shard",
            "lmh_status_string", "lmh_version", "lmh_watchdog_selftest",
            "lmh_gemm_watchdog_selftest", "beam_select", "beam_select_workspace_bytes",
-           "beam_reorder")
+           "beam_reorder", "lmhead_fwd_lora", "lmhead_lora_workspace_bytes", "lmhead_bwd_dx_lora",
+           "lmhead_bwd_lora")
 
 _lib = None
 
@@ -80,7 +82,13 @@ def lib() -> ctypes.CDLL:
         L.beam_select_workspace_bytes.argtypes = [I64, I64, I64, I64]
         L.beam_select_workspace_bytes.restype = I64
         L.beam_reorder.argtypes = [P, I64, P, I64, I64, I64, I64, I64, P, P, I64, P, P]
-        for f in ("beam_select", "beam_reorder"):
+        L.lmhead_lora_workspace_bytes.argtypes = [I64] * 5
+        L.lmhead_lora_workspace_bytes.restype = I64
+        for f in ("lmhead_fwd_lora", "lmhead_bwd_dx_lora"):
+            getattr(L, f).argtypes = [P] * 8 + [I32, P] + [I64] * 6 + [P, P]
+        L.lmhead_bwd_lora.argtypes = [P] * 8 + [I64] * 6 + [P, P]
+        for f in ("beam_select", "beam_reorder", "lmhead_fwd_lora", "lmhead_bwd_dx_lora",
+                  "lmhead_bwd_lora"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -245,7 +253,8 @@ def gemm_watchdog_selftest(X: torch.Tensor, W: torch.Tensor, logits: torch.Tenso
     _check(lib().lmh_gemm_watchdog_selftest(_ptr(X), _ptr(W), _ptr(logits), M, K, V,
                                             int(limit_ns), _ptr(status), _stream(stream)),
            "lmh_gemm_watchdog_selftest", "beam_select", "beam_select_workspace_bytes",
-           "beam_reorder")
+           "beam_reorder", "lmhead_fwd_lora", "lmhead_lora_workspace_bytes", "lmhead_bwd_dx_lora",
+           "lmhead_bwd_lora")
 
 
 def lmhead_bwd_dw_acc(dlogits: torch.Tensor, X: torch.Tensor, dW: torch.Tensor,
@@ -433,3 +442,74 @@ def beam_reorder(states, parents: torch.Tensor, entry_dim: int = 0,
                    first.stride(entry_dim) * es, first.stride(entry_dim + 1) * es, run,
                    (I64 * k)(*outer), (I64 * k)(*strides), k, sp), "beam_reorder")
     return states
+
+
+def lmhead_lora_workspace_bytes(M: int, K: int, V: int, R: int, N: int) -> int:
+    """Scratch bytes each of the adapter calls needs at most for M tokens and N
+    adapters of rank R (-1 for sizes out of range)."""
+    return int(lib().lmhead_lora_workspace_bytes(int(M), int(K), int(V), int(R), int(N)))
+
+
+def lmhead_fwd_lora(X: torch.Tensor, W: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
+                    scale: torch.Tensor, adapter: torch.Tensor, u: torch.Tensor,
+                    logits: torch.Tensor, workspace: torch.Tensor,
+                    status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """logits[M,V] (FP32 or BF16) = X[M,K] . W[V,K]^T + u . B_a^T with
+    u[M,R] (FP32, written) = scale[a] X . A_a^T, the adapter a = adapter[i] (int32,
+    -1 for none) of each token out of A[N,R,K], B[N,V,R] (BF16), scale[N] (FP32)."""
+    if X.dim() != 2 or W.dim() != 2 or A.dim() != 3:
+        raise ValueError("expected X [M,K], W [V,K], A [N,R,K]")
+    (M, K), V, (N, R) = X.shape, W.shape[0], A.shape[:2]
+    b16, f32 = torch.bfloat16, torch.float32
+    wp, wn = _workspace(workspace, X)
+    _check(_on(X, stream, lib().lmhead_fwd_lora, _take("X", X, (M, K), b16),
+               _take("W", W, (V, K), b16, like=X), _take("A", A, (N, R, K), b16, like=X),
+               _take("B", B, (N, V, R), b16, like=X), _take("scale", scale, (N,), f32, like=X),
+               _take("adapter", adapter, (M,), torch.int32, like=X),
+               _take("u", u, (M, R), f32, like=X), _take("logits", logits, (M, V), f32, b16, like=X),
+               _dtype_code(logits.dtype), wp, wn, M, K, V, R, N, _status(status, X)),
+           "lmhead_fwd_lora")
+    return logits
+
+
+def lmhead_bwd_dx_lora(dlogits: torch.Tensor, W: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
+                       scale: torch.Tensor, adapter: torch.Tensor, g: torch.Tensor,
+                       dX: torch.Tensor, workspace: torch.Tensor,
+                       status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """dX[M,K] (FP32 or BF16) = dlogits[M,V] . W + g . A_a with g[M,R] (FP32, written)
+    = scale[a] dlogits . B_a: the input gradient of lmhead_fwd_lora."""
+    if dlogits.dim() != 2 or W.dim() != 2 or A.dim() != 3:
+        raise ValueError("expected dlogits [M,V], W [V,K], A [N,R,K]")
+    (M, V), K, (N, R) = dlogits.shape, W.shape[1], A.shape[:2]
+    b16, f32 = torch.bfloat16, torch.float32
+    wp, wn = _workspace(workspace, dlogits)
+    _check(_on(dlogits, stream, lib().lmhead_bwd_dx_lora, _take("dlogits", dlogits, (M, V), b16),
+               _take("W", W, (V, K), b16, like=dlogits), _take("A", A, (N, R, K), b16, like=dlogits),
+               _take("B", B, (N, V, R), b16, like=dlogits),
+               _take("scale", scale, (N,), f32, like=dlogits),
+               _take("adapter", adapter, (M,), torch.int32, like=dlogits),
+               _take("g", g, (M, R), f32, like=dlogits), _take("dX", dX, (M, K), f32, b16, like=dlogits),
+               _dtype_code(dX.dtype), wp, wn, M, K, V, R, N, _status(status, dlogits)),
+           "lmhead_bwd_dx_lora")
+    return dX
+
+
+def lmhead_bwd_lora(dlogits: torch.Tensor, X: torch.Tensor, u: torch.Tensor, g: torch.Tensor,
+                    adapter: torch.Tensor, dA: torch.Tensor, dB: torch.Tensor,
+                    workspace: torch.Tensor, status: Optional[torch.Tensor] = None, stream=None):
+    """The adapters' gradients dA[N,R,K], dB[N,V,R] (FP32) from the u of
+    lmhead_fwd_lora and the g of lmhead_bwd_dx_lora: over the tokens of each adapter,
+    dA_a = g^T . X and dB_a = dlogits^T . u (zeros for an adapter without tokens)."""
+    if dlogits.dim() != 2 or X.dim() != 2 or dA.dim() != 3:
+        raise ValueError("expected dlogits [M,V], X [M,K], dA [N,R,K]")
+    (M, V), K, (N, R) = dlogits.shape, X.shape[1], dA.shape[:2]
+    b16, f32 = torch.bfloat16, torch.float32
+    wp, wn = _workspace(workspace, dlogits)
+    _check(_on(dlogits, stream, lib().lmhead_bwd_lora, _take("dlogits", dlogits, (M, V), b16),
+               _take("X", X, (M, K), b16, like=dlogits), _take("u", u, (M, R), f32, like=dlogits),
+               _take("g", g, (M, R), f32, like=dlogits),
+               _take("adapter", adapter, (M,), torch.int32, like=dlogits),
+               _take("dA", dA, (N, R, K), f32, like=dlogits),
+               _take("dB", dB, (N, V, R), f32, like=dlogits), wp, wn, M, K, V, R, N,
+               _status(status, dlogits)), "lmhead_bwd_lora")
+    return dA, dB

@@ -35,6 +35,14 @@ def _check_inputs(X: torch.Tensor, W: torch.Tensor, target: torch.Tensor):
         raise ValueError("expected X [M,K], W [V,K], target [M]")
 
 
+def _row_gradients(grad_loss: torch.Tensor) -> torch.Tensor:
+    """The loss gradient as ce_bwd takes it: one element when every token has the
+    same (loss.sum(), loss.mean()), otherwise one per token."""
+    if grad_loss.dim() == 1 and grad_loss.shape[0] > 1 and grad_loss.stride(0) == 0:
+        grad_loss = grad_loss[:1]
+    return grad_loss.to(torch.float32).contiguous()
+
+
 class _LMHeadCrossEntropy(torch.autograd.Function):
     @staticmethod
     def forward(ctx, X, W, target, ignore_index, fused, main_grad, status):
@@ -60,13 +68,7 @@ class _LMHeadCrossEntropy(torch.autograd.Function):
     def backward(ctx, grad_loss):
         X, W, target, logits, stats, status = ctx.saved_tensors
         M, V = logits.shape
-        # one element when every token has the same gradient (loss.sum(),
-        # loss.mean()), which ce_bwd broadcasts; otherwise one per token
-        if grad_loss.dim() == 1 and grad_loss.shape[0] > 1 and grad_loss.stride(0) == 0:
-            g = grad_loss[:1]
-        else:
-            g = grad_loss
-        g = g.to(torch.float32).contiguous()
+        g = _row_gradients(grad_loss)
         dl = torch.empty((M, V), dtype=torch.bfloat16, device=X.device)
         lmhead.ce_bwd(logits, target, stats, g, dl, ctx.ignore_index, status)
         dX = dW = None
@@ -98,3 +100,71 @@ def lm_head_cross_entropy(X: torch.Tensor, W: torch.Tensor, target: torch.Tensor
         raise ValueError("main_grad must be an FP32 tensor shaped like W")
     return _LMHeadCrossEntropy.apply(X.contiguous(), W.contiguous(), target.contiguous(),
                                      int(ignore_index), bool(fused), main_grad, status)
+
+
+class _LMHeadLoraCrossEntropy(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, X, W, A, B, scale, adapter, target, ignore_index, status):
+        (M, K), V, (N, R) = X.shape, W.shape[0], A.shape[:2]
+        dev = X.device
+        if status is None:
+            status = torch.zeros(1, dtype=torch.int32, device=dev)
+        logits = torch.empty((M, V), dtype=torch.float32, device=dev)
+        stats = torch.empty((M, 4), dtype=torch.float32, device=dev)
+        u = torch.empty((M, R), dtype=torch.float32, device=dev)
+        ws = torch.empty(max(lmhead.lmhead_lora_workspace_bytes(M, K, V, R, N), 16),
+                         dtype=torch.uint8, device=dev)
+        lmhead.lmhead_fwd_lora(X, W, A, B, scale, adapter, u, logits, ws, status)
+        with torch.cuda.device(dev):
+            lmhead.ce_fwd(logits, target, stats, ignore_index, status)
+        ctx.save_for_backward(X, W, A, B, scale, adapter, target, logits, stats, u, status)
+        ctx.ignore_index = ignore_index
+        return stats[:, 3].clone()
+
+    @staticmethod
+    def backward(ctx, grad_loss):
+        X, W, A, B, scale, adapter, target, logits, stats, u, status = ctx.saved_tensors
+        (M, K), V, (N, R) = X.shape, W.shape[0], A.shape[:2]
+        dev = X.device
+        need_x, need_w, need_a, need_b = ctx.needs_input_grad[:4]
+        dl = torch.empty((M, V), dtype=torch.bfloat16, device=dev)
+        with torch.cuda.device(dev):
+            lmhead.ce_bwd(logits, target, stats, _row_gradients(grad_loss), dl, ctx.ignore_index,
+                          status)
+        dX = dW = dA = dB = None
+        if need_x or need_a or need_b:
+            ws = torch.empty(max(lmhead.lmhead_lora_workspace_bytes(M, K, V, R, N), 16),
+                             dtype=torch.uint8, device=dev)
+            # g, which dA needs, comes with dX
+            g = torch.empty((M, R), dtype=torch.float32, device=dev)
+            dX = lmhead.lmhead_bwd_dx_lora(dl, W, A, B, scale, adapter, g, torch.empty_like(X), ws,
+                                           status)
+            if need_a or need_b:
+                dA = torch.empty(A.shape, dtype=torch.float32, device=dev)
+                dB = torch.empty(B.shape, dtype=torch.float32, device=dev)
+                lmhead.lmhead_bwd_lora(dl, X, u, g, adapter, dA, dB, ws, status)
+                dA, dB = dA.to(A.dtype), dB.to(B.dtype)
+        if need_w:
+            with torch.cuda.device(dev):
+                dW = lmhead.lmhead_bwd_dw(dl, X, torch.empty_like(W), status)
+        return dX, dW, dA, dB, None, None, None, None, None
+
+
+def lm_head_lora_cross_entropy(X: torch.Tensor, W: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
+                               scale: torch.Tensor, adapter: torch.Tensor, target: torch.Tensor,
+                               ignore_index: int = lmhead.IGNORE_INDEX,
+                               status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Per-token loss [M] (FP32) of the LM head with low-rank adapters, one per token:
+    -log softmax(X . W^T + scale[a] (X . A_a^T) . B_a^T)[target], a = adapter[i].
+
+    X, W, target as in lm_head_cross_entropy (V % 8 == 0); A: [N, R, K], B: [N, V, R]
+    bfloat16, scale: [N] float32 (no gradient), adapter: [M] int32, -1 for a token
+    without adapter.  The backward gives X, A, B and, where it asks for one (a frozen
+    head does not), W bfloat16 gradients; the adapters' are summed in FP32 and
+    rounded once."""
+    _check_inputs(X, W, target)
+    if A.dim() != 3 or B.dim() != 3 or A.dtype != torch.bfloat16 or B.dtype != torch.bfloat16:
+        raise ValueError("expected bfloat16 A [N,R,K] and B [N,V,R]")
+    return _LMHeadLoraCrossEntropy.apply(X.contiguous(), W.contiguous(), A.contiguous(),
+                                         B.contiguous(), scale.contiguous(), adapter.contiguous(),
+                                         target.contiguous(), int(ignore_index), status)
