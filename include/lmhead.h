@@ -273,16 +273,17 @@ LMH_API lmh_status_t lmhead_bwd_dw_acc(const void *dlogits, const void *X, float
  *   u       [M,R] FP32, written (0 for a token without adapter); the backward
  *           calls take it.   logits as lmhead_fwd.
  *   One kernel forms both products in the same sums, FP32 rounded to nearest
- *   every 512 terms of K, so the base part is as lmhead_fwd's but with a smaller
- *   error and not bitwise equal to it.  u enters the second product as two BF16
- *   parts (2^-18 of u).  An adapter's values reach the tokens that use it and no
+ *   every 768 terms of K (4096 for BF16 logits), so the base part is as
+ *   lmhead_fwd's but with a smaller error and not bitwise equal to it.  Above 128
+ *   tokens u enters the second product as two BF16 parts (2^-18 of u).  An adapter's values reach the tokens that use it and no
  *   others, infinities and NaN included.  Any order of the tokens; those of one
  *   adapter next to each other cost least (each 256-token tile reads the
  *   adapters that occur in it).
  *   workspace: device scratch of lmhead_lora_workspace_bytes(M, K, V, R, N)
  *   bytes, 256-byte aligned; its contents do not matter before or after.
  *   Requirements: K % 8 == 0, R % 8 == 0, R <= 256, N <= 65535, M <= 4194240;
- *   X, W, A, B 16-byte aligned; logits aligned to its element.  Deterministic. */
+ *   X, W, A, B, u 16-byte aligned; logits aligned to its element.
+ *   Deterministic. */
 LMH_API lmh_status_t lmhead_fwd_lora(const void *X, const void *W, const void *A, const void *B,
                                      const float *scale, const int32_t *adapter, float *u,
                                      void *logits, int32_t out_dtype, void *workspace,
@@ -297,7 +298,7 @@ LMH_API int64_t lmhead_lora_workspace_bytes(int64_t M, int64_t K, int64_t V, int
  *   g[i,:]  = scale[a] dlogits[i,:] . B_a          (written, [M,R] FP32)
  *   dX[i,:] = dlogits[i,:] . W + g[i,:] . A_a      (FP32 or BF16)
  * summed as in lmhead_fwd_lora.  Requirements as there, and V % 8 == 0,
- * dlogits and dX 16-byte aligned.  Deterministic. */
+ * dlogits, g and dX 16-byte aligned.  Deterministic. */
 LMH_API lmh_status_t lmhead_bwd_dx_lora(const void *dlogits, const void *W, const void *A,
                                         const void *B, const float *scale, const int32_t *adapter,
                                         float *g, void *dX, int32_t out_dtype, void *workspace,

@@ -36,16 +36,28 @@ int pick_bn(int64_t M, int least) { return M <= least ? least : M <= 32 ? 32 : M
 // Ranges the columns of a row kernel are cut into: enough CTAs to fill the GPU,
 // and no more, since each range writes a partial result.
 struct RowRanges {
-    int64_t subs, ranges;
+    int64_t subs, ranges, groups;
 };
-RowRanges row_ranges(int64_t M, int64_t Cdim, int64_t R)
+RowRanges row_ranges(int64_t M, int64_t Cdim, int64_t R, int64_t N)
 {
     const int64_t nsub = ceil_div(Cdim, lmh::kRowsSub);
     const int64_t base = ceil_div(M, lmh::kRowsTokens) * ceil_div(R, lmh::kRankBlock);
     int64_t want = kRowsCtas / base;
     want = want < 1 ? 1 : want > nsub ? nsub : want;
     const int64_t subs = ceil_div(nsub, want);
-    return {subs, ceil_div(nsub, subs)};
+    const int64_t ranges = ceil_div(nsub, subs);
+    // CTAs still to spare: the adapters of a tile are dealt out to several
+    const int64_t most = N < M ? (N < lmh::kRowsTokens ? N : lmh::kRowsTokens) : (M < lmh::kRowsTokens ? M : lmh::kRowsTokens);
+    int64_t groups = kRowsCtas / (base * ranges);
+    groups = groups < 1 ? 1 : groups > most ? most : groups;
+    return {subs, ranges, groups};
+}
+
+// Whether the row kernel takes the tokens adapter by adapter: where the matrix it
+// reads is large and the tokens are more than one tile.
+bool rows_sorted(int64_t M, int64_t Cdim, int64_t N)
+{
+    return M > lmh::kRowsTokens && N > 1 && M * Cdim >= (int64_t{1} << 25);
 }
 
 int64_t rank_pad(int64_t R) { return (R + 15) / 16 * 16; }
@@ -53,7 +65,7 @@ int64_t rank_pad(int64_t R) { return (R + 15) / 16 * 16; }
 // Byte offsets in the workspace of lmhead_fwd_lora (Cdim = K) and
 // lmhead_bwd_dx_lora (Cdim = V).
 struct GemmSpace {
-    int64_t partial, ux, nslots, slot_id, slot_mask, bytes;
+    int64_t partial, ux, nslots, slot_id, slot_mask, start, order, bytes;
     int64_t tiles, stages, max_slots, slot_stride;
 };
 GemmSpace gemm_space(int64_t M, int64_t Cdim, int64_t R, int64_t N, int bn)
@@ -64,11 +76,13 @@ GemmSpace gemm_space(int64_t M, int64_t Cdim, int64_t R, int64_t N, int bn)
     g.max_slots = N < bn ? N : bn;
     g.slot_stride = (g.max_slots + 3) / 4 * 4;
     g.partial = 0;
-    g.ux = align256(row_ranges(M, Cdim, R).ranges * M * rank_pad(R) * 4);
+    g.ux = align256(row_ranges(M, Cdim, R, N).ranges * M * rank_pad(R) * 4);
     g.nslots = g.ux + align256(g.tiles * g.stages * bn * 128);
     g.slot_id = g.nslots + align256(g.tiles * 4);
     g.slot_mask = g.slot_id + align256(g.tiles * g.slot_stride * 4);
-    g.bytes = g.slot_mask + align256(g.tiles * g.max_slots * lmh::kSlotMaskWords * 4);
+    g.start = g.slot_mask + align256(g.tiles * g.max_slots * lmh::kSlotMaskWords * 4);
+    g.order = g.start + align256((N + 1) * 4);
+    g.bytes = g.order + align256(M * 4);
     return g;
 }
 
@@ -162,9 +176,12 @@ lmh_status_t launch_lora(const void *a, uint64_t a_inner, uint64_t a_outer, cons
     using C = GemmCfg<BN, A_MN, false, PAIR, RES, lmh::lora_epi_warps(BN)>;
     CUtensorMap ta, tb, tc, ts, tu;
     if (!make_map(&ta, a, a_inner, a_outer, 64, A_MN ? lmh::kBlockK : lmh::kBlockM) ||
-        !make_map(&tb, b, static_cast<uint64_t>(p.Kdim), static_cast<uint64_t>(p.Ndim), lmh::kBlockK, C::BN_CTA) ||
-        !make_map3(&ts, ad.base, ad.inner, ad.mid, ad.N, A_MN ? lmh::kBlockK : lmh::kBlockM) ||
-        !make_map(&tu, ad.ux, 64, ad.ux_rows, 64, C::BN_CTA))
+        !make_map(&tb, b, static_cast<uint64_t>(p.Kdim), static_cast<uint64_t>(p.Ndim), lmh::kBlockK, C::BN_CTA))
+        return LMH_ERR_CUDA;
+    std::memset(&ts, 0, sizeof ts);
+    std::memset(&tu, 0, sizeof tu);
+    if (BN > 128 && (!make_map3(&ts, ad.base, ad.inner, ad.mid, ad.N, A_MN ? lmh::kBlockK : lmh::kBlockM) ||
+                     !make_map(&tu, ad.ux, 64, ad.ux_rows, 64, C::BN_CTA)))
         return LMH_ERR_CUDA;
     if (make_out_map(&tc, p.out, sizeof(OutT) == 2, static_cast<uint64_t>(p.Mdim), static_cast<uint64_t>(p.Ndim),
                      static_cast<uint64_t>(p.ldo), C::EPI_CHUNK))
@@ -177,7 +194,8 @@ lmh_status_t launch_lora(const void *a, uint64_t a_inner, uint64_t a_outer, cons
 
 template <bool P_MN, int NT>
 lmh_status_t launch_rows(const void *Y, const void *P, const int32_t *adapter, float *partial, int64_t M, int64_t Cdim,
-                         int64_t R, int64_t N, const RowRanges &rr, cudaStream_t s)
+                         int64_t R, int64_t N, const RowRanges &rr, const int32_t *order, const int32_t *total,
+                         cudaStream_t s)
 {
     using G = lmh::RowsCfg<P_MN, NT>;
     auto kern = lmh::lora_rows_kernel<P_MN, NT>;
@@ -186,10 +204,11 @@ lmh_status_t launch_rows(const void *Y, const void *P, const int32_t *adapter, f
         return r;
     return launch_ex(kern,
                      dim3(static_cast<unsigned>(rr.ranges), static_cast<unsigned>(ceil_div(M, lmh::kRowsTokens)),
-                          static_cast<unsigned>(ceil_div(R, lmh::kRankBlock))),
+                          static_cast<unsigned>(ceil_div(R, lmh::kRankBlock) * rr.groups)),
                      dim3(lmh::kRowsThreads), G::SMEM, s, 1u, static_cast<const __nv_bfloat16 *>(Y),
                      static_cast<const __nv_bfloat16 *>(P), adapter, partial, M, Cdim, static_cast<int32_t>(R),
-                     static_cast<int32_t>(rank_pad(R)), static_cast<int32_t>(N), static_cast<int32_t>(rr.subs));
+                     static_cast<int32_t>(rank_pad(R)), static_cast<int32_t>(N), static_cast<int32_t>(rr.subs),
+                     static_cast<int32_t>(rr.groups), order, total);
 }
 
 // t = s Y P_a over Cdim, its split and the slots of the token tiles, into the
@@ -199,15 +218,25 @@ lmh_status_t run_rows(const void *Y, const void *P, const float *scale, const in
                       uint8_t *ws, const GemmSpace &g, int bn, int64_t M, int64_t Cdim, int64_t R, int64_t N,
                       int32_t *status, cudaStream_t s)
 {
-    const RowRanges rr = row_ranges(M, Cdim, R);
+    const RowRanges rr = row_ranges(M, Cdim, R, N);
     float *partial = reinterpret_cast<float *>(ws + g.partial);
+    int32_t *order = nullptr, *total = nullptr;
+    lmh_status_t r = LMH_OK;
+    if (rows_sorted(M, Cdim, N)) {
+        int32_t *start = reinterpret_cast<int32_t *>(ws + g.start);
+        order = reinterpret_cast<int32_t *>(ws + g.order);
+        total = start + N;
+        r = launch_ex(lmh::lora_group_kernel, dim3(static_cast<unsigned>(N)), dim3(1024), 0, s, 1u, adapter, start,
+                      order, M, static_cast<int32_t>(N), static_cast<int32_t *>(nullptr));
+        if (r != LMH_OK)
+            return r;
+    }
     const int64_t nt = R > 48 ? 4 : rank_pad(R) / 16;
-    lmh_status_t r;
     switch (nt) {
-    case 1: r = launch_rows<P_MN, 1>(Y, P, adapter, partial, M, Cdim, R, N, rr, s); break;
-    case 2: r = launch_rows<P_MN, 2>(Y, P, adapter, partial, M, Cdim, R, N, rr, s); break;
-    case 3: r = launch_rows<P_MN, 3>(Y, P, adapter, partial, M, Cdim, R, N, rr, s); break;
-    default: r = launch_rows<P_MN, 4>(Y, P, adapter, partial, M, Cdim, R, N, rr, s); break;
+    case 1: r = launch_rows<P_MN, 1>(Y, P, adapter, partial, M, Cdim, R, N, rr, order, total, s); break;
+    case 2: r = launch_rows<P_MN, 2>(Y, P, adapter, partial, M, Cdim, R, N, rr, order, total, s); break;
+    case 3: r = launch_rows<P_MN, 3>(Y, P, adapter, partial, M, Cdim, R, N, rr, order, total, s); break;
+    default: r = launch_rows<P_MN, 4>(Y, P, adapter, partial, M, Cdim, R, N, rr, order, total, s); break;
     }
     if (r != LMH_OK)
         return r;
@@ -215,16 +244,19 @@ lmh_status_t run_rows(const void *Y, const void *P, const float *scale, const in
                      dim3(static_cast<unsigned>(g.tiles), static_cast<unsigned>(ceil_div(bn, lmh::kExpandTokens))),
                      dim3(256), lmh::kExpandTokens * rank_pad(R) * sizeof(float), s, 1u,
                      static_cast<const float *>(partial), static_cast<int32_t>(rr.ranges), adapter, scale, t_out,
-                     reinterpret_cast<__nv_bfloat16 *>(ws + g.ux), reinterpret_cast<int32_t *>(ws + g.nslots),
+                     bn > 128 ? reinterpret_cast<__nv_bfloat16 *>(ws + g.ux) : nullptr,
+                     reinterpret_cast<int32_t *>(ws + g.nslots),
                      reinterpret_cast<int32_t *>(ws + g.slot_id), reinterpret_cast<uint32_t *>(ws + g.slot_mask),
                      static_cast<int32_t>(bn), static_cast<int32_t>(g.slot_stride), static_cast<int32_t>(g.max_slots),
                      static_cast<int32_t>(g.stages), M, static_cast<int32_t>(R), static_cast<int32_t>(rank_pad(R)),
                      static_cast<int32_t>(N), status);
 }
 
-LoraParams lora_params(uint8_t *ws, const GemmSpace &g, int64_t R)
+LoraParams lora_params(uint8_t *ws, const GemmSpace &g, int64_t R, const void *adapters, const float *t)
 {
     LoraParams q{};
+    q.adapters = static_cast<const __nv_bfloat16 *>(adapters);
+    q.t = t;
     q.nslots = reinterpret_cast<const int32_t *>(ws + g.nslots);
     q.slot_id = reinterpret_cast<const int32_t *>(ws + g.slot_id);
     q.slot_mask = reinterpret_cast<const uint32_t *>(ws + g.slot_mask);
@@ -317,7 +349,7 @@ lmh_status_t lmhead_fwd_lora(const void *X, const void *W, const void *A, const 
     if (bad_dtype(out_dtype))
         return LMH_ERR_UNSUPPORTED;
     if (K % 8 || R % 8 || !aligned(X, 16) || !aligned(W, 16) || !aligned(A, 16) || !aligned(B, 16) ||
-        !aligned(scale, 4) || !aligned(adapter, 4) || !aligned(u, 4) || !aligned(workspace, 256) ||
+        !aligned(scale, 4) || !aligned(adapter, 4) || !aligned(u, 16) || !aligned(workspace, 256) ||
         !aligned(logits, out_dtype == LMH_F32 ? 4 : 2))
         return LMH_ERR_MISALIGNED;
     const int bn = pick_bn(M, 16);
@@ -342,7 +374,7 @@ lmh_status_t lmhead_fwd_lora(const void *X, const void *W, const void *A, const 
     p.status = status;
     const AdapterOperands ad{B, static_cast<uint64_t>(R), static_cast<uint64_t>(V), static_cast<uint64_t>(N),
                              ws + g.ux, static_cast<uint64_t>(g.tiles * g.stages * bn)};
-    const LoraParams q = lora_params(ws, g, R);
+    const LoraParams q = lora_params(ws, g, R, B, u);
     const bool pair = V >= 256;
     const uint64_t k = static_cast<uint64_t>(K), v = static_cast<uint64_t>(V);
     return out_dtype == LMH_F32 ? dispatch_fwd<float>(bn, pair, W, k, v, X, ad, p, q, s)
@@ -360,7 +392,7 @@ lmh_status_t lmhead_bwd_dx_lora(const void *dlogits, const void *W, const void *
     if (bad_dtype(out_dtype))
         return LMH_ERR_UNSUPPORTED;
     if (K % 8 || V % 8 || R % 8 || !aligned(dlogits, 16) || !aligned(W, 16) || !aligned(A, 16) || !aligned(B, 16) ||
-        !aligned(scale, 4) || !aligned(adapter, 4) || !aligned(g_out, 4) || !aligned(dX, 16) ||
+        !aligned(scale, 4) || !aligned(adapter, 4) || !aligned(g_out, 16) || !aligned(dX, 16) ||
         !aligned(workspace, 256))
         return LMH_ERR_MISALIGNED;
     const int bn = pick_bn(M, 64);
@@ -384,7 +416,7 @@ lmh_status_t lmhead_bwd_dx_lora(const void *dlogits, const void *W, const void *
     p.status = status;
     const AdapterOperands ad{A, static_cast<uint64_t>(K), static_cast<uint64_t>(R), static_cast<uint64_t>(N),
                              ws + g.ux, static_cast<uint64_t>(g.tiles * g.stages * bn)};
-    const LoraParams q = lora_params(ws, g, R);
+    const LoraParams q = lora_params(ws, g, R, A, g_out);
     const bool pair = K >= 256;
     const uint64_t k = static_cast<uint64_t>(K), v = static_cast<uint64_t>(V);
     return out_dtype == LMH_F32 ? dispatch_dx<float>(bn, pair, W, k, v, dlogits, ad, p, q, s)

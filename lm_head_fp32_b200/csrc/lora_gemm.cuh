@@ -17,10 +17,16 @@
 //
 // The sum over the reduction is kept in FP32 as FP32 should be: the tensor
 // cores' own accumulation loses about 2^-24 of the running sum at each MMA,
-// always towards zero, which grows with the length (4e-6 relative at K = 4096,
-// 1e-4 at K = 128256).  Here a tensor-memory accumulator takes kPromote k-blocks
-// and the epilogue warps add it, rounded to nearest, to sums they hold in
+// always towards zero, which grows with the length.  Here a tensor-memory
+// accumulator takes promote_kblocks k-blocks and the epilogue warps add it, rounded to nearest, to sums they hold in
 // registers, while the MMAs fill the other accumulator.
+//
+// Up to 128 tokens (one token tile, bound by the read of W) there is time to spare
+// on the epilogue warps and none in the handing over of accumulators, each about
+// 1 us: there the warps add u B_a themselves, FP32 on the CUDA cores, to the sums
+// they hold, out of the adapter's rows fetched ahead with cp.async, while the
+// shared product is under way (64 tokens with 28 adapters of rank 16, V = 128256:
+// see lora.cu).
 //
 // Roles, ring, tile order, TMA epilogue and the unwinding after a timeout are
 // those of gemm_tc.cuh.
@@ -29,7 +35,13 @@
 
 namespace lmh {
 
-constexpr int kPromote = 8;  // k-blocks (512 of the reduction) per tensor-memory accumulation
+// k-blocks of 64 per tensor-memory accumulation.  FP32 outputs: 12 (768 terms)
+// keep the error of a product at 7.1e-7 of its norm at any length (8: 4.7e-7,
+// 16: 1.0e-6, one accumulation of 4096 terms: 4.4e-6, of 32768: 3.8e-5; an FP32
+// product on the CUDA cores: 6.1e-7 at 4096).  A switch of accumulators costs the
+// tensor pipe about 0.2 us: 4096 x 4096 x 128256 takes 3163, 3101, 3043 us with 8,
+// 12, 16 and 2966 without.  BF16 outputs round at 2e-3, so 64 (4e-6) do.
+__host__ __device__ constexpr int promote_kblocks(int out_bytes) { return out_bytes == 4 ? 12 : 64; }
 
 constexpr int kSlotMaskWords = 8;  // one bit per token of a tile of up to 256
 
@@ -41,6 +53,8 @@ struct LoraParams {
     int32_t max_slots;
     int32_t stages_per_slot;   // ring stages of one slot: 1 up to 32 ranks, then 2 per 64
     int32_t rank;
+    const __nv_bfloat16 *adapters;  // [adapter][Mdim][rank], A_MN: [adapter][rank][Mdim]
+    const float *t;                 // u (g): [Ndim][rank]
 };
 
 // Epilogue warps: sums of a whole tile stay in their registers, 128 per thread
@@ -55,6 +69,9 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
 {
     using C = GemmCfg<BN, A_MN, false, PAIR, RES, EW>;
     constexpr int S = C::STAGES;
+    // the epilogue warps form the adapters' term; otherwise the tensor cores
+    constexpr bool IN_REGS = BN <= 128;
+    constexpr int kPromote = promote_kblocks(sizeof(OutT));
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -94,8 +111,10 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
         fence_mbar_init();
         tma_prefetch_desc(&tmA);
         tma_prefetch_desc(&tmB);
-        tma_prefetch_desc(&tmS);
-        tma_prefetch_desc(&tmU);
+        if (!IN_REGS) {
+            tma_prefetch_desc(&tmS);
+            tma_prefetch_desc(&tmU);
+        }
         if (TMA_STORE)
             tma_prefetch_desc(&tmC);
     }
@@ -112,7 +131,9 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
         __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    pdl_wait();
+    // X, W and dlogits were complete before the row kernel of this call began, and
+    // this kernel starts once the expand kernel after it has: only what those two
+    // write (u, the slots) has to be waited for, by each role that reads it.
     pdl_launch_dependents();
 
     const uint64_t pol_a = policy_of(p.l2_a);
@@ -173,12 +194,12 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
             uint32_t stage = 0, phase = 0;
             uint32_t issued = 0;
             bool ok = true;
+            bool slots_there = false;
             for (int t = unit; t < num_tiles && ok; t += num_units) {
                 int mt, nt;
                 tile_coords(t, p, mt, nt);
                 const int m0 = mt * C::TILE_M + static_cast<int>(rank) * kBlockM;
                 const int nb0 = nt * BN + static_cast<int>(rank) * C::BN_CTA;
-                const int ns = q.nslots[nt];
                 for (int kb = 0; kb < num_kb; ++kb) {
                     if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.wait_limit_ns)) {
                         ok = false;
@@ -191,6 +212,12 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
                         phase ^= 1;
                     }
                 }
+                if (IN_REGS)
+                    continue;
+                if (!slots_there)
+                    pdl_wait();
+                slots_there = true;
+                const int ns = q.nslots[nt];
                 const int4 *ids = reinterpret_cast<const int4 *>(q.slot_id + static_cast<int64_t>(nt) * q.slot_stride);
                 for (int s4 = 0; s4 < ns && ok; s4 += 4) {
                     const int4 four = ids[s4 >> 2];
@@ -222,80 +249,115 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
             uint32_t stage = 0, phase = 0;
             uint32_t acc = 0, acc_phase = 0;
             bool ok = true;
+            bool slots_there = false;
+            // a stage whose copies have landed, its descriptors' bases
+            uint32_t sa = 0, sb = 0, d_tmem = 0;
+            auto mma = [&](int ka, int kbb, uint32_t accumulate) {
+                // K-major: 32 bytes along the swizzled row per 16 of the
+                // reduction.  MN-major: 16 rows of 128 bytes.
+                const uint64_t da = A_MN ? smem_desc_sw128(sa + ka * 2048, 64 * kBlockK * 2, 1024)
+                                         : smem_desc_sw128(sa + ka * 32, 16, 1024);
+                const uint64_t db = smem_desc_sw128(sb + kbb * 32, 16, 1024);
+                if (PAIR)
+                    mma_bf16_pair(d_tmem, da, db, C::IDESC, accumulate);
+                else
+                    mma_bf16(d_tmem, da, db, C::IDESC, accumulate);
+            };
+            auto begin_acc = [&]() -> bool {
+                if (!mbar_wait(&acc_empty[acc], acc_phase ^ 1, abort_flag, p.wait_limit_ns))
+                    return false;
+                tc_fence_after();
+                d_tmem = tmem_base + acc * BN;
+                return true;
+            };
+            auto end_acc = [&]() {
+                if (PAIR)
+                    mma_commit_pair(&acc_full[acc], 0x3);
+                else
+                    mma_commit(&acc_full[acc]);
+                if (++acc == 2) {
+                    acc = 0;
+                    acc_phase ^= 1;
+                }
+            };
+            auto begin_stage = [&]() -> bool {
+                if (!mbar_wait(&full[stage], phase, abort_flag, p.wait_limit_ns))
+                    return false;
+                tc_fence_after();
+                sa = smem_u32(tiles + stage * C::STAGE_BYTES);
+                sb = sa + C::A_BYTES;
+                return true;
+            };
+            auto end_stage = [&]() {
+                // frees the smem slot (of both CTAs) when these MMAs finish
+                if (PAIR)
+                    mma_commit_pair(&empty[stage], 0x3);
+                else
+                    mma_commit(&empty[stage]);
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            };
             for (int t = unit; t < num_tiles && ok; t += num_units) {
                 int mt, nt;
                 tile_coords(t, p, mt, nt);
-                const int total = num_kb + q.nslots[nt] * sps;
-                int in_chunk = 0;  // k-blocks in the current accumulator
-                for (int kb = 0; kb < total; ++kb) {
-                    if (in_chunk == 0) {
-                        if (!mbar_wait(&acc_empty[acc], acc_phase ^ 1, abort_flag, p.wait_limit_ns)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                    }
-                    const uint32_t d_tmem = tmem_base + acc * BN;
-                    if (!mbar_wait(&full[stage], phase, abort_flag, p.wait_limit_ns)) {
+                int ns = slots_there && !IN_REGS ? q.nslots[nt] : 0;  // wanted after the shared product
+                for (int kb0 = 0; kb0 < num_kb && ok; kb0 += kPromote) {
+                    if (!begin_acc()) {
                         ok = false;
                         break;
                     }
-                    tc_fence_after();
-                    const uint32_t sa = smem_u32(tiles + stage * C::STAGE_BYTES);
-                    const uint32_t sb = sa + C::A_BYTES;
-                    auto mma = [&](int ka, int kbb, uint32_t accumulate) {
-                        // K-major: 32 bytes along the swizzled row per 16 of the
-                        // reduction.  MN-major: 16 rows of 128 bytes.
-                        const uint64_t da = A_MN ? smem_desc_sw128(sa + ka * 2048, 64 * kBlockK * 2, 1024)
-                                                 : smem_desc_sw128(sa + ka * 32, 16, 1024);
-                        const uint64_t db = smem_desc_sw128(sb + kbb * 32, 16, 1024);
-                        if (PAIR)
-                            mma_bf16_pair(d_tmem, da, db, C::IDESC, accumulate);
-                        else
-                            mma_bf16(d_tmem, da, db, C::IDESC, accumulate);
-                    };
-                    if (kb < num_kb) {
+                    const int kb1 = min(num_kb, kb0 + kPromote);
+                    for (int kb = kb0; kb < kb1; ++kb) {
+                        if (!begin_stage()) {
+                            ok = false;
+                            break;
+                        }
 #pragma unroll
                         for (int k = 0; k < kBlockK / kUmmaK; ++k)
-                            mma(k, k, (in_chunk != 0 || k != 0) ? 1u : 0u);
-                    } else if (sps == 1) {
-                        // up to 32 ranks: columns 0..31 of u are its high parts,
-                        // 32..63 the low ones, against the same ranks of B_a
-                        mma(0, 0, 0u);
-                        mma(0, 2, 1u);
-                        if (q.rank > 16) {
-                            mma(1, 1, 1u);
-                            mma(1, 3, 1u);
+                            mma(k, k, (kb != kb0 || k != 0) ? 1u : 0u);
+                        end_stage();
+                    }
+                    if (ok)
+                        end_acc();
+                }
+                if (!IN_REGS && !slots_there) {
+                    pdl_wait();
+                    slots_there = true;
+                    ns = q.nslots[nt];
+                }
+#pragma unroll 1
+                for (int s = 0; s < ns && ok; ++s) {
+                    if (!begin_acc()) {
+                        ok = false;
+                        break;
+                    }
+#pragma unroll 1
+                    for (int j = 0; j < sps; ++j) {
+                        if (!begin_stage()) {
+                            ok = false;
+                            break;
                         }
-                    } else {
-                        // 64 ranks: the high parts, then the low ones
-                        const int r0 = (in_chunk >> 1) * 64;
-                        const int steps = min(4, (q.rank - r0 + kUmmaK - 1) / kUmmaK);
-                        for (int k = 0; k < steps; ++k)
-                            mma(k, k, (in_chunk != 0 || k != 0) ? 1u : 0u);
-                    }
-                    if (PAIR)
-                        mma_commit_pair(&empty[stage], 0x3);
-                    else
-                        mma_commit(&empty[stage]);
-                    if (++stage == S) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
-                    ++in_chunk;
-                    // an accumulator is full after kPromote k-blocks, at the end
-                    // of the shared product, and at the end of each slot
-                    if (kb < num_kb ? (in_chunk == kPromote || kb == num_kb - 1) : in_chunk == sps) {
-                        in_chunk = 0;
-                        if (PAIR)
-                            mma_commit_pair(&acc_full[acc], 0x3);
-                        else
-                            mma_commit(&acc_full[acc]);
-                        if (++acc == 2) {
-                            acc = 0;
-                            acc_phase ^= 1;
+                        if (sps == 1) {
+                            // up to 32 ranks: columns 0..31 of u are its high parts,
+                            // 32..63 the low ones, against the same ranks of B_a
+                            mma(0, 0, 0u);
+                            mma(0, 2, 1u);
+                            if (q.rank > 16) {
+                                mma(1, 1, 1u);
+                                mma(1, 3, 1u);
+                            }
+                        } else {
+                            // 64 ranks: the high parts, then the low ones
+                            const int steps = min(4, (q.rank - (j >> 1) * 64 + kUmmaK - 1) / kUmmaK);
+                            for (int k = 0; k < steps; ++k)
+                                mma(k, k, (j != 0 || k != 0) ? 1u : 0u);
                         }
+                        end_stage();
                     }
+                    if (ok)
+                        end_acc();
                 }
             }
             // wait until every MMA issued by this thread has completed
@@ -320,11 +382,16 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
         const uint32_t empty_addr0 = PAIR ? mapa_shared(smem_u32(&acc_empty[0]), 0) : 0u;
         uint32_t acc = 0, acc_phase = 0;
         bool ok = true;
+        pdl_wait();
         for (int t = unit; t < num_tiles && ok; t += num_units) {
             int mt, nt;
             tile_coords(t, p, mt, nt);
+            const int mbase = mt * C::TILE_M + static_cast<int>(rank) * kBlockM;
+            const int m = mbase + quarter * 32 + lane;
+            const int n0 = nt * BN + half * COLS;
             const int chunks = (num_kb + kPromote - 1) / kPromote;
-            const int all = chunks + q.nslots[nt];
+            const int ns = q.nslots[nt];
+            const int all = IN_REGS ? chunks : chunks + ns;
             // this warp's columns of the tile's slot masks, one slot ahead
             const uint32_t *masks = q.slot_mask + static_cast<int64_t>(nt) * q.max_slots * kSlotMaskWords +
                                     half * COLS / 32;
@@ -337,9 +404,98 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
 #pragma unroll
             for (int i = 0; i < COLS; ++i)
                 sum[i] = 0.f;
+            if constexpr (IN_REGS) {
+                // Step (slot, 8 ranks): this lane's row of the adapter, 16 bytes,
+                // through its own place in the staging slots (free until the
+                // tile's stores), AHEAD steps before it is used.
+                constexpr int AHEAD = C::NSLOT * C::EPI_SLOT_BYTES / 512 < 8 ? C::NSLOT * C::EPI_SLOT_BYTES / 512 : 8;
+                uint4 *ring = reinterpret_cast<uint4 *>(slots);
+                const int32_t *ids = q.slot_id + static_cast<int64_t>(nt) * q.slot_stride;
+                const int per_slot = q.rank / 8;
+                const int steps = ns * per_slot;
+                const bool in = m < p.Mdim;
+                int fs = 0, fr = 0;  // slot and rank block of the next fetch
+                if (lane == 0)
+                    bulk_wait_read<0>();  // the last tile's stores have left the slots
+                __syncwarp();
+                auto fetch = [&](int step) {
+                    if (step < steps) {
+                        if constexpr (!A_MN) {
+                            const __nv_bfloat16 *src =
+                                q.adapters + (static_cast<int64_t>(ids[fs]) * p.Mdim + (in ? m : 0)) * q.rank + fr * 8;
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                             smem_u32(ring + (step % AHEAD) * 32 + lane)),
+                                         "l"(src), "r"(in ? 16 : 0)
+                                         : "memory");
+                        }
+                        if (++fr == per_slot) {
+                            fr = 0;
+                            ++fs;
+                        }
+                    }
+                    asm volatile("cp.async.commit_group;" ::: "memory");
+                };
+                if constexpr (!A_MN)
+                    for (int i = 0; i < AHEAD - 1; ++i)
+                        fetch(i);
+                int cs = 0, cr = 0;
+#pragma unroll 1
+                for (int step = 0; step < steps; ++step) {
+                    float b[8];
+                    if constexpr (!A_MN) {
+                        asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 2) : "memory");
+                        const uint4 v = ring[(step % AHEAD) * 32 + lane];
+                        fetch(step + AHEAD - 1);
+                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            b[2 * j] = __uint_as_float(w[j] << 16);
+                            b[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+                        }
+                    } else {
+                        const __nv_bfloat16 *src =
+                            q.adapters + (static_cast<int64_t>(ids[cs]) * q.rank + cr * 8) * p.Mdim + (in ? m : 0);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            b[j] = in ? __bfloat162float(src[static_cast<int64_t>(j) * p.Mdim]) : 0.f;
+                    }
+                    const float *trow = q.t + static_cast<int64_t>(n0) * q.rank + cr * 8;
+#pragma unroll
+                    for (int i = 0; i < MW; ++i)
+                        mask[i] = masks[cs * kSlotMaskWords + i];
+#pragma unroll
+                    for (int c0 = 0; c0 < COLS; c0 += 8) {
+                        if ((mask[c0 / 32] >> (c0 & 31) & 0xffu) == 0)
+                            continue;
+#pragma unroll
+                        for (int c = c0; c < c0 + 8; ++c) {
+                            if (mask[c / 32] >> (c & 31) & 1u) {
+                                const float4 *tp = reinterpret_cast<const float4 *>(trow + static_cast<int64_t>(c) * q.rank);
+                                const float4 x = tp[0], y = tp[1];
+                                float s = sum[c];
+                                s = fmaf(x.x, b[0], s);
+                                s = fmaf(x.y, b[1], s);
+                                s = fmaf(x.z, b[2], s);
+                                s = fmaf(x.w, b[3], s);
+                                s = fmaf(y.x, b[4], s);
+                                s = fmaf(y.y, b[5], s);
+                                s = fmaf(y.z, b[6], s);
+                                s = fmaf(y.w, b[7], s);
+                                sum[c] = s;
+                            }
+                        }
+                    }
+                    if (++cr == per_slot) {
+                        cr = 0;
+                        ++cs;
+                    }
+                }
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+                __syncwarp();
+            }
 #pragma unroll 1
             for (int ch = 0; ch < all; ++ch) {
-                const bool shared = ch < chunks;
+                const bool shared = IN_REGS || ch < chunks;
                 if (!shared) {
 #pragma unroll
                     for (int i = 0; i < MW; ++i) {
@@ -396,9 +552,6 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
             }
             if (!ok)
                 break;
-            const int mbase = mt * C::TILE_M + static_cast<int>(rank) * kBlockM;
-            const int m = mbase + quarter * 32 + lane;
-            const int n0 = nt * BN + half * COLS;
 #pragma unroll
             for (int c = 0; c < COLS; c += CH) {
                 if (TMA_STORE) {

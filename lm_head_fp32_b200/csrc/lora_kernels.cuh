@@ -92,44 +92,66 @@ struct RowsCfg {
 
 // partial[range][i][r]: the range's share of t.  Y [M][Cdim] BF16; P_MN: P
 // [adapter][Cdim][R] (B), else [adapter][R][Cdim] (A).  Rpad: R rounded up to 16.
+// grid (ranges of columns, tiles of tokens, rank blocks x slot groups).
+//   order (or NULL) gives the tokens adapter by adapter, total[0] of them: a tile
+//     then holds one or two adapters instead of as many as 64 tokens in any order
+//     have, each of which costs a read of its columns and a product.
+//   groups: a tile's adapters are dealt out to so many CTAs, each of which keeps
+//     the rows of its own (few tokens with many adapters: 20 us -> see below).
 template <bool P_MN, int NT>
 __global__ void __launch_bounds__(kRowsThreads)
     lora_rows_kernel(const __nv_bfloat16 *__restrict__ Y, const __nv_bfloat16 *__restrict__ P,
                      const int32_t *__restrict__ adapter, float *__restrict__ partial, int64_t M,
-                     int64_t Cdim, int32_t R, int32_t Rpad, int32_t N, int32_t subs_per_range)
+                     int64_t Cdim, int32_t R, int32_t Rpad, int32_t N, int32_t subs_per_range,
+                     int32_t groups, const int32_t *__restrict__ order, const int32_t *__restrict__ total)
 {
     using G = RowsCfg<P_MN, NT>;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ int32_t ids[kRowsTokens];
+    __shared__ int32_t toks[kRowsTokens];
     __shared__ int32_t list[kRowsTokens];
     __shared__ int warp_n[2];
     uint8_t *ybuf = smem, *pbuf = smem + 3 * G::Y_BYTES;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t i0 = static_cast<int64_t>(blockIdx.y) * kRowsTokens;
-    const int r0 = blockIdx.z * kRankBlock;
+    const int r0 = static_cast<int>(blockIdx.z) / groups * kRankBlock;
+    const int group = static_cast<int>(blockIdx.z) % groups;
     pdl_wait();
     pdl_launch_dependents();
     bool first = false;
     if (tid < kRowsTokens) {
-        int32_t a = i0 + tid < M ? adapter[i0 + tid] : -1;
+        const int64_t i = i0 + tid;
+        int32_t tok = -1;
+        if (order)
+            tok = i < *total ? order[i] : -1;
+        else if (i < M)
+            tok = static_cast<int32_t>(i);
+        const int32_t a = tok >= 0 ? adapter[tok] : -1;
         ids[tid] = a < 0 || a >= N ? -1 : a;
+        toks[tid] = tok;
     }
     __syncthreads();
     if (tid < kRowsTokens) {
         const int32_t a = ids[tid];
-        first = a >= 0;
-        for (int j = 0; j < tid && first; ++j)
-            first = ids[j] != a;
+        bool seen = false;
+#pragma unroll 16
+        for (int j = 0; j < kRowsTokens; ++j)
+            seen |= j < tid && ids[j] == a;
+        first = a >= 0 && !seen;
         const unsigned b = __ballot_sync(0xffffffffu, first);
         if (lane == 0)
             warp_n[warp] = __popc(b);
     }
     __syncthreads();
-    const int nslot = warp_n[0] + warp_n[1];
+    // this CTA's share of the tile's adapters: every groups-th from `group`
+    const int nslot = (warp_n[0] + warp_n[1] - group + groups - 1) / groups;
+    if (nslot <= 0)
+        return;
     if (tid < kRowsTokens) {
         const unsigned b = __ballot_sync(0xffffffffu, first);
-        if (first)
-            list[(warp ? warp_n[0] : 0) + __popc(b & ((1u << lane) - 1u))] = ids[tid];
+        const int slot = (warp ? warp_n[0] : 0) + __popc(b & ((1u << lane) - 1u));
+        if (first && slot % groups == group)
+            list[slot / groups] = ids[tid];
     }
     __syncthreads();
 
@@ -152,8 +174,9 @@ __global__ void __launch_bounds__(kRowsThreads)
                 uint8_t *y = ybuf + (sub % 3) * G::Y_BYTES;
                 for (int k = tid; k < kRowsTokens * (kRowsSub / 8); k += kRowsThreads) {
                     const int row = k / (kRowsSub / 8), ch = k % (kRowsSub / 8);
-                    const bool in = i0 + row < M && c0 + ch * 8 < Cdim;
-                    cp16(y + row * G::Y_ROW + ch * 16, in ? Y + (i0 + row) * Cdim + c0 + ch * 8 : Y, in);
+                    const bool in = toks[row] >= 0 && c0 + ch * 8 < Cdim;
+                    cp16(y + row * G::Y_ROW + ch * 16,
+                         in ? Y + static_cast<int64_t>(toks[row]) * Cdim + c0 + ch * 8 : Y, in);
                 }
             }
             uint8_t *pb = pbuf + (t % 3) * G::P_BYTES;
@@ -225,16 +248,22 @@ __global__ void __launch_bounds__(kRowsThreads)
         }
     }
     cp_wait<0>();
+    // rows of tokens without an adapter, and of other groups', are not this CTA's
+    bool own0 = false, own1 = false;
+    for (int j = 0; j < nslot; ++j) {
+        own0 |= id0 == list[j];
+        own1 |= id1 == list[j];
+    }
     float *out = partial + static_cast<int64_t>(blockIdx.x) * M * Rpad;
+    const int64_t ta = toks[warp * 16 + g], tb = toks[warp * 16 + g + 8];
 #pragma unroll
     for (int n = 0; n < 2 * NT; ++n) {
         const int r = r0 + n * 8 + (lane & 3) * 2;
         if (r < Rpad) {
-            const int64_t ia = i0 + warp * 16 + g;
-            if (ia < M)
-                *reinterpret_cast<float2 *>(out + ia * Rpad + r) = make_float2(acc[n][0], acc[n][1]);
-            if (ia + 8 < M)
-                *reinterpret_cast<float2 *>(out + (ia + 8) * Rpad + r) = make_float2(acc[n][2], acc[n][3]);
+            if (own0)
+                *reinterpret_cast<float2 *>(out + ta * Rpad + r) = make_float2(acc[n][0], acc[n][1]);
+            if (own1)
+                *reinterpret_cast<float2 *>(out + tb * Rpad + r) = make_float2(acc[n][2], acc[n][3]);
         }
     }
 }
@@ -250,7 +279,7 @@ __device__ __forceinline__ __nv_bfloat16 split_hi(float x, float &rest)
 
 // grid (token tiles of the GEMM, parts of kExpandTokens tokens).
 //   t    [M][R] FP32, scaled: u or g (0 for a token without adapter)
-//   ux   [tile][stages][bn][64] BF16: up to 32 ranks one stage {high 0..31, low
+//   ux   (or NULL) [tile][stages][bn][64] BF16: up to 32 ranks one stage {high 0..31, low
 //        0..31}, above that per 64 ranks a stage of high and one of low parts
 //   nslots, slot_id, slot_mask: see LoraParams (written by part 0)
 __global__ void __launch_bounds__(256)
@@ -303,7 +332,7 @@ __global__ void __launch_bounds__(256)
     __syncthreads();
     // the split parts of this CTA's tokens, eight columns per store
     const int per_token = stages * 8;
-    for (int k = tid; k < kExpandTokens * per_token; k += 256) {
+    for (int k = tid; ux && k < kExpandTokens * per_token; k += 256) {
         const int j = k / per_token, rest = k % per_token;
         const int st = rest >> 3, c0 = (rest & 7) * 8;
         const int tk = tok0 + j;
@@ -323,11 +352,33 @@ __global__ void __launch_bounds__(256)
     }
     if (blockIdx.y != 0)
         return;
-    // the tile's slots, in the order in which their adapters occur
+    // The tile's slots, in the order in which their adapters occur: a hash table
+    // of the ids, each with its first token and the bits of all its tokens.
+    constexpr int kBuckets = 512;
+    __shared__ int32_t key[kBuckets], lead[kBuckets];
+    __shared__ __align__(16) uint32_t bits[kBuckets][kSlotMaskWords];
+    for (int k = tid; k < kBuckets; k += 256) {
+        key[k] = -1;
+        lead[k] = 256;
+        *reinterpret_cast<uint4 *>(&bits[k][0]) = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4 *>(&bits[k][4]) = make_uint4(0, 0, 0, 0);
+    }
+    __syncthreads();
     const int32_t a = ids[tid];
-    bool first = a >= 0;
-    for (int j = 0; j < tid && first; ++j)
-        first = ids[j] != a;
+    uint32_t h = 0;
+    if (a >= 0) {
+        h = (static_cast<uint32_t>(a) * 2654435761u) >> 23;
+        while (true) {  // at most 256 of the 512 buckets are taken
+            const int32_t old = atomicCAS(&key[h], -1, a);
+            if (old == -1 || old == a)
+                break;
+            h = (h + 1) & (kBuckets - 1);
+        }
+        atomicMin(&lead[h], tid);
+        atomicOr(&bits[h][warp], 1u << lane);
+    }
+    __syncthreads();
+    const bool first = a >= 0 && lead[h] == tid;
     const unsigned b = __ballot_sync(0xffffffffu, first);
     if (lane == 0)
         warp_n[warp] = __popc(b);
@@ -342,13 +393,9 @@ __global__ void __launch_bounds__(256)
         nslots[tile] = all;
     if (first) {
         slot_id[tile * slot_stride + slot] = a;
-        uint32_t *m = slot_mask + (tile * max_slots + slot) * kSlotMaskWords;
-        for (int w = 0; w < kSlotMaskWords; ++w) {
-            uint32_t bits = 0;
-            for (int j = 0; j < 32; ++j)
-                bits |= static_cast<uint32_t>(ids[w * 32 + j] == a) << j;
-            m[w] = bits;
-        }
+        uint4 *m = reinterpret_cast<uint4 *>(slot_mask + (tile * max_slots + slot) * kSlotMaskWords);
+        m[0] = *reinterpret_cast<uint4 *>(&bits[h][0]);
+        m[1] = *reinterpret_cast<uint4 *>(&bits[h][4]);
     }
 }
 

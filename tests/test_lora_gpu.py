@@ -2,22 +2,23 @@
 
 Tolerances, per element, with S the sum of the absolute values of the terms:
 
-  GEMM sums: per 512 terms (32 MMAs) the tensor cores lose at most 2^-23 of the
-    running sum per MMA and about four such inside one, then the parts are
-    added in FP32: 2^-23 * (36 + terms / 1024) * S.
+  GEMM sums, FP32 output: per 768 terms (48 MMAs) the tensor cores lose at most
+    2^-23 of the running sum per MMA and about four such inside one, then the
+    parts are added in FP32: 2^-23 * (52 + terms / 1536) * S.  BF16 output: per
+    4096 terms (256 MMAs): 2^-23 * (260 + terms / 8192) * S.
   row sums (u, g): the same per 128 terms (8 MMAs), parts added in FP64 or FP32,
     one rounding: 2^-23 * (12 + terms / 256) * S.
-  u in the second product: two BF16 parts, 2^-17 of sum |u| |B|, beside u's own
-    tolerance carried through B.
+  u in the second product: two BF16 parts (up to 128 tokens none), 2^-17 of
+    sum |u| |B|, beside u's own tolerance carried through B.
   gradients dA, dB: 256 terms (3 x 16 MMAs) at a time: 2^-23 * (52 + tokens / 512) * S.
   BF16 outputs: half a BF16 step (2^-9 of the value's power of two, so at most
     2^-8 of the value) beside these.
 
 The norm of a whole FP32 product's error has a tighter bound, because the MMAs'
-losses in a random sum grow like its square root: over a chunk of 32 MMAs of 16
-terms they add to at most 2^-23 * (2/3) 32^1.5 * sqrt(16) of a term's size, the
-chunks add in squares, and the sum itself grows as sqrt(terms): 22 * 2^-23 =
-2.6e-6 whatever the length; 3e-6 with the FP32 additions.
+losses in a random sum grow like its square root: over a chunk of 48 MMAs of 16
+terms they add to at most 2^-23 * (2/3) 48^1.5 * sqrt(16) of a term's size, the
+chunks add in squares, and the sum itself grows as sqrt(terms): (2/3) 48 * 2^-23 =
+3.8e-6 whatever the length; 4e-6 with the FP32 additions.
 """
 import pytest
 import torch
@@ -53,6 +54,7 @@ def workspace(M, K, V, R, N):
 def fwd(X, W, A, B, scale, ids, dtype=torch.float32, status=None):
     (M, K), V, (N, R) = X.shape, W.shape[0], A.shape[:2]
     u, logits = guarded_empty((M, R)), guarded_empty((M, V), dtype)
+    u.fill_(7.0)
     lmhead.lmhead_fwd_lora(X, W, A, B, scale, ids, u, logits, workspace(M, K, V, R, N), status)
     torch.cuda.synchronize()
     return logits, u
@@ -66,20 +68,24 @@ def per_token(ids, N):
             yield a, at
 
 
-def ref_fwd(X, W, A, B, scale, ids):
+def gemm_eps(terms, dtype=torch.float32):
+    return E23 * (52 + terms / 1536 if dtype == torch.float32 else 260 + terms / 8192)
+
+
+def ref_fwd(X, W, A, B, scale, ids, dtype=torch.float32):
     """(u, its tolerance, logits, their tolerance) in FP64."""
     X, W, A, B, scale = (t.double() for t in (X, W, A, B, scale))
     M, K = X.shape
     N, R = A.shape[:2]
     out = X @ W.T
-    tol = E23 * (36 + K / 1024) * (X.abs() @ W.abs().T)
+    tol = gemm_eps(K, dtype) * (X.abs() @ W.abs().T)
     u, tu = (torch.zeros((M, R), dtype=torch.float64, device=DEV) for _ in range(2))
     for a, at in per_token(ids, N):
         u[at] = scale[a] * (X[at] @ A[a].T)
         tu[at] = E23 * (12 + K / 256) * scale[a] * (X[at].abs() @ A[a].abs().T)
         ub = u[at].abs() @ B[a].abs().T
         out[at] += u[at] @ B[a].T
-        tol[at] += tu[at] @ B[a].abs().T + (2.0 ** -17 + E23 * 40) * ub
+        tol[at] += tu[at] @ B[a].abs().T + (2.0 ** -17 + E23 * 56) * ub
     return u, tu, out, tol
 
 
@@ -106,7 +112,7 @@ def test_forward(M, K, V, R, N, order, dtype):
     a = make(M, K, V, R, N, order=order)
     st = torch.zeros(1, dtype=torch.int32, device=DEV)
     logits, u = fwd(*a, dtype=dtype, status=st)
-    ru, tu, rl, tl = ref_fwd(*a)
+    ru, tu, rl, tl = ref_fwd(*a, dtype)
     close(u, ru, tu, "u")
     close(logits, rl, tl, "logits")
     assert int(st.item()) == 0
@@ -117,8 +123,8 @@ def test_forward_norm_of_the_error(M, K):
     a = make(M, K, 1024, 16, 4)
     logits, u = fwd(*a)
     ru, _, rl, _ = ref_fwd(*a)
-    assert float((logits.double() - rl).norm() / rl.norm()) < 3e-6
-    assert float((u.double() - ru).norm() / ru.norm()) < 3e-6
+    assert float((logits.double() - rl).norm() / rl.norm()) < 4e-6
+    assert float((u.double() - ru).norm() / ru.norm()) < 4e-6
 
 
 @pytest.mark.parametrize("M,K,V,R,N", [(1, 512, 300, 8, 1), (40, 1024, 515, 16, 5), (300, 2048, 1024, 32, 3),
@@ -185,7 +191,7 @@ def test_ids_out_of_range_and_none():
     st = torch.zeros(1, dtype=torch.int32, device=DEV)
     base, u = fwd(X, W, A, B, scale, ids, status=st)
     assert int(st.item()) == 0 and not u.any()
-    close(base, X.double() @ W.double().T, E23 * 40 * (X.double().abs() @ W.double().abs().T), "base")
+    close(base, X.double() @ W.double().T, gemm_eps(128) * (X.double().abs() @ W.double().abs().T), "base")
     ids[3], ids[69] = 3, -2
     got, u = fwd(X, W, A, B, scale, ids, status=st)
     assert int(st.item()) == lmhead.DEV_BAD_ADAPTER and torch.equal(got, base) and not u.any()
@@ -224,13 +230,13 @@ def check_bwd(M, K, V, R, N, order, dtype, seed=0):
     assert int(st.item()) == 0
     Xd, Wd, Ad, Bd, sd, dd, ud = (t.double() for t in (X, W, A, B, scale, dl, u))
     rg, tg = (torch.zeros((M, R), dtype=torch.float64, device=DEV) for _ in range(2))
-    rX, tX = dd @ Wd, E23 * (36 + V / 1024) * (dd.abs() @ Wd.abs())
+    rX, tX = dd @ Wd, gemm_eps(V, dtype) * (dd.abs() @ Wd.abs())
     for a in range(N):
         at = torch.nonzero(ids == a).view(-1)
         rg[at] = sd[a] * (dd[at] @ Bd[a])
         tg[at] = E23 * (12 + V / 256) * sd[a] * (dd[at].abs() @ Bd[a].abs())
         rX[at] += rg[at] @ Ad[a]
-        tX[at] += tg[at] @ Ad[a].abs() + (2.0 ** -17 + E23 * 40) * (rg[at].abs() @ Ad[a].abs())
+        tX[at] += tg[at] @ Ad[a].abs() + (2.0 ** -17 + E23 * 56) * (rg[at].abs() @ Ad[a].abs())
         c = E23 * (52 + at.numel() / 512)
         gf = g[at].double()  # as the call was given it
         close(dA[a], gf.T @ Xd[at], c * (gf.abs().T @ Xd[at].abs()), f"dA[{a}]")
@@ -246,6 +252,7 @@ def check_bwd(M, K, V, R, N, order, dtype, seed=0):
     (1, 64, 256, 8, 1), (3, 72, 136, 8, 2), (16, 512, 304, 24, 5), (33, 520, 1032, 32, 40),
     (64, 1024, 2048, 16, 64), (129, 264, 512, 16, 9), (300, 136, 256, 48, 300), (513, 512, 776, 128, 4),
     (260, 72, 1280, 256, 2), (1000, 320, 4096, 72, 6), (70, 128, 20000, 64, 3), (1100, 256, 1024, 16, 1),
+    (530, 64, 65536, 24, 7),  # the rows taken adapter by adapter
 ])
 def test_backward(M, K, V, R, N, order):
     check_bwd(M, K, V, R, N, order, torch.bfloat16 if M % 2 else torch.float32)
@@ -262,8 +269,8 @@ def test_backward_long_reduction_norm():
         at = torch.nonzero(ids == a).view(-1)
         rg[at] = scale[a].double() * (dl[at].double() @ B[a].double())
         rX[at] += rg[at] @ A[a].double()
-    assert float((dX.double() - rX).norm() / rX.norm()) < 3e-6
-    assert float((g.double() - rg).norm() / rg.norm()) < 3e-6
+    assert float((dX.double() - rX).norm() / rX.norm()) < 4e-6
+    assert float((g.double() - rg).norm() / rg.norm()) < 4e-6
 
 
 def test_backward_bad_values_stay_with_their_adapter():
