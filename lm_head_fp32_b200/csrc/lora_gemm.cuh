@@ -396,19 +396,46 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
             const uint32_t *masks = q.slot_mask + static_cast<int64_t>(nt) * q.max_slots * kSlotMaskWords +
                                     half * COLS / 32;
             constexpr int MW = COLS < 32 ? 1 : COLS / 32;
-            uint32_t mask[MW], ahead[MW];
-#pragma unroll
-            for (int i = 0; i < MW; ++i)
-                ahead[i] = all > chunks ? masks[i] : 0u;
             float sum[COLS];
 #pragma unroll
             for (int i = 0; i < COLS; ++i)
                 sum[i] = 0.f;
+            int ch = 0;
+            // adds the accumulator that has come full to the sums and frees it
+            auto take_shared = [&]() {
+                tc_fence_after();
+                const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * BN + half * COLS;
+#pragma unroll
+                for (int c = 0; c < COLS; c += 16) {
+                    uint32_t r[32];
+                    tmem_ld_chunk<16>(taddr + c, r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        sum[c + j] += __uint_as_float(r[j]);
+                }
+            };
+            auto release_acc = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (PAIR)
+                        mbar_arrive_cluster(empty_addr0 + acc * 8);
+                    else
+                        mbar_arrive(&acc_empty[acc]);
+                }
+                if (++acc == 2) {
+                    acc = 0;
+                    acc_phase ^= 1;
+                }
+                ++ch;
+            };
             if constexpr (IN_REGS) {
                 // Step (slot, 8 ranks): this lane's row of the adapter, 16 bytes,
                 // through its own place in the staging slots (free until the
                 // tile's stores), AHEAD steps before it is used.
-                constexpr int AHEAD = C::NSLOT * C::EPI_SLOT_BYTES / 512 < 8 ? C::NSLOT * C::EPI_SLOT_BYTES / 512 : 8;
+                constexpr int ROOM = C::NSLOT * C::EPI_SLOT_BYTES / 512;
+                constexpr int AHEAD = ROOM < 16 ? ROOM : 16;
                 uint4 *ring = reinterpret_cast<uint4 *>(slots);
                 const int32_t *ids = q.slot_id + static_cast<int64_t>(nt) * q.slot_stride;
                 const int per_slot = q.rank / 8;
@@ -441,6 +468,12 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
                 int cs = 0, cr = 0;
 #pragma unroll 1
                 for (int step = 0; step < steps; ++step) {
+                    // an accumulator that is full meanwhile is not kept waiting
+                    if (ch < chunks &&
+                        __all_sync(0xffffffffu, mbar_test_wait(smem_u32(&acc_full[acc]), acc_phase))) {
+                        take_shared();
+                        release_acc();
+                    }
                     float b[8];
                     if constexpr (!A_MN) {
                         asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 2) : "memory");
@@ -460,6 +493,7 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
                             b[j] = in ? __bfloat162float(src[static_cast<int64_t>(j) * p.Mdim]) : 0.f;
                     }
                     const float *trow = q.t + static_cast<int64_t>(n0) * q.rank + cr * 8;
+                    uint32_t mask[MW];
 #pragma unroll
                     for (int i = 0; i < MW; ++i)
                         mask[i] = masks[cs * kSlotMaskWords + i];
@@ -493,9 +527,14 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
                 asm volatile("cp.async.wait_group 0;" ::: "memory");
                 __syncwarp();
             }
+            uint32_t ahead[MW];
+#pragma unroll
+            for (int i = 0; i < MW; ++i)
+                ahead[i] = all > chunks ? masks[i] : 0u;
 #pragma unroll 1
-            for (int ch = 0; ch < all; ++ch) {
+            while (ch < all) {
                 const bool shared = IN_REGS || ch < chunks;
+                uint32_t mask[MW] = {};
                 if (!shared) {
 #pragma unroll
                     for (int i = 0; i < MW; ++i) {
@@ -510,19 +549,12 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
                     ok = false;
                     break;
                 }
-                tc_fence_after();
-                const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * BN + half * COLS;
                 if (shared) {
-#pragma unroll
-                    for (int c = 0; c < COLS; c += 16) {
-                        uint32_t r[32];
-                        tmem_ld_chunk<16>(taddr + c, r);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            sum[c + j] += __uint_as_float(r[j]);
-                    }
+                    take_shared();
                 } else {
+                    tc_fence_after();
+                    const uint32_t taddr =
+                        tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * BN + half * COLS;
 #pragma unroll
                     for (int c = 0; c < COLS; c += 16) {
                         const uint32_t m16 = (mask[c / 32] >> (c & 31)) & 0xffffu;
@@ -537,18 +569,7 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
                                 sum[c + j] += __uint_as_float(r[j]);
                     }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if (PAIR)
-                        mbar_arrive_cluster(empty_addr0 + acc * 8);
-                    else
-                        mbar_arrive(&acc_empty[acc]);
-                }
-                if (++acc == 2) {
-                    acc = 0;
-                    acc_phase ^= 1;
-                }
+                release_acc();
             }
             if (!ok)
                 break;

@@ -37,7 +37,7 @@ constexpr int kColsTokens = 32;    // tokens staged at once
 constexpr int kColsThreads = 128;
 constexpr int kColsStages = 4;
 constexpr int kColsPromote = 8;    // stages (256 tokens) summed in the MMAs
-constexpr int kExpandTokens = 16;  // tokens of one lora_expand_kernel CTA
+constexpr int kExpandTokens = 4;  // tokens of one lora_expand_kernel CTA
 constexpr int kDevBadAdapter = 0x8;  // LMH_DEV_BAD_ADAPTER
 
 // 16 bytes global -> shared; zeros where `in` is false (nothing is read then).
@@ -292,6 +292,7 @@ __global__ void __launch_bounds__(256)
 {
     __shared__ int32_t ids[256];
     __shared__ int32_t warp_n[8];
+    __shared__ double share[256];
     extern __shared__ float val[];  // [kExpandTokens][Rpad]
     pdl_wait();
     pdl_launch_dependents();
@@ -312,22 +313,37 @@ __global__ void __launch_bounds__(256)
     }
     __syncthreads();
 
-    for (int k = tid; k < kExpandTokens * Rpad; k += 256) {
+    // Sums over the ranges: `lanes` threads take every lanes-th range of an item
+    // (token, rank), and the first of them adds theirs in order.
+    const int items = kExpandTokens * Rpad;
+    const int lanes = items >= 256 ? 1 : 256 / items;
+    const int per_pass = 256 / lanes;
+    for (int k0 = 0; k0 < items; k0 += per_pass) {
+        const int k = k0 + tid % per_pass, q0 = tid / per_pass;
         const int tk = tok0 + k / Rpad, r = k % Rpad;
-        float v = 0.f;
-        if (tk < bn && i0 + tk < M && r < R) {
-            const int a = ids[tk];
-            if (a >= 0) {
-                const float *p = partial + (i0 + tk) * Rpad + r;
-                double s = 0.0;
+        const bool in = k < items && q0 < lanes && tk < bn && i0 + tk < M && r < R;
+        const int a = in ? ids[tk] : -1;
+        double s = 0.0;
+        if (a >= 0) {
+            const float *p = partial + (i0 + tk) * Rpad + r;
 #pragma unroll 8
-                for (int q = 0; q < ranges; ++q)
-                    s += static_cast<double>(p[static_cast<int64_t>(q) * M * Rpad]);
-                v = static_cast<float>(s * static_cast<double>(scale[a]));
-            }
-            t_out[(i0 + tk) * R + r] = v;
+            for (int q = q0; q < ranges; q += lanes)
+                s += static_cast<double>(p[static_cast<int64_t>(q) * M * Rpad]);
         }
-        val[k] = v;
+        if (lanes > 1) {
+            share[tid] = s;
+            __syncthreads();
+            if (q0 == 0)
+                for (int q = 1; q < lanes; ++q)
+                    s += share[q * per_pass + tid];
+            __syncthreads();
+        }
+        if (k < items && q0 == 0) {
+            const float v = a >= 0 ? static_cast<float>(s * static_cast<double>(scale[a])) : 0.f;
+            val[k] = v;
+            if (in)
+                t_out[(i0 + tk) * R + r] = v;
+        }
     }
     __syncthreads();
     // the split parts of this CTA's tokens, eight columns per store
