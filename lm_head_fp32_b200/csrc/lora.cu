@@ -300,11 +300,12 @@ lmh_status_t dispatch_fwd(int bn, bool pair, const void *W, uint64_t K, uint64_t
                           const AdapterOperands &ad, const GemmParams &p, const LoraParams &q, cudaStream_t s)
 {
     switch (bn) {
-    // one token tile: bound by W, two CTAs resident per SM
+    // one token tile: bound by W.  Two CTAs resident per SM where tensor memory has
+    // room for both
     case 16: return launch_lora<16, false, OutT, false, 2>(W, K, V, X, ad, p, q, s);
     case 32: return launch_lora<32, false, OutT, false, 2>(W, K, V, X, ad, p, q, s);
     case 64: return launch_lora<64, false, OutT, false, 2>(W, K, V, X, ad, p, q, s);
-    case 128: return launch_lora<128, false, OutT, false, 2>(W, K, V, X, ad, p, q, s);
+    case 128: return launch_lora<128, false, OutT, false>(W, K, V, X, ad, p, q, s);
     default:
         return pair ? launch_lora<256, false, OutT, true>(W, K, V, X, ad, p, q, s)
                     : launch_lora<256, false, OutT, false>(W, K, V, X, ad, p, q, s);

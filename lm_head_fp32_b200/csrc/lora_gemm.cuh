@@ -23,10 +23,11 @@
 //
 // Up to 128 tokens (one token tile, bound by the read of W) there is time to spare
 // on the epilogue warps and none in the handing over of accumulators, each about
-// 1 us: there the warps add u B_a themselves, FP32 on the CUDA cores, to the sums
-// they hold, out of the adapter's rows fetched ahead with cp.async, while the
-// shared product is under way (64 tokens with 28 adapters of rank 16, V = 128256:
-// see lora.cu).
+// 1 us: there the warps form u B_a themselves, FP32 on the CUDA cores, while the
+// shared product is under way.  A lane holds its row of the adapter, fetched ahead
+// with cp.async, and goes over that adapter's tokens; the results wait in spare
+// tensor-memory columns, which, unlike registers, can be addressed by a token
+// number, until they are added to the sums.
 //
 // Roles, ring, tile order, TMA epilogue and the unwinding after a timeout are
 // those of gemm_tc.cuh.
@@ -61,6 +62,16 @@ struct LoraParams {
 // with a 256-wide tile and eight warps, at most 64 with the narrower ones.
 constexpr int lora_epi_warps(int bn) { return bn >= 128 ? 8 : 4; }
 
+// Tensor-memory columns: two accumulators and, up to 128 tokens, the adapters' term.
+__host__ __device__ constexpr uint32_t lora_tmem_cols(int bn)
+{
+    const int want = bn <= 128 ? 3 * bn : 2 * bn;
+    uint32_t n = 32;
+    while (static_cast<int>(n) < want)
+        n *= 2;
+    return n;
+}
+
 template <int BN, bool A_MN, typename OutT, bool TMA_STORE, bool PAIR, int RES = 1, int EW = lora_epi_warps(BN)>
 __global__ void __launch_bounds__(64 + 32 * EW, RES)
     lora_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -71,6 +82,8 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
     constexpr int S = C::STAGES;
     // the epilogue warps form the adapters' term; otherwise the tensor cores
     constexpr bool IN_REGS = BN <= 128;
+    constexpr uint32_t TMEM_COLS = lora_tmem_cols(BN);
+    static_assert(RES * TMEM_COLS <= 512, "tensor memory of the resident CTAs");
     constexpr int kPromote = promote_kblocks(sizeof(OutT));
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -120,9 +133,9 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
     }
     if (warp == 1) {
         if (PAIR)
-            tmem_alloc_pair(tmem_slot, C::TMEM_COLS);
+            tmem_alloc_pair(tmem_slot, TMEM_COLS);
         else
-            tmem_alloc(tmem_slot, C::TMEM_COLS);
+            tmem_alloc(tmem_slot, TMEM_COLS);
     }
     tc_fence_before();
     if (PAIR)
@@ -431,30 +444,32 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
                 ++ch;
             };
             if constexpr (IN_REGS) {
-                // Step (slot, 8 ranks): this lane's row of the adapter, 16 bytes,
-                // through its own place in the staging slots (free until the
-                // tile's stores), AHEAD steps before it is used.
+                // A piece is 8 ranks of one slot: 16 bytes per lane, its row of the
+                // adapter, through the lane's own places in the staging slots (free
+                // until the tile's stores), up to AHEAD pieces before they are used.
                 constexpr int ROOM = C::NSLOT * C::EPI_SLOT_BYTES / 512;
                 constexpr int AHEAD = ROOM < 16 ? ROOM : 16;
+                constexpr int RC = 32;  // ranks held in registers at once
                 uint4 *ring = reinterpret_cast<uint4 *>(slots);
                 const int32_t *ids = q.slot_id + static_cast<int64_t>(nt) * q.slot_stride;
                 const int per_slot = q.rank / 8;
-                const int steps = ns * per_slot;
+                const int pieces = ns * per_slot;
                 const bool in = m < p.Mdim;
-                int fs = 0, fr = 0;  // slot and rank block of the next fetch
+                const uint32_t stash = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + 2 * BN + half * COLS;
+                uint32_t has[MW] = {};
+                int fs = 0, fr = 0, fetched = 0;  // slot and rank block of the next fetch
                 if (lane == 0)
                     bulk_wait_read<0>();  // the last tile's stores have left the slots
                 __syncwarp();
-                auto fetch = [&](int step) {
-                    if (step < steps) {
-                        if constexpr (!A_MN) {
-                            const __nv_bfloat16 *src =
-                                q.adapters + (static_cast<int64_t>(ids[fs]) * p.Mdim + (in ? m : 0)) * q.rank + fr * 8;
-                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                                             smem_u32(ring + (step % AHEAD) * 32 + lane)),
-                                         "l"(src), "r"(in ? 16 : 0)
-                                         : "memory");
-                        }
+                auto fetch = [&]() {
+                    if (fetched < pieces) {
+                        const __nv_bfloat16 *src =
+                            q.adapters + (static_cast<int64_t>(ids[fs]) * p.Mdim + (in ? m : 0)) * q.rank + fr * 8;
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                         smem_u32(ring + (fetched % AHEAD) * 32 + lane)),
+                                     "l"(src), "r"(in ? 16 : 0)
+                                     : "memory");
+                        ++fetched;
                         if (++fr == per_slot) {
                             fr = 0;
                             ++fs;
@@ -464,68 +479,94 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
                 };
                 if constexpr (!A_MN)
                     for (int i = 0; i < AHEAD - 1; ++i)
-                        fetch(i);
-                int cs = 0, cr = 0;
+                        fetch();
+                int used = 0;
 #pragma unroll 1
-                for (int step = 0; step < steps; ++step) {
+                for (int s = 0; s < ns; ++s) {
                     // an accumulator that is full meanwhile is not kept waiting
                     if (ch < chunks &&
                         __all_sync(0xffffffffu, mbar_test_wait(smem_u32(&acc_full[acc]), acc_phase))) {
                         take_shared();
                         release_acc();
                     }
-                    float b[8];
-                    if constexpr (!A_MN) {
-                        asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 2) : "memory");
-                        const uint4 v = ring[(step % AHEAD) * 32 + lane];
-                        fetch(step + AHEAD - 1);
-                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            b[2 * j] = __uint_as_float(w[j] << 16);
-                            b[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-                        }
-                    } else {
-                        const __nv_bfloat16 *src =
-                            q.adapters + (static_cast<int64_t>(ids[cs]) * q.rank + cr * 8) * p.Mdim + (in ? m : 0);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            b[j] = in ? __bfloat162float(src[static_cast<int64_t>(j) * p.Mdim]) : 0.f;
-                    }
-                    const float *trow = q.t + static_cast<int64_t>(n0) * q.rank + cr * 8;
                     uint32_t mask[MW];
 #pragma unroll
-                    for (int i = 0; i < MW; ++i)
-                        mask[i] = masks[cs * kSlotMaskWords + i];
+                    for (int i = 0; i < MW; ++i) {
+                        mask[i] = masks[s * kSlotMaskWords + i];
+                        has[i] |= mask[i];
+                    }
+#pragma unroll 1
+                    for (int r0 = 0; r0 < q.rank; r0 += RC) {
+                        const int n8 = min(RC / 8, (q.rank - r0) / 8);
+                        float b[RC];
 #pragma unroll
-                    for (int c0 = 0; c0 < COLS; c0 += 8) {
-                        if ((mask[c0 / 32] >> (c0 & 31) & 0xffu) == 0)
-                            continue;
+                        for (int k = 0; k < RC / 8; ++k) {
+                            if (k >= n8)
+                                continue;
+                            if constexpr (!A_MN) {
+                                asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 2) : "memory");
+                                const uint4 v = ring[(used++ % AHEAD) * 32 + lane];
+                                fetch();
+                                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                        for (int c = c0; c < c0 + 8; ++c) {
-                            if (mask[c / 32] >> (c & 31) & 1u) {
-                                const float4 *tp = reinterpret_cast<const float4 *>(trow + static_cast<int64_t>(c) * q.rank);
-                                const float4 x = tp[0], y = tp[1];
-                                float s = sum[c];
-                                s = fmaf(x.x, b[0], s);
-                                s = fmaf(x.y, b[1], s);
-                                s = fmaf(x.z, b[2], s);
-                                s = fmaf(x.w, b[3], s);
-                                s = fmaf(y.x, b[4], s);
-                                s = fmaf(y.y, b[5], s);
-                                s = fmaf(y.z, b[6], s);
-                                s = fmaf(y.w, b[7], s);
-                                sum[c] = s;
+                                for (int j = 0; j < 4; ++j) {
+                                    b[8 * k + 2 * j] = __uint_as_float(w[j] << 16);
+                                    b[8 * k + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+                                }
+                            } else {
+                                const __nv_bfloat16 *src =
+                                    q.adapters + (static_cast<int64_t>(ids[s]) * q.rank + r0 + 8 * k) * p.Mdim + (in ? m : 0);
+#pragma unroll
+                                for (int j = 0; j < 8; ++j)
+                                    b[8 * k + j] = in ? __bfloat162float(src[static_cast<int64_t>(j) * p.Mdim]) : 0.f;
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < MW; ++i) {
+#pragma unroll 1
+                            for (uint32_t left = mask[i]; left; left &= left - 1) {
+                                const int c = i * 32 + __ffs(left) - 1;
+                                const float4 *tp = reinterpret_cast<const float4 *>(
+                                    q.t + static_cast<int64_t>(n0 + c) * q.rank + r0);
+                                float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                                for (int k = 0; k < RC / 4; ++k) {
+                                    if (k >= 2 * n8)
+                                        continue;
+                                    const float4 x = tp[k];
+                                    d[0] = fmaf(x.x, b[4 * k], d[0]);
+                                    d[1] = fmaf(x.y, b[4 * k + 1], d[1]);
+                                    d[2] = fmaf(x.z, b[4 * k + 2], d[2]);
+                                    d[3] = fmaf(x.w, b[4 * k + 3], d[3]);
+                                }
+                                float sum4 = (d[0] + d[1]) + (d[2] + d[3]);
+                                if (r0 > 0) {
+                                    tmem_st_wait();
+                                    const uint32_t before = tmem_ld1(stash + c);
+                                    tmem_ld_wait();
+                                    sum4 += __uint_as_float(before);
+                                }
+                                tmem_st1(stash + c, __float_as_uint(sum4));
                             }
                         }
                     }
-                    if (++cr == per_slot) {
-                        cr = 0;
-                        ++cs;
-                    }
                 }
                 asm volatile("cp.async.wait_group 0;" ::: "memory");
+                tmem_st_wait();
                 __syncwarp();
+#pragma unroll
+                for (int c = 0; c < COLS; c += 16) {
+                    const uint32_t m16 = (has[c / 32] >> (c & 31)) & 0xffffu;
+                    if (m16 == 0)
+                        continue;
+                    uint32_t r[32];
+                    tmem_ld_chunk<16>(stash + c, r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (m16 >> j & 1u)
+                            sum[c + j] += __uint_as_float(r[j]);
+                }
             }
             uint32_t ahead[MW];
 #pragma unroll
@@ -650,9 +691,9 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
         __syncwarp();
         tc_fence_after();
         if (PAIR)
-            tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+            tmem_dealloc_pair(tmem_base, TMEM_COLS);
         else
-            tmem_dealloc(tmem_base, C::TMEM_COLS);
+            tmem_dealloc(tmem_base, TMEM_COLS);
     }
     if (threadIdx.x == 0 && *abort_flag && p.status)
         atomicOr(p.status, 2);
