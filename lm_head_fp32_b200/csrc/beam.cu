@@ -13,14 +13,33 @@ namespace {
 
 using namespace lmh::host;
 
-int64_t beam_chunks(int64_t V) { return (V + lmh::kBeamChunk - 1) / lmh::kBeamChunk; }
+// How a row is cut into parts of `batches` batches, one CTA each: enough parts
+// that the CTAs fill the GPU a few times over, and no more, since each part hands
+// C candidates on.  A part's threshold comes from its first batch, and each batch
+// then brings about 2.5 C candidates into a buffer of kBeamBuf, so many candidates
+// mean short parts.
+struct BeamParts {
+    int64_t batches, parts;
+};
+constexpr int64_t kBeamCtas = 148 * 6 * 2;  // CTAs aimed at: two rounds of six per SM
+BeamParts beam_parts(int64_t rows, int64_t V, int64_t C)
+{
+    const int64_t per_row = (V + lmh::kBeamBatch - 1) / lmh::kBeamBatch;  // batches
+    int64_t batches = rows * per_row / kBeamCtas;
+    const int64_t room = lmh::kBeamBuf / (5 * C) < lmh::kBeamMaxBatches ? lmh::kBeamBuf / (5 * C) : lmh::kBeamMaxBatches;
+    batches = batches > room ? room : batches;
+    batches = batches < 1 ? 1 : batches;
+    return {batches, (per_row + batches - 1) / batches};
+}
 
 bool beam_dims_ok(int64_t N, int64_t W, int64_t V, int64_t C)
 {
     if (N < 1 || W < 1 || W > lmh::kBeamMaxWidth || V < 1 || V > kMaxDim || C < 1 ||
-        C > lmh::kBeamMaxCand || N > kMaxDim / W || N * W > kMaxDim / beam_chunks(V))
+        C > lmh::kBeamMaxCand || N > kMaxDim / W)
         return false;
-    return W * beam_chunks(V) <= kMaxDim / C;  // the merge counts an entry's candidates in 32 bits
+    const int64_t parts = beam_parts(N * W, V, C).parts;
+    // CTAs of the scan, and an entry's candidates in the merge, are counted in 32 bits
+    return N * W <= kMaxDim / parts && W * parts <= kMaxDim / C;
 }
 
 int64_t align16(int64_t n) { return (n + 15) / 16 * 16; }
@@ -28,12 +47,12 @@ int64_t align16(int64_t n) { return (n + 15) / 16 * 16; }
 template <typename T>
 lmh_status_t launch_scan(const void *logits, const float *scores, const int32_t *done,
                          lmh::BeamPartial *part, lmh::BeamCand *cand, int64_t N, int64_t W, int64_t V,
-                         int64_t C, int64_t chunks, int32_t *status, cudaStream_t s)
+                         int64_t C, const BeamParts &bp, int32_t *status, cudaStream_t s)
 {
-    return launch_ex(lmh::beam_scan_kernel<T>, dim3(static_cast<unsigned>(N * W * chunks)),
+    return launch_ex(lmh::beam_scan_kernel<T>, dim3(static_cast<unsigned>(N * W * bp.parts)),
                      dim3(lmh::kBeamThreads), 0, s, 1u, static_cast<const T *>(logits), scores, done,
                      part, cand, static_cast<int32_t>(W), V, static_cast<int32_t>(C),
-                     static_cast<int32_t>(chunks), status);
+                     static_cast<int32_t>(bp.parts), static_cast<int32_t>(bp.batches), status);
 }
 
 template <typename VecT, int MAXW>
@@ -74,7 +93,7 @@ int64_t beam_select_workspace_bytes(int64_t N, int64_t W, int64_t V, int64_t C)
 {
     if (!beam_dims_ok(N, W, V, C))
         return -1;
-    const int64_t parts = N * W * beam_chunks(V);
+    const int64_t parts = N * W * beam_parts(N * W, V, C).parts;
     return align16(parts * static_cast<int64_t>(sizeof(lmh::BeamPartial))) +
            parts * C * static_cast<int64_t>(sizeof(lmh::BeamCand));
 }
@@ -105,22 +124,22 @@ lmh_status_t beam_select(const void *logits, int32_t logits_dtype, const float *
         !aligned(next_token, 8) || !aligned(workspace, 16))
         return LMH_ERR_MISALIGNED;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const int64_t chunks = beam_chunks(V);
+    const BeamParts bp = beam_parts(N * W, V, C);
     auto *part = static_cast<lmh::BeamPartial *>(workspace);
     auto *cand = reinterpret_cast<lmh::BeamCand *>(
         static_cast<uint8_t *>(workspace) +
-        align16(N * W * chunks * static_cast<int64_t>(sizeof(lmh::BeamPartial))));
+        align16(N * W * bp.parts * static_cast<int64_t>(sizeof(lmh::BeamPartial))));
     const lmh_status_t r =
         logits_dtype == LMH_F32
-            ? launch_scan<float>(logits, scores, done, part, cand, N, W, V, C, chunks, status, s)
-            : launch_scan<__nv_bfloat16>(logits, scores, done, part, cand, N, W, V, C, chunks, status, s);
+            ? launch_scan<float>(logits, scores, done, part, cand, N, W, V, C, bp, status, s)
+            : launch_scan<__nv_bfloat16>(logits, scores, done, part, cand, N, W, V, C, bp, status, s);
     if (r != LMH_OK)
         return r;
     const lmh::BeamOut o{cand_score, cand_beam, cand_token, next_score, next_beam, next_token};
     return launch_ex(lmh::beam_merge_kernel, dim3(static_cast<unsigned>(N)), dim3(lmh::kBeamThreads), 0, s,
                      1u, scores, done, static_cast<const lmh::BeamPartial *>(part),
                      static_cast<const lmh::BeamCand *>(cand), o, static_cast<int32_t>(W), V,
-                     static_cast<int32_t>(C), static_cast<int32_t>(chunks), eos, status);
+                     static_cast<int32_t>(C), static_cast<int32_t>(bp.parts), eos, status);
 }
 
 lmh_status_t beam_reorder(void *const *states, int64_t num_states, const int32_t *parents, int64_t N,

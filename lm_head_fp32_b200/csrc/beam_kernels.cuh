@@ -5,10 +5,12 @@
 // Selection.  A continuation of beam w by token v scores
 //     total(w, v) = score_w + x_wv - lse_w,   lse_w = log sum_v exp(x_wv).
 // Within a row the order is that of the logits, so the best C of a row are
-// among the best C logits of each of its chunks, and one pass over the logits
-// gives both those and the chunk's share of lse_w:
-//   beam_scan_kernel   one CTA per 8192-logit chunk, held in registers: maximum,
-//                      sum of exponentials, best C logits
+// among the best C logits of each of its parts, and one pass over the logits
+// gives both those and the part's share of lse_w:
+//   beam_scan_kernel   one CTA per part of a row: sum of exponentials, best C
+//                      logits.  A stream like the cross-entropy forward: after the
+//                      first batch a threshold that C logits reach keeps all but
+//                      a few of the others from costing more than one comparison.
 //   beam_merge_kernel  one CTA per batch entry: lse of every beam, the best C
 //                      of all beams' candidates, the beams that go on
 // Continuations are compared by the FP64 value of total, ties by the lower
@@ -24,8 +26,9 @@ namespace lmh {
 
 constexpr int kBeamThreads = 256;
 constexpr int kBeamWarps = kBeamThreads / 32;
-constexpr int kBeamPerThread = 32;                              // logits a thread holds
-constexpr int kBeamChunk = kBeamThreads * kBeamPerThread;       // logits of one CTA
+constexpr int kBeamPerThread = 16;                         // logits of a batch, per thread
+constexpr int kBeamBatch = kBeamThreads * kBeamPerThread;  // logits of a batch
+constexpr int kBeamMaxBatches = 8;                         // batches of a part, at most
 constexpr int kBeamBuf = 1024;        // candidates at or above the threshold a CTA can hold
 constexpr int kBeamMaxCand = 128;
 constexpr int kBeamMaxWidth = 64;
@@ -33,11 +36,11 @@ constexpr float kBeamMaxLogit = 1e38f;
 constexpr int kBeamDevBadLogit = 0x4;   // LMH_DEV_BAD_LOGIT
 constexpr int kBeamDevBadParent = 0x10; // LMH_DEV_BAD_PARENT
 
-// One logit chunk's share of its row.
+// A part's share of its row.
 struct BeamPartial {
     double sum;     // sum of 2^(x log2(e) - ref)
     float ref;      // integer-valued: rint(max * log2(e)); -inf if no finite logit
-    int32_t count;  // candidates in the chunk's list
+    int32_t count;  // candidates in the part's list
 };
 
 struct BeamCand {
@@ -65,16 +68,22 @@ __device__ __forceinline__ double warp_sum(double v)
     return v;
 }
 
+// 2^d for a whole number d <= 0 (0 below 2^-1022).
+__device__ __forceinline__ double pow2(float d)
+{
+    return d < -1022.f ? 0.0 : __hiloint2double((static_cast<int>(d) + 1023) << 20, 0);
+}
+
 // A value that at least `want` of the block's per-thread maxima reach, found
 // from the q-th largest maximum of each warp: the h-th largest of those, with
-// h warps x q lanes >= want.  h = 4 of the 8 warps: near the median warp the
-// threshold lets about twice `want` values through (h = 1 about six times as
-// many, h = 8 three times).  -inf when too few threads hold a finite value.
-// `red` has kBeamWarps entries.
+// h warps x q lanes >= want.  Of 8 warps, h = 4 lets about twice `want` values
+// through for a small `want` (h = 1 about six times as many, h = 8 three times);
+// from 32 on all 8 do, since the last few of a warp's 32 maxima are low.  -inf
+// when too few threads hold a finite value.  `red` has kBeamWarps entries.
 __device__ __forceinline__ float block_threshold(float best, int want, uint32_t *red)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int h = want > 4 * 32 ? 8 : 4;
+    const int h = want >= 32 ? 8 : 4;
     const int q = (want + h - 1) / h;
     uint32_t key = ordered(best), kth = 0;
     for (int i = 0; i < q; ++i) {
@@ -157,128 +166,173 @@ __device__ __forceinline__ void ldg_straddle(const void *p, int bytes, uint32_t 
 
 __device__ __forceinline__ bool beam_live(float score) { return score > -INFINITY && score < INFINITY; }
 
-// One CTA per chunk of a row.  A logit's thread and place go by its column alone,
-// so that equal rows give equal sums and their ties fall by beam number wherever
-// the rows start (V may be odd).  A row that does not start on 16 bytes is read
-// in the aligned vectors around each 16 bytes (the second of the two is the
-// neighbour's first, an L1 hit), and its first and last elements one by one.
-// Rows of beams that cannot go on (score -inf) and of entries that are done are
-// not read.
+// Logits [v0, v0 + kBeamBatch) of a row into registers, -inf past the row's end.
+// A logit's thread and place go by its column alone, so that equal rows give equal
+// sums and their ties fall by beam number wherever the rows start (V may be odd).
+// A row that does not start on 16 bytes is read in the aligned vectors around each
+// 16 bytes (the second of the two is the neighbour's first, an L1 hit), and its
+// first and last elements one by one.
 template <typename T>
-__global__ void __launch_bounds__(kBeamThreads, 4)
-    beam_scan_kernel(const T *__restrict__ logits, const float *__restrict__ scores,
-                     const int32_t *__restrict__ done, BeamPartial *__restrict__ part,
-                     BeamCand *__restrict__ cand, int32_t W, int64_t V, int32_t C, int32_t chunks,
-                     int32_t *status)
+__device__ __forceinline__ void beam_load(const T *x0, int64_t v0, int64_t V, int off, float (&x)[kBeamPerThread])
 {
     constexpr int VN = BeamVec<T>::N;
-    __shared__ uint32_t red[kBeamWarps];
-    __shared__ double red_sum[kBeamWarps];
-    __shared__ uint64_t buf[kBeamBuf];
-    __shared__ int count;
-    pdl_wait();
-    pdl_launch_dependents();
-    const int64_t row = blockIdx.x / chunks;
-    const int chunk = static_cast<int>(blockIdx.x - row * chunks);
-    if ((done && done[row / W]) || !beam_live(scores[row]))
-        return;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const T *x0 = logits + row * V;
-    const int64_t base = static_cast<int64_t>(chunk) * kBeamChunk;  // column of the chunk's start
-    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(x0) & 15);  // bytes past a boundary
-    const int offe = off / static_cast<int>(sizeof(T));
-
-    float x[kBeamPerThread];
-    bool bad = false;
-    if (off == 0 && base + kBeamChunk <= V) {  // every load in flight at once
+    const int tid = threadIdx.x;
+    if (off == 0 && v0 + kBeamBatch <= V) {  // every load in flight at once
         uint4 q[kBeamPerThread / VN];
 #pragma unroll
         for (int i = 0; i < kBeamPerThread / VN; ++i)
-            q[i] = ldg_vec(x0 + base + (i * kBeamThreads + tid) * VN);
+            q[i] = ldg_vec(x0 + v0 + (i * kBeamThreads + tid) * VN);
 #pragma unroll
         for (int i = 0; i < kBeamPerThread / VN; ++i) {
             const uint32_t u[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
             BeamVec<T>::unpack(u, x + i * VN);
         }
-    } else {
+        return;
+    }
+    const int offe = off / static_cast<int>(sizeof(T));
 #pragma unroll
-        for (int i = 0; i < kBeamPerThread / VN; ++i) {
-            const int64_t v = base + (i * kBeamThreads + tid) * VN;
-            if (v >= offe && v - offe + (off ? 2 : 1) * VN <= V) {
-                uint32_t u[4];
-                ldg_straddle(x0 + v - offe, off, u);
-                BeamVec<T>::unpack(u, x + i * VN);
-            } else {
+    for (int i = 0; i < kBeamPerThread / VN; ++i) {
+        const int64_t v = v0 + (i * kBeamThreads + tid) * VN;
+        if (v >= offe && v - offe + (off ? 2 : 1) * VN <= V) {
+            uint32_t u[4];
+            ldg_straddle(x0 + v - offe, off, u);
+            BeamVec<T>::unpack(u, x + i * VN);
+        } else {
 #pragma unroll
-                for (int e = 0; e < VN; ++e)
-                    x[i * VN + e] = v + e < V ? BeamVec<T>::one(x0 + v + e) : -INFINITY;
-            }
+            for (int e = 0; e < VN; ++e)
+                x[i * VN + e] = v + e < V ? BeamVec<T>::one(x0 + v + e) : -INFINITY;
         }
     }
-    if (tid == 0)
-        count = 0;
-    float best = -INFINITY;
+}
+
+// Token of element i of a thread's batch that starts at v0.
+template <typename T>
+__device__ __forceinline__ int64_t beam_token(int64_t v0, int i)
+{
+    constexpr int VN = BeamVec<T>::N;
+    return v0 + ((i / VN) * kBeamThreads + threadIdx.x) * VN + i % VN;
+}
+
+// Higher is better: the logit first, then the lower token.
+__device__ __forceinline__ uint64_t beam_key(float x, int64_t tok)
+{
+    return (static_cast<uint64_t>(ordered(x)) << 32) | (0xffffffffu - static_cast<uint32_t>(tok));
+}
+
+// Makes unusable logits -inf; whether there were any.
+__device__ __forceinline__ bool beam_clean(float (&x)[kBeamPerThread])
+{
+    bool bad = false;
 #pragma unroll
     for (int i = 0; i < kBeamPerThread; ++i) {
         const bool ok = x[i] < kBeamMaxLogit;  // NaN, +inf and what log2(e) times would be: -inf
         bad |= !ok;
         x[i] = ok ? x[i] : -INFINITY;
-        best = fmaxf(best, x[i]);
     }
-    if (__any_sync(0xffffffffu, bad) && lane == 0 && status)
-        atomicOr(status, kBeamDevBadLogit);
+    return bad;
+}
 
-    const uint32_t wmax = __reduce_max_sync(0xffffffffu, ordered(best));
-    // the block's maximum comes with the threshold: both go through `red`
-    if (lane == 0)
-        red[warp] = wmax;
-    __syncthreads();
-    uint32_t bmax = red[0];
-#pragma unroll
-    for (int i = 1; i < kBeamWarps; ++i)
-        bmax = max(bmax, red[i]);
-    const float top = from_ordered(bmax);
-    __syncthreads();
-    BeamPartial *pp = part + row * chunks + chunk;
-    if (top == -INFINITY) {  // the same for the whole block
-        if (tid == 0)
-            *pp = BeamPartial{0.0, -INFINITY, 0};
+// One CTA per part (`batches` batches) of a row.  Rows of beams that cannot go on
+// (score -inf) and of entries that are done are not read.
+template <typename T>
+__global__ void __launch_bounds__(kBeamThreads, 6)
+    beam_scan_kernel(const T *__restrict__ logits, const float *__restrict__ scores,
+                     const int32_t *__restrict__ done, BeamPartial *__restrict__ part,
+                     BeamCand *__restrict__ cand, int32_t W, int64_t V, int32_t C, int32_t parts,
+                     int32_t batches, int32_t *status)
+{
+    __shared__ uint32_t red[kBeamWarps];
+    __shared__ float red_ref[kBeamWarps];
+    __shared__ double red_sum[kBeamWarps];
+    __shared__ uint64_t buf[kBeamBuf];
+    __shared__ uint64_t win[kBeamWarps];
+    __shared__ int count;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t row = blockIdx.x / parts;
+    const int pt = static_cast<int>(blockIdx.x - row * parts);
+    if ((done && done[row / W]) || !beam_live(scores[row]))
         return;
-    }
-    const float thr = block_threshold(best, C, red);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const T *x0 = logits + row * V;
+    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(x0) & 15);  // bytes past a boundary
+    const int64_t begin = static_cast<int64_t>(pt) * batches * kBeamBatch;
+    const int64_t end = begin + static_cast<int64_t>(batches) * kBeamBatch < V
+                            ? begin + static_cast<int64_t>(batches) * kBeamBatch : V;
+    if (tid == 0)
+        count = 0;
 
-    // Sum of exponentials against an integer power of two: x log2(e) - ref is
-    // then rounded once per term, near its own size (log2(e) as two floats, so
-    // that large logits keep their last places); short FP32 sums, joined in
-    // FP64, leave lse good to about 1e-8.
+    // Sum of exponentials against an integer power of two 2^ref: x log2(e) - ref is
+    // then rounded once per term, near its own size (log2(e) as two floats, so that
+    // large logits keep their last places), and a new ref scales the sum exactly.
+    // FP32 sums of 16 terms, joined in FP64, leave lse good to about 1e-8.
     constexpr float kLh = 1.44269502162933349609f, kLl = 1.92596303e-8f;
-    const float ref = rintf(top * kLh);
-    float s4[4] = {0.f, 0.f, 0.f, 0.f};
+    float ref = -INFINITY, top = -INFINITY, thr = -INFINITY;
+    double sum = 0.0;
+    bool any_bad = false;
+    for (int64_t v0 = begin; v0 < end; v0 += kBeamBatch) {
+        float x[kBeamPerThread];
+        beam_load(x0, v0, V, off, x);
+        float best = x[0];
 #pragma unroll
-    for (int i = 0; i < kBeamPerThread; ++i) {
-        const float t = fmaf(x[i], kLl, fmaf(x[i], kLh, -ref));
-        float y;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(t));
-        s4[i & 3] += y;
-    }
-    const double ws = warp_sum(static_cast<double>((s4[0] + s4[1]) + (s4[2] + s4[3])));
-    if (lane == 0)
-        red_sum[warp] = ws;
-
-    if (best >= thr) {
-#pragma unroll
-        for (int i = 0; i < kBeamPerThread; ++i)
-            if (x[i] >= thr && x[i] > -INFINITY) {
-                const int at = atomicAdd(&count, 1);
-                const int64_t v = base + ((i / VN) * kBeamThreads + tid) * VN + i % VN;
-                // higher is better: logit first, then the lower token
-                if (at < kBeamBuf)
-                    buf[at] = (static_cast<uint64_t>(ordered(x[i])) << 32) | (0xffffffffu - static_cast<uint32_t>(v));
+        for (int i = 1; i < kBeamPerThread; ++i)
+            best = fmaxf(best, x[i]);
+        auto add = [&]() -> float {
+            if (best > top) {
+                const float r = rintf(best * kLh);
+                // the first time ref is -inf and the sum 0
+                sum = ref > -INFINITY ? sum * pow2(ref - r) : 0.0;
+                ref = r;
+                top = best;
             }
+            float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < kBeamPerThread; ++i) {
+                const float t = fmaf(x[i], kLl, fmaf(x[i], kLh, -ref));
+                float y;
+                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(t));
+                s4[i & 3] += y;
+            }
+            return (s4[0] + s4[1]) + (s4[2] + s4[3]);
+        };
+        // A NaN, an infinity or a row that begins with -inf shows in the sum
+        // (fmaxf passes over NaN; -inf against a ref of -inf is NaN).
+        float s = best < kBeamMaxLogit ? add() : NAN;
+        if (!(s < INFINITY)) {
+            any_bad |= beam_clean(x);
+            best = x[0];
+#pragma unroll
+            for (int i = 1; i < kBeamPerThread; ++i)
+                best = fmaxf(best, x[i]);
+            s = best > -INFINITY || ref > -INFINITY ? add() : 0.f;
+        }
+        sum += static_cast<double>(s);
+        if (thr == -INFINITY) {  // the first batch, or too little in those before
+            thr = block_threshold(best, C, red);
+            __syncthreads();
+        }
+        if (best >= thr && best > -INFINITY) {
+#pragma unroll
+            for (int i = 0; i < kBeamPerThread; ++i)
+                if (x[i] >= thr && x[i] > -INFINITY) {
+                    const int at = atomicAdd(&count, 1);
+                    if (at < kBeamBuf)
+                        buf[at] = beam_key(x[i], beam_token<T>(v0, i));
+                }
+        }
+    }
+    if (__any_sync(0xffffffffu, any_bad) && lane == 0 && status)
+        atomicOr(status, kBeamDevBadLogit);
+    // the warp's reference, then the block's; scaling by powers of two is exact
+    const float wref = from_ordered(__reduce_max_sync(0xffffffffu, ordered(ref)));
+    const double ws = warp_sum(ref > -INFINITY ? sum * pow2(ref - wref) : 0.0);
+    if (lane == 0) {
+        red_ref[warp] = wref;
+        red_sum[warp] = ws;
     }
     __syncthreads();
     const int n = count;
-    BeamCand *out = cand + (row * chunks + chunk) * C;
+    BeamCand *out = cand + (row * parts + pt) * C;
     int kept;
     if (n <= kBeamBuf) {
         kept = n < C ? n : C;
@@ -292,18 +346,21 @@ __global__ void __launch_bounds__(kBeamThreads, 4)
                                      static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(k))};
         }
     } else {
-        // more values at the threshold than fit (many equal logits): the best
-        // one below the last, C times
-        __shared__ uint64_t win[kBeamWarps];
+        // more values at the threshold than fit (many equal logits, or a row that
+        // ascends): the best one below the last, C times over the part
         uint64_t last = ~0ull;
         for (kept = 0; kept < C; ++kept) {
             uint64_t b = 0;
+            for (int64_t v0 = begin; v0 < end; v0 += kBeamBatch) {
+                float x[kBeamPerThread];
+                beam_load(x0, v0, V, off, x);
+                beam_clean(x);
 #pragma unroll
-            for (int i = 0; i < kBeamPerThread; ++i) {
-                const int64_t v = base + ((i / VN) * kBeamThreads + tid) * VN + i % VN;
-                const uint64_t k = (static_cast<uint64_t>(ordered(x[i])) << 32) | (0xffffffffu - static_cast<uint32_t>(v));
-                if (x[i] > -INFINITY && k < last && k > b)
-                    b = k;
+                for (int i = 0; i < kBeamPerThread; ++i) {
+                    const uint64_t k = beam_key(x[i], beam_token<T>(v0, i));
+                    if (x[i] > -INFINITY && k < last && k > b)
+                        b = k;
+                }
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) {
@@ -327,11 +384,16 @@ __global__ void __launch_bounds__(kBeamThreads, 4)
         }
     }
     if (tid == 0) {
+        float r = red_ref[0];
+#pragma unroll
+        for (int i = 1; i < kBeamWarps; ++i)
+            r = fmaxf(r, red_ref[i]);
         double s = 0.0;
 #pragma unroll
         for (int i = 0; i < kBeamWarps; ++i)
-            s += red_sum[i];
-        *pp = BeamPartial{s, ref, kept};
+            if (red_ref[i] > -INFINITY)
+                s += red_sum[i] * pow2(red_ref[i] - r);
+        part[row * parts + pt] = BeamPartial{s, r, kept};
     }
 }
 
@@ -355,13 +417,13 @@ __device__ __forceinline__ bool ahead(const BeamKey &a, const BeamKey &b)
     return a.total > b.total || (a.total == b.total && a.at < b.at);
 }
 
-// One CTA per batch entry.  The candidates of all chunks of all beams are read
-// twice from L2 (a few KB): once for a threshold, once for those that reach it.
+// One CTA per batch entry.  The candidates of all parts of all beams (a few KB in
+// L2) give a threshold, and those that reach it are ranked.
 // o.next_score may be `scores`: an entry's are read before any is written.
 __global__ void __launch_bounds__(kBeamThreads)
     beam_merge_kernel(const float *scores, const int32_t *__restrict__ done,
                       const BeamPartial *part, const BeamCand *cand, BeamOut o, int32_t W, int64_t V,
-                      int32_t C, int32_t chunks, int64_t eos, int32_t *status)
+                      int32_t C, int32_t parts, int64_t eos, int32_t *status)
 {
     __shared__ double off[kBeamMaxWidth];   // score - lse; -inf for a beam with no continuation
     __shared__ uint32_t red[kBeamWarps];
@@ -394,16 +456,16 @@ __global__ void __launch_bounds__(kBeamThreads)
         const float sc = scores[n * W + w];
         double r = -INFINITY;
         if (beam_live(sc)) {
-            const BeamPartial *pp = part + (n * W + w) * chunks;
+            const BeamPartial *pp = part + (n * W + w) * parts;
             float c = -INFINITY;
-            for (int k = lane; k < chunks; k += 32)
+            for (int k = lane; k < parts; k += 32)
                 c = fmaxf(c, pp[k].ref);
             c = from_ordered(__reduce_max_sync(0xffffffffu, ordered(c)));
             if (c > -INFINITY) {
                 double s = 0.0;
-                for (int k = lane; k < chunks; k += 32)
+                for (int k = lane; k < parts; k += 32)
                     if (pp[k].ref > -INFINITY)
-                        s += pp[k].sum * exp2(static_cast<double>(pp[k].ref) - static_cast<double>(c));
+                        s += pp[k].sum * pow2(pp[k].ref - c);
                 s = warp_sum(s);
                 constexpr double kLn2 = 0.69314718055994530942;
                 r = static_cast<double>(sc) - (static_cast<double>(c) + log2(s)) * kLn2;
@@ -416,38 +478,58 @@ __global__ void __launch_bounds__(kBeamThreads)
     }
     __syncthreads();
 
-    const int per_row = chunks * C;
+    const int per_row = parts * C;
     const int items = W * per_row;
-    // item i: rank i % C of chunk (i / C) % chunks of beam i / per_row
+    // item i: rank i % C of part (i / C) % parts of beam i / per_row
     auto load = [&](int i, BeamKey &k) -> bool {
         const int w = i / per_row, rest = i - w * per_row;
         if (off[w] == -INFINITY)
             return false;
-        const int64_t rc = (n * W + w) * chunks + rest / C;
-        if (rest % C >= part[rc].count)
+        const int pt = rest / C, j = rest - pt * C;
+        const int64_t rc = (n * W + w) * parts + pt;
+        const BeamCand c = cand[rc * C + j];  // past the list's end: not used
+        if (j >= part[rc].count)
             return false;
-        const BeamCand c = cand[rc * C + rest % C];
         k.total = off[w] + static_cast<double>(c.x);
         k.at = w * V + c.tok;
         return true;
     };
     // rounded down, so that a thread's maximum is a bound its candidate reaches
     float best = -INFINITY;
-    for (int i = tid; i < items; i += kBeamThreads) {
+    constexpr int HELD = 4;  // candidates a thread keeps; more are read twice
+    BeamKey held[HELD];
+    bool have[HELD];
+#pragma unroll
+    for (int j = 0; j < HELD; ++j) {
+        const int i = tid + j * kBeamThreads;
+        have[j] = i < items && load(i, held[j]);
+        if (have[j])
+            best = fmaxf(best, __double2float_rd(held[j].total));
+    }
+    for (int i = tid + HELD * kBeamThreads; i < items; i += kBeamThreads) {
         BeamKey k;
         if (load(i, k))
             best = fmaxf(best, __double2float_rd(k.total));
     }
     const float thr = block_threshold(best, C, red);
-    if (best >= thr && best > -INFINITY)
-        for (int i = tid; i < items; i += kBeamThreads) {
-            BeamKey k;
-            if (load(i, k) && k.total >= static_cast<double>(thr)) {
+    if (best >= thr && best > -INFINITY) {
+        auto put = [&](const BeamKey &k) {
+            if (k.total >= static_cast<double>(thr)) {
                 const int at = atomicAdd(&count, 1);
                 if (at < kBeamBuf)
                     buf[at] = k;
             }
+        };
+#pragma unroll
+        for (int j = 0; j < HELD; ++j)
+            if (have[j])
+                put(held[j]);
+        for (int i = tid + HELD * kBeamThreads; i < items; i += kBeamThreads) {
+            BeamKey k;
+            if (load(i, k))
+                put(k);
         }
+    }
     __syncthreads();
     const int m = count;
     int kept;

@@ -8,6 +8,7 @@ or cannot be loaded, every call raises; there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -310,45 +311,52 @@ def ce_bwd_shard(logits: torch.Tensor, target: torch.Tensor, stats: torch.Tensor
     return dlogits
 
 
-def _take(name: str, t: Optional[torch.Tensor], shape, *dtypes, like: Optional[torch.Tensor] = None):
-    """Check one argument of a call (contiguous, its shape, one of its dtypes, on
-    the device of `like`) and return its address; None passes through."""
-    if t is None:
-        return None
+_F32, _B16, _I32, _I64 = ((d,) for d in (torch.float32, torch.bfloat16, torch.int32, torch.int64))
+_LOGITS = _F32 + _B16
+
+
+def _refuse(name: str, t: torch.Tensor, shape, dtypes, dev: int):
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous (row-major)")
-    if like is not None and t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
-    return t.data_ptr()
+    raise ValueError(f"{name} is on another device than the call's first tensor")
 
 
-def _workspace(t: torch.Tensor, like: torch.Tensor):
+def _take(dev: int, *args):
+    """The addresses of a call's tensors, each given as (name, tensor, shape, dtypes)
+    and checked: contiguous, on device number `dev`.  None stays None."""
+    out = []
+    for name, t, shape, dtypes in args:
+        if t is None:
+            out.append(None)
+            continue
+        if t.shape != shape or t.dtype not in dtypes or not t.is_contiguous() or t.get_device() != dev:
+            _refuse(name, t, shape, dtypes, dev)
+        out.append(t.data_ptr())
+    return out
+
+
+def _workspace(t: torch.Tensor, dev: int):
     """(address, bytes) of a caller's scratch buffer."""
-    if not t.is_contiguous() or t.device != like.device:
-        raise ValueError(f"workspace must be contiguous and on {like.device}")
+    if not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError("workspace must be contiguous and on the device of the call's first tensor")
     return t.data_ptr(), t.numel() * t.element_size()
 
 
-def _status(status: Optional[torch.Tensor], like: torch.Tensor):
-    return _take("status", status, (1,), torch.int32, like=like)
-
-
-def _on(like: torch.Tensor, stream, fn, *args) -> int:
-    """fn(*args, stream) with the device of `like` current; stream None is that
+def _on(dev: int, stream, fn, *args) -> int:
+    """fn(*args, stream) with device number `dev` current; stream None is that
     device's current stream."""
-    if not like.is_cuda:
+    if dev < 0:
         raise ValueError("expected CUDA tensors (the library has no CPU path)")
-    dev = like.device.index
+    # the raw handle, without the Stream object around it (1.5 us less per call)
+    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
     if dev == torch.cuda.current_device():
-        s = torch.cuda.current_stream() if stream is None else stream
-        return fn(*args, s.cuda_stream)
+        return fn(*args, s)
     with torch.cuda.device(dev):
-        s = torch.cuda.current_stream() if stream is None else stream
-        return fn(*args, s.cuda_stream)
+        return fn(*args, s)
 
 
 def beam_select_workspace_bytes(N: int, W: int, V: int, C: int) -> int:
@@ -371,30 +379,28 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, cand_score: torch.Te
     if logits.dim() != 3 or cand_score.dim() != 2:
         raise ValueError("expected logits [N,W,V] and cand_score [N,C]")
     N, W, V = logits.shape
-    C = cand_score.shape[1]
-    f32, i32, i64 = torch.float32, torch.int32, torch.int64
-    wp, wn = _workspace(workspace, logits)
-    _check(_on(logits, stream, lib().beam_select,
-               _take("logits", logits, (N, W, V), f32, torch.bfloat16), _dtype_code(logits.dtype),
-               _take("scores", scores, (N, W), f32, like=logits),
-               _take("done", done, (N,), i32, like=logits),
-               _take("cand_score", cand_score, (N, C), f32, like=logits),
-               _take("cand_beam", cand_beam, (N, C), i32, like=logits),
-               _take("cand_token", cand_token, (N, C), i64, like=logits),
-               _take("next_score", next_score, (N, W), f32, like=logits),
-               _take("next_beam", next_beam, (N, W), i32, like=logits),
-               _take("next_token", next_token, (N, W), i64, like=logits),
-               wp, wn, N, W, V, C, int(eos), _status(status, logits)), "beam_select")
+    nw, nc, dev = (N, W), (N, cand_score.shape[1]), logits.get_device()
+    wp, wn = _workspace(workspace, dev)
+    lg, *ptrs, st = _take(
+        dev, ("logits", logits, (N, W, V), _LOGITS), ("scores", scores, nw, _F32),
+        ("done", done, (N,), _I32), ("cand_score", cand_score, nc, _F32),
+        ("cand_beam", cand_beam, nc, _I32), ("cand_token", cand_token, nc, _I64),
+        ("next_score", next_score, nw, _F32), ("next_beam", next_beam, nw, _I32),
+        ("next_token", next_token, nw, _I64), ("status", status, (1,), _I32))
+    code = _on(dev, stream, lib().beam_select, lg, F32 if logits.dtype is torch.float32 else BF16,
+               *ptrs, wp, wn, N, W, V, nc[1], eos, st)
+    if code:
+        raise LmhError(code, "beam_select")
     return cand_score, cand_beam, cand_token, next_score, next_beam, next_token
 
 
-def _state_geometry(t: torch.Tensor, entry_dim: int):
+@functools.lru_cache(maxsize=256)
+def _state_geometry(shape, strides, es: int, entry_dim: int):
     """(run_bytes, outer extents, outer strides) of a state seen as elements
     [.., n, w, ..]: the dimensions that are contiguous below every other one form
     the run, the others are merged where one steps over the next."""
-    es = t.element_size()
-    dims = sorted((t.stride(d) * es, t.shape[d]) for d in range(t.dim())
-                  if d not in (entry_dim, entry_dim + 1) and t.shape[d] != 1)
+    dims = sorted((strides[d] * es, shape[d]) for d in range(len(shape))
+                  if d not in (entry_dim, entry_dim + 1) and shape[d] != 1)
     run = es
     while dims and dims[0][0] == run:
         run *= dims.pop(0)[1]
@@ -406,7 +412,8 @@ def _state_geometry(t: torch.Tensor, entry_dim: int):
             merged.append((st, n))
     if len(merged) > 3:
         raise ValueError("a state may have at most three strided dimensions beside its beams")
-    return run, [n for _, n in merged], [st for st, _ in merged]
+    k = len(merged)
+    return run, (ctypes.c_int64 * k)(*[n for _, n in merged]), (ctypes.c_int64 * k)(*[st for st, _ in merged])
 
 
 def beam_reorder(states, parents: torch.Tensor, entry_dim: int = 0,
@@ -419,28 +426,27 @@ def beam_reorder(states, parents: torch.Tensor, entry_dim: int = 0,
     states = [states] if isinstance(states, torch.Tensor) else list(states)
     if parents.dim() != 2 or not states:
         raise ValueError("expected parents [N,W] and at least one state")
-    N, W = parents.shape
+    (N, W), dev = parents.shape, parents.get_device()
     first = states[0]
-    if not 0 <= entry_dim <= first.dim() - 2 or tuple(first.shape[entry_dim:entry_dim + 2]) != (N, W):
+    shape, strides, dtype, es = tuple(first.shape), first.stride(), first.dtype, first.element_size()
+    if not 0 <= entry_dim <= len(shape) - 2 or shape[entry_dim:entry_dim + 2] != (N, W):
         raise ValueError(f"dimensions {entry_dim} and {entry_dim + 1} of a state must be {(N, W)}")
     for t in states:
-        if t.shape != first.shape or t.stride() != first.stride() or t.dtype != first.dtype:
+        if t.shape != shape or t.stride() != strides or t.dtype is not dtype:
             raise ValueError("the states of one call must have one shape, dtype and strides")
-        if t.device != parents.device:
-            raise ValueError(f"a state is on {t.device}, parents on {parents.device}")
-    pp = _take("parents", parents, (N, W), torch.int32)
-    sp = _status(status, parents)
-    if first.numel() == 0:
+        if t.get_device() != dev:
+            raise ValueError("the states and parents must be on one device")
+    pp, sp = _take(dev, ("parents", parents, (N, W), _I32), ("status", status, (1,), _I32))
+    if 0 in shape:
         return states
-    run, outer, strides = _state_geometry(first, entry_dim)
-    es, k = first.element_size(), len(outer)
-    I64 = ctypes.c_int64
+    run, outer, outer_strides = _state_geometry(shape, strides, es, entry_dim)
     for i in range(0, len(states), 128):
         part = states[i:i + 128]
         ptrs = (ctypes.c_void_p * len(part))(*[t.data_ptr() for t in part])
-        _check(_on(parents, stream, lib().beam_reorder, ptrs, len(part), pp, N, W,
-                   first.stride(entry_dim) * es, first.stride(entry_dim + 1) * es, run,
-                   (I64 * k)(*outer), (I64 * k)(*strides), k, sp), "beam_reorder")
+        code = _on(dev, stream, lib().beam_reorder, ptrs, len(part), pp, N, W, strides[entry_dim] * es,
+                   strides[entry_dim + 1] * es, run, outer, outer_strides, len(outer), sp)
+        if code:
+            raise LmhError(code, "beam_reorder")
     return states
 
 
@@ -460,15 +466,16 @@ def lmhead_fwd_lora(X: torch.Tensor, W: torch.Tensor, A: torch.Tensor, B: torch.
     if X.dim() != 2 or W.dim() != 2 or A.dim() != 3:
         raise ValueError("expected X [M,K], W [V,K], A [N,R,K]")
     (M, K), V, (N, R) = X.shape, W.shape[0], A.shape[:2]
-    b16, f32 = torch.bfloat16, torch.float32
-    wp, wn = _workspace(workspace, X)
-    _check(_on(X, stream, lib().lmhead_fwd_lora, _take("X", X, (M, K), b16),
-               _take("W", W, (V, K), b16, like=X), _take("A", A, (N, R, K), b16, like=X),
-               _take("B", B, (N, V, R), b16, like=X), _take("scale", scale, (N,), f32, like=X),
-               _take("adapter", adapter, (M,), torch.int32, like=X),
-               _take("u", u, (M, R), f32, like=X), _take("logits", logits, (M, V), f32, b16, like=X),
-               _dtype_code(logits.dtype), wp, wn, M, K, V, R, N, _status(status, X)),
-           "lmhead_fwd_lora")
+    dev = X.get_device()
+    wp, wn = _workspace(workspace, dev)
+    *ptrs, st = _take(dev, ("X", X, (M, K), _B16), ("W", W, (V, K), _B16), ("A", A, (N, R, K), _B16),
+                      ("B", B, (N, V, R), _B16), ("scale", scale, (N,), _F32),
+                      ("adapter", adapter, (M,), _I32), ("u", u, (M, R), _F32),
+                      ("logits", logits, (M, V), _LOGITS), ("status", status, (1,), _I32))
+    code = _on(dev, stream, lib().lmhead_fwd_lora, *ptrs,
+               F32 if logits.dtype is torch.float32 else BF16, wp, wn, M, K, V, R, N, st)
+    if code:
+        raise LmhError(code, "lmhead_fwd_lora")
     return logits
 
 
@@ -481,16 +488,16 @@ def lmhead_bwd_dx_lora(dlogits: torch.Tensor, W: torch.Tensor, A: torch.Tensor, 
     if dlogits.dim() != 2 or W.dim() != 2 or A.dim() != 3:
         raise ValueError("expected dlogits [M,V], W [V,K], A [N,R,K]")
     (M, V), K, (N, R) = dlogits.shape, W.shape[1], A.shape[:2]
-    b16, f32 = torch.bfloat16, torch.float32
-    wp, wn = _workspace(workspace, dlogits)
-    _check(_on(dlogits, stream, lib().lmhead_bwd_dx_lora, _take("dlogits", dlogits, (M, V), b16),
-               _take("W", W, (V, K), b16, like=dlogits), _take("A", A, (N, R, K), b16, like=dlogits),
-               _take("B", B, (N, V, R), b16, like=dlogits),
-               _take("scale", scale, (N,), f32, like=dlogits),
-               _take("adapter", adapter, (M,), torch.int32, like=dlogits),
-               _take("g", g, (M, R), f32, like=dlogits), _take("dX", dX, (M, K), f32, b16, like=dlogits),
-               _dtype_code(dX.dtype), wp, wn, M, K, V, R, N, _status(status, dlogits)),
-           "lmhead_bwd_dx_lora")
+    dev = dlogits.get_device()
+    wp, wn = _workspace(workspace, dev)
+    *ptrs, st = _take(dev, ("dlogits", dlogits, (M, V), _B16), ("W", W, (V, K), _B16),
+                      ("A", A, (N, R, K), _B16), ("B", B, (N, V, R), _B16), ("scale", scale, (N,), _F32),
+                      ("adapter", adapter, (M,), _I32), ("g", g, (M, R), _F32),
+                      ("dX", dX, (M, K), _LOGITS), ("status", status, (1,), _I32))
+    code = _on(dev, stream, lib().lmhead_bwd_dx_lora, *ptrs,
+               F32 if dX.dtype is torch.float32 else BF16, wp, wn, M, K, V, R, N, st)
+    if code:
+        raise LmhError(code, "lmhead_bwd_dx_lora")
     return dX
 
 
@@ -503,13 +510,13 @@ def lmhead_bwd_lora(dlogits: torch.Tensor, X: torch.Tensor, u: torch.Tensor, g: 
     if dlogits.dim() != 2 or X.dim() != 2 or dA.dim() != 3:
         raise ValueError("expected dlogits [M,V], X [M,K], dA [N,R,K]")
     (M, V), K, (N, R) = dlogits.shape, X.shape[1], dA.shape[:2]
-    b16, f32 = torch.bfloat16, torch.float32
-    wp, wn = _workspace(workspace, dlogits)
-    _check(_on(dlogits, stream, lib().lmhead_bwd_lora, _take("dlogits", dlogits, (M, V), b16),
-               _take("X", X, (M, K), b16, like=dlogits), _take("u", u, (M, R), f32, like=dlogits),
-               _take("g", g, (M, R), f32, like=dlogits),
-               _take("adapter", adapter, (M,), torch.int32, like=dlogits),
-               _take("dA", dA, (N, R, K), f32, like=dlogits),
-               _take("dB", dB, (N, V, R), f32, like=dlogits), wp, wn, M, K, V, R, N,
-               _status(status, dlogits)), "lmhead_bwd_lora")
+    dev = dlogits.get_device()
+    wp, wn = _workspace(workspace, dev)
+    *ptrs, st = _take(dev, ("dlogits", dlogits, (M, V), _B16), ("X", X, (M, K), _B16),
+                      ("u", u, (M, R), _F32), ("g", g, (M, R), _F32), ("adapter", adapter, (M,), _I32),
+                      ("dA", dA, (N, R, K), _F32), ("dB", dB, (N, V, R), _F32),
+                      ("status", status, (1,), _I32))
+    code = _on(dev, stream, lib().lmhead_bwd_lora, *ptrs, wp, wn, M, K, V, R, N, st)
+    if code:
+        raise LmhError(code, "lmhead_bwd_lora")
     return dA, dB

@@ -46,7 +46,7 @@ def test_select_unsupported_and_misaligned():
 def test_select_workspace_bytes():
     f = lmhead.beam_select_workspace_bytes
     assert f(1, 1, 1, 1) == 16 + 8
-    assert f(3, 2, 8193, 4) == 3 * 2 * 2 * (16 + 8 * 4)
+    assert f(3, 2, 4097, 4) == 3 * 2 * 2 * (16 + 8 * 4)
     assert f(0, 1, 1, 1) == f(1, 65, 1, 1) == f(1, 1, 1, 129) == f(1, 1, 1 << 31, 1) == -1
     # an entry's candidates are counted in 32 bits
     assert f(1, 64, (1 << 31) - 1, 128) == -1
@@ -121,7 +121,9 @@ def test_binding_reorder_refuses():
 
 
 def test_state_geometry():
-    g = lmhead._state_geometry
+    def g(t, entry_dim):
+        run, outer, strides = lmhead._state_geometry(tuple(t.shape), t.stride(), t.element_size(), entry_dim)
+        return run, list(outer), list(strides)
     t = torch.zeros(2, 4, 3, 8, 16, 6)                          # [outer, N, W, heads, room, width]
     assert g(t[:, :, :, :, :10], 1) == (10 * 6 * 4, [8, 2], [16 * 6 * 4, 4 * 3 * 8 * 16 * 6 * 4])
     assert g(t, 1) == (8 * 16 * 6 * 4, [2], [4 * 3 * 8 * 16 * 6 * 4])
