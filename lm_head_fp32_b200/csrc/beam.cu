@@ -14,20 +14,18 @@ namespace {
 using namespace lmh::host;
 
 // How a row is cut into parts of `batches` batches, one CTA each: enough parts
-// that the CTAs fill the GPU a few times over, and no more, since each part hands
-// C candidates on.  A part's threshold comes from its first batch, and each batch
-// then brings about 2.5 C candidates into a buffer of kBeamBuf, so many candidates
-// mean short parts.
+// that the CTAs fill the GPU (twice as many: 64 x 8 x 151936 75.5 against 72.6 us,
+// 16 x 4 x 128256 22.2 against 17.8), and no more, since each part hands
+// C candidates on.
 struct BeamParts {
     int64_t batches, parts;
 };
-constexpr int64_t kBeamCtas = 148 * 6 * 2;  // CTAs aimed at: two rounds of six per SM
-BeamParts beam_parts(int64_t rows, int64_t V, int64_t C)
+constexpr int64_t kBeamCtas = 148 * 6;  // CTAs aimed at: what the SMs hold at once
+BeamParts beam_parts(int64_t rows, int64_t V)
 {
     const int64_t per_row = (V + lmh::kBeamBatch - 1) / lmh::kBeamBatch;  // batches
     int64_t batches = rows * per_row / kBeamCtas;
-    const int64_t room = lmh::kBeamBuf / (5 * C) < lmh::kBeamMaxBatches ? lmh::kBeamBuf / (5 * C) : lmh::kBeamMaxBatches;
-    batches = batches > room ? room : batches;
+    batches = batches > lmh::kBeamMaxBatches ? lmh::kBeamMaxBatches : batches;
     batches = batches < 1 ? 1 : batches;
     return {batches, (per_row + batches - 1) / batches};
 }
@@ -37,7 +35,7 @@ bool beam_dims_ok(int64_t N, int64_t W, int64_t V, int64_t C)
     if (N < 1 || W < 1 || W > lmh::kBeamMaxWidth || V < 1 || V > kMaxDim || C < 1 ||
         C > lmh::kBeamMaxCand || N > kMaxDim / W)
         return false;
-    const int64_t parts = beam_parts(N * W, V, C).parts;
+    const int64_t parts = beam_parts(N * W, V).parts;
     // CTAs of the scan, and an entry's candidates in the merge, are counted in 32 bits
     return N * W <= kMaxDim / parts && W * parts <= kMaxDim / C;
 }
@@ -93,7 +91,7 @@ int64_t beam_select_workspace_bytes(int64_t N, int64_t W, int64_t V, int64_t C)
 {
     if (!beam_dims_ok(N, W, V, C))
         return -1;
-    const int64_t parts = N * W * beam_parts(N * W, V, C).parts;
+    const int64_t parts = N * W * beam_parts(N * W, V).parts;
     return align16(parts * static_cast<int64_t>(sizeof(lmh::BeamPartial))) +
            parts * C * static_cast<int64_t>(sizeof(lmh::BeamCand));
 }
@@ -124,7 +122,7 @@ lmh_status_t beam_select(const void *logits, int32_t logits_dtype, const float *
         !aligned(next_token, 8) || !aligned(workspace, 16))
         return LMH_ERR_MISALIGNED;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const BeamParts bp = beam_parts(N * W, V, C);
+    const BeamParts bp = beam_parts(N * W, V);
     auto *part = static_cast<lmh::BeamPartial *>(workspace);
     auto *cand = reinterpret_cast<lmh::BeamCand *>(
         static_cast<uint8_t *>(workspace) +
@@ -138,7 +136,7 @@ lmh_status_t beam_select(const void *logits, int32_t logits_dtype, const float *
     const lmh::BeamOut o{cand_score, cand_beam, cand_token, next_score, next_beam, next_token};
     return launch_ex(lmh::beam_merge_kernel, dim3(static_cast<unsigned>(N)), dim3(lmh::kBeamThreads), 0, s,
                      1u, scores, done, static_cast<const lmh::BeamPartial *>(part),
-                     static_cast<const lmh::BeamCand *>(cand), o, static_cast<int32_t>(W), V,
+                     static_cast<const lmh::BeamCand *>(cand), o, static_cast<int32_t>(W),
                      static_cast<int32_t>(C), static_cast<int32_t>(bp.parts), eos, status);
 }
 

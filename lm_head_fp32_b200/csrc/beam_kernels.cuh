@@ -8,9 +8,13 @@
 // among the best C logits of each of its parts, and one pass over the logits
 // gives both those and the part's share of lse_w:
 //   beam_scan_kernel   one CTA per part of a row: sum of exponentials, best C
-//                      logits.  A stream like the cross-entropy forward: after the
-//                      first batch a threshold that C logits reach keeps all but
-//                      a few of the others from costing more than one comparison.
+//                      logits.  A stream like the cross-entropy forward that also
+//                      notes the maximum of each thread's 16 logits; the maxima
+//                      give a threshold that C logits reach and few others, and
+//                      only the sixteens that reach it are looked at again.  (Kept
+//                      as they stream, against the threshold of the first batch,
+//                      they cost 33 instructions per logit instead of 9: 103 us
+//                      at 512 x 151936.)
 //   beam_merge_kernel  one CTA per batch entry: lse of every beam, the best C
 //                      of all beams' candidates, the beams that go on
 // Continuations are compared by the FP64 value of total, ties by the lower
@@ -28,7 +32,7 @@ constexpr int kBeamThreads = 256;
 constexpr int kBeamWarps = kBeamThreads / 32;
 constexpr int kBeamPerThread = 16;                         // logits of a batch, per thread
 constexpr int kBeamBatch = kBeamThreads * kBeamPerThread;  // logits of a batch
-constexpr int kBeamMaxBatches = 8;                         // batches of a part, at most
+constexpr int kBeamMaxBatches = 16;                        // batches of a part, at most
 constexpr int kBeamBuf = 1024;        // candidates at or above the threshold a CTA can hold
 constexpr int kBeamMaxCand = 128;
 constexpr int kBeamMaxWidth = 64;
@@ -95,17 +99,14 @@ __device__ __forceinline__ float block_threshold(float best, int want, uint32_t 
     if (lane == 0)
         red[warp] = kth;
     __syncthreads();
-    uint32_t t = 0;
-#pragma unroll
-    for (int i = 0; i < kBeamWarps; ++i) {
-        int above = 0;  // warps ahead of warp i (ties by warp number)
-#pragma unroll
-        for (int j = 0; j < kBeamWarps; ++j)
-            above += red[j] > red[i] || (red[j] == red[i] && j < i);
-        if (above == h - 1)
-            t = red[i];
+    key = lane < kBeamWarps ? red[lane] : 0;
+    for (int i = 0; i < h; ++i) {
+        kth = __reduce_max_sync(0xffffffffu, key);
+        const unsigned at = __ballot_sync(0xffffffffu, key == kth);
+        if (lane == __ffs(at) - 1)
+            key = 0;
     }
-    return t ? from_ordered(t) : -INFINITY;
+    return from_ordered(kth);
 }
 
 __device__ __forceinline__ uint4 ldg_vec(const void *p)
@@ -178,10 +179,11 @@ __device__ __forceinline__ void beam_load(const T *x0, int64_t v0, int64_t V, in
     constexpr int VN = BeamVec<T>::N;
     const int tid = threadIdx.x;
     if (off == 0 && v0 + kBeamBatch <= V) {  // every load in flight at once
+        const uint4 *p = reinterpret_cast<const uint4 *>(x0 + v0) + tid;
         uint4 q[kBeamPerThread / VN];
 #pragma unroll
         for (int i = 0; i < kBeamPerThread / VN; ++i)
-            q[i] = ldg_vec(x0 + v0 + (i * kBeamThreads + tid) * VN);
+            q[i] = ldg_vec(p + i * kBeamThreads);
 #pragma unroll
         for (int i = 0; i < kBeamPerThread / VN; ++i) {
             const uint32_t u[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
@@ -205,12 +207,12 @@ __device__ __forceinline__ void beam_load(const T *x0, int64_t v0, int64_t V, in
     }
 }
 
-// Token of element i of a thread's batch that starts at v0.
+// Token of element i of thread tid's batch that starts at v0.
 template <typename T>
-__device__ __forceinline__ int64_t beam_token(int64_t v0, int i)
+__device__ __forceinline__ int64_t beam_token(int64_t v0, int i, int tid)
 {
     constexpr int VN = BeamVec<T>::N;
-    return v0 + ((i / VN) * kBeamThreads + threadIdx.x) * VN + i % VN;
+    return v0 + ((i / VN) * kBeamThreads + tid) * VN + i % VN;
 }
 
 // Higher is better: the logit first, then the lower token.
@@ -244,14 +246,16 @@ __global__ void __launch_bounds__(kBeamThreads, 6)
     __shared__ uint32_t red[kBeamWarps];
     __shared__ float red_ref[kBeamWarps];
     __shared__ double red_sum[kBeamWarps];
+    __shared__ float noted[kBeamMaxBatches][kBeamThreads];  // maximum of each thread's batch
     __shared__ uint64_t buf[kBeamBuf];
     __shared__ uint64_t win[kBeamWarps];
     __shared__ int count;
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t row = blockIdx.x / parts;
-    const int pt = static_cast<int>(blockIdx.x - row * parts);
-    if ((done && done[row / W]) || !beam_live(scores[row]))
+    const unsigned row32 = blockIdx.x / static_cast<unsigned>(parts);
+    const int64_t row = row32;
+    const int pt = static_cast<int>(blockIdx.x - row32 * parts);
+    if ((done && done[row32 / static_cast<unsigned>(W)]) || !beam_live(scores[row]))
         return;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const T *x0 = logits + row * V;
@@ -265,25 +269,24 @@ __global__ void __launch_bounds__(kBeamThreads, 6)
     // Sum of exponentials against an integer power of two 2^ref: x log2(e) - ref is
     // then rounded once per term, near its own size (log2(e) as two floats, so that
     // large logits keep their last places), and a new ref scales the sum exactly.
-    // FP32 sums of 16 terms, joined in FP64, leave lse good to about 1e-8.
-    constexpr float kLh = 1.44269502162933349609f, kLl = 1.92596303e-8f;
-    float ref = -INFINITY, top = -INFINITY, thr = -INFINITY;
+    // A new ref is taken only when a term would pass 2^8.  FP32 sums of 16 terms,
+    // joined in FP64, leave lse good to about 1e-8.
+    constexpr float kLh = 1.44269502162933349609f, kLl = 1.92596303e-8f, kSlack = 8.f / kLh;
+    float ref = -INFINITY, top = -INFINITY, most = -INFINITY;
     double sum = 0.0;
     bool any_bad = false;
-    for (int64_t v0 = begin; v0 < end; v0 += kBeamBatch) {
+    int nb = 0;
+    for (int64_t v0 = begin; v0 < end; v0 += kBeamBatch, ++nb) {
         float x[kBeamPerThread];
         beam_load(x0, v0, V, off, x);
-        float best = x[0];
-#pragma unroll
-        for (int i = 1; i < kBeamPerThread; ++i)
-            best = fmaxf(best, x[i]);
+        float best;
         auto add = [&]() -> float {
             if (best > top) {
                 const float r = rintf(best * kLh);
                 // the first time ref is -inf and the sum 0
                 sum = ref > -INFINITY ? sum * pow2(ref - r) : 0.0;
                 ref = r;
-                top = best;
+                top = best + kSlack;
             }
             float s4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -296,29 +299,43 @@ __global__ void __launch_bounds__(kBeamThreads, 6)
             return (s4[0] + s4[1]) + (s4[2] + s4[3]);
         };
         // A NaN, an infinity or a row that begins with -inf shows in the sum
-        // (fmaxf passes over NaN; -inf against a ref of -inf is NaN).
-        float s = best < kBeamMaxLogit ? add() : NAN;
-        if (!(s < INFINITY)) {
-            any_bad |= beam_clean(x);
+        // (fmaxf passes over NaN; -inf against a ref of -inf is NaN): once more then.
+        float s;
+        bool again = false;
+        do {
+            if (again)
+                any_bad |= beam_clean(x);
             best = x[0];
 #pragma unroll
             for (int i = 1; i < kBeamPerThread; ++i)
                 best = fmaxf(best, x[i]);
-            s = best > -INFINITY || ref > -INFINITY ? add() : 0.f;
-        }
+            s = best < kBeamMaxLogit ? add() : NAN;
+            if (again && !(s < INFINITY))
+                s = 0.f;  // nothing but -inf so far
+            again = !again && !(s < INFINITY);
+        } while (again);
         sum += static_cast<double>(s);
-        if (thr == -INFINITY) {  // the first batch, or too little in those before
-            thr = block_threshold(best, C, red);
-            __syncthreads();
-        }
-        if (best >= thr && best > -INFINITY) {
-#pragma unroll
-            for (int i = 0; i < kBeamPerThread; ++i)
-                if (x[i] >= thr && x[i] > -INFINITY) {
-                    const int at = atomicAdd(&count, 1);
-                    if (at < kBeamBuf)
-                        buf[at] = beam_key(x[i], beam_token<T>(v0, i));
-                }
+        noted[nb][tid] = best;
+        most = fmaxf(most, best);
+    }
+    const float thr = block_threshold(most, C, red);
+    // The sixteens that reach it, one by one, a lane of the warp per logit.
+    static_assert(kBeamPerThread == 16, "half a warp reads one thread's batch");
+    for (int b = 0; b < nb; ++b) {
+        const int64_t v0 = begin + static_cast<int64_t>(b) * kBeamBatch;
+        const float mine = noted[b][tid];
+        unsigned hit = __ballot_sync(0xffffffffu, mine >= thr && mine > -INFINITY);
+        for (; hit; hit &= hit - 1) {
+            const int64_t v = beam_token<T>(v0, lane & 15, warp * 32 + __ffs(hit) - 1);
+            const float x = lane < 16 && v < V ? BeamVec<T>::one(x0 + v) : -INFINITY;
+            const bool in = x >= thr && x < kBeamMaxLogit && x > -INFINITY;
+            const unsigned put = __ballot_sync(0xffffffffu, in);
+            int at = 0;
+            if (lane == 0)
+                at = atomicAdd(&count, __popc(put));
+            at = __shfl_sync(0xffffffffu, at, 0) + __popc(put & ((1u << lane) - 1u));
+            if (in && at < kBeamBuf)
+                buf[at] = beam_key(x, v);
         }
     }
     if (__any_sync(0xffffffffu, any_bad) && lane == 0 && status)
@@ -346,8 +363,8 @@ __global__ void __launch_bounds__(kBeamThreads, 6)
                                      static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(k))};
         }
     } else {
-        // more values at the threshold than fit (many equal logits, or a row that
-        // ascends): the best one below the last, C times over the part
+        // more values at the threshold than fit (many equal logits): the best one
+        // below the last, C times over the part
         uint64_t last = ~0ull;
         for (kept = 0; kept < C; ++kept) {
             uint64_t b = 0;
@@ -357,7 +374,7 @@ __global__ void __launch_bounds__(kBeamThreads, 6)
                 beam_clean(x);
 #pragma unroll
                 for (int i = 0; i < kBeamPerThread; ++i) {
-                    const uint64_t k = beam_key(x[i], beam_token<T>(v0, i));
+                    const uint64_t k = beam_key(x[i], beam_token<T>(v0, i, tid));
                     if (x[i] > -INFINITY && k < last && k > b)
                         b = k;
                 }
@@ -406,7 +423,8 @@ struct BeamOut {
     int64_t *next_token;
 };
 
-// A candidate of the merge: the FP64 total and the place w * V + v.
+// A candidate of the merge: the FP64 total and the place (beam << 32 | token),
+// which orders as w * V + v does.
 struct BeamKey {
     double total;
     int64_t at;
@@ -421,9 +439,9 @@ __device__ __forceinline__ bool ahead(const BeamKey &a, const BeamKey &b)
 // L2) give a threshold, and those that reach it are ranked.
 // o.next_score may be `scores`: an entry's are read before any is written.
 __global__ void __launch_bounds__(kBeamThreads)
-    beam_merge_kernel(const float *scores, const int32_t *__restrict__ done,
-                      const BeamPartial *part, const BeamCand *cand, BeamOut o, int32_t W, int64_t V,
-                      int32_t C, int32_t parts, int64_t eos, int32_t *status)
+    beam_merge_kernel(const float *scores, const int32_t *__restrict__ done, const BeamPartial *part,
+                      const BeamCand *cand, BeamOut o, int32_t W, int32_t C, int32_t parts, int64_t eos,
+                      int32_t *status)
 {
     __shared__ double off[kBeamMaxWidth];   // score - lse; -inf for a beam with no continuation
     __shared__ uint32_t red[kBeamWarps];
@@ -452,6 +470,38 @@ __global__ void __launch_bounds__(kBeamThreads)
     }
     if (tid == 0)
         count = 0;
+
+    const int items = W * parts * C;
+    // item i: rank i % C of part (i / C) % parts of beam i / per_row.  What lies past
+    // a list's end, or belongs to a beam whose row was not read, is not used.
+    struct Raw {
+        BeamCand c;
+        int32_t w;
+        bool listed;
+    };
+    auto fetch = [&](int i) -> Raw {
+        const unsigned list = static_cast<unsigned>(i) / static_cast<unsigned>(C);  // of the entry
+        const int j = i - static_cast<int>(list) * C;
+        const int64_t rc = n * W * parts + list;
+        return Raw{cand[rc * C + j], static_cast<int32_t>(list / static_cast<unsigned>(parts)), j < part[rc].count};
+    };
+    auto key_of = [&](const Raw &r, BeamKey &k) -> bool {
+        if (!(off[r.w] > -INFINITY) || !r.listed)
+            return false;
+        k.total = off[r.w] + static_cast<double>(r.c.x);
+        k.at = (static_cast<int64_t>(r.w) << 32) | static_cast<uint32_t>(r.c.tok);
+        return true;
+    };
+    constexpr int HELD = 4;  // candidates a thread keeps, under way while lse is made
+    Raw raw[HELD];
+#pragma unroll
+    for (int j = 0; j < HELD; ++j) {
+        const int i = tid + j * kBeamThreads;
+        raw[j].listed = false;
+        raw[j].w = 0;
+        if (i < items)
+            raw[j] = fetch(i);
+    }
     for (int w = warp; w < W; w += kBeamWarps) {
         const float sc = scores[n * W + w];
         double r = -INFINITY;
@@ -478,43 +528,20 @@ __global__ void __launch_bounds__(kBeamThreads)
     }
     __syncthreads();
 
-    const int per_row = parts * C;
-    const int items = W * per_row;
-    // item i: rank i % C of part (i / C) % parts of beam i / per_row
-    auto load = [&](int i, BeamKey &k) -> bool {
-        const int w = i / per_row, rest = i - w * per_row;
-        if (off[w] == -INFINITY)
-            return false;
-        const int pt = rest / C, j = rest - pt * C;
-        const int64_t rc = (n * W + w) * parts + pt;
-        const BeamCand c = cand[rc * C + j];  // past the list's end: not used
-        if (j >= part[rc].count)
-            return false;
-        k.total = off[w] + static_cast<double>(c.x);
-        k.at = w * V + c.tok;
-        return true;
-    };
     // rounded down, so that a thread's maximum is a bound its candidate reaches
     float best = -INFINITY;
-    constexpr int HELD = 4;  // candidates a thread keeps; more are read twice
-    BeamKey held[HELD];
-    bool have[HELD];
+    BeamKey k;
 #pragma unroll
-    for (int j = 0; j < HELD; ++j) {
-        const int i = tid + j * kBeamThreads;
-        have[j] = i < items && load(i, held[j]);
-        if (have[j])
-            best = fmaxf(best, __double2float_rd(held[j].total));
-    }
-    for (int i = tid + HELD * kBeamThreads; i < items; i += kBeamThreads) {
-        BeamKey k;
-        if (load(i, k))
+    for (int j = 0; j < HELD; ++j)
+        if (key_of(raw[j], k))
             best = fmaxf(best, __double2float_rd(k.total));
-    }
+    for (int i = tid + HELD * kBeamThreads; i < items; i += kBeamThreads)
+        if (key_of(fetch(i), k))
+            best = fmaxf(best, __double2float_rd(k.total));
     const float thr = block_threshold(best, C, red);
     if (best >= thr && best > -INFINITY) {
-        auto put = [&](const BeamKey &k) {
-            if (k.total >= static_cast<double>(thr)) {
+        auto put = [&](const Raw &r) {
+            if (key_of(r, k) && k.total >= static_cast<double>(thr)) {
                 const int at = atomicAdd(&count, 1);
                 if (at < kBeamBuf)
                     buf[at] = k;
@@ -522,13 +549,9 @@ __global__ void __launch_bounds__(kBeamThreads)
         };
 #pragma unroll
         for (int j = 0; j < HELD; ++j)
-            if (have[j])
-                put(held[j]);
-        for (int i = tid + HELD * kBeamThreads; i < items; i += kBeamThreads) {
-            BeamKey k;
-            if (load(i, k))
-                put(k);
-        }
+            put(raw[j]);
+        for (int i = tid + HELD * kBeamThreads; i < items; i += kBeamThreads)
+            put(fetch(i));
     }
     __syncthreads();
     const int m = count;
@@ -536,23 +559,21 @@ __global__ void __launch_bounds__(kBeamThreads)
     if (m <= kBeamBuf) {
         kept = m < C ? m : C;
         for (int i = tid; i < m; i += kBeamThreads) {
-            const BeamKey k = buf[i];
+            const BeamKey c = buf[i];
             int rank = 0;
             for (int j = 0; j < m; ++j)
-                rank += ahead(buf[j], k);
+                rank += ahead(buf[j], c);
             if (rank < C)
-                sorted[rank] = k;
+                sorted[rank] = c;
         }
         __syncthreads();
     } else {
         BeamKey last{INFINITY, -1};
         for (kept = 0; kept < C; ++kept) {
             BeamKey b{-INFINITY, INT64_MAX};
-            for (int i = tid; i < items; i += kBeamThreads) {
-                BeamKey k;
-                if (load(i, k) && ahead(last, k) && ahead(k, b))
+            for (int i = tid; i < items; i += kBeamThreads)
+                if (key_of(fetch(i), k) && ahead(last, k) && ahead(k, b))
                     b = k;
-            }
 #pragma unroll
             for (int s = 16; s > 0; s >>= 1) {
                 const BeamKey c{__shfl_xor_sync(0xffffffffu, b.total, s),
@@ -576,23 +597,23 @@ __global__ void __launch_bounds__(kBeamThreads)
         }
         __syncthreads();
     }
-    int gone_on = 0;  // candidates before this one that do not end their sequence
+    auto token = [&](int i) -> int64_t { return sorted[i].at & 0xffffffff; };
     for (int i = tid; i < C; i += kBeamThreads) {
         const bool have = i < kept;
-        const int32_t beam = have ? static_cast<int32_t>(sorted[i].at / V) : -1;
-        const int64_t tok = have ? sorted[i].at - beam * V : -1;
+        const int32_t beam = have ? static_cast<int32_t>(sorted[i].at >> 32) : -1;
+        const int64_t tok = have ? token(i) : -1;
         const float sc = have ? static_cast<float>(sorted[i].total) : -INFINITY;
         o.cand_score[n * C + i] = sc;
         o.cand_beam[n * C + i] = beam;
         o.cand_token[n * C + i] = tok;
         if (o.next_score && have && tok != eos) {
-            gone_on = 0;
+            int before = 0;  // candidates ahead of this one that do not end their sequence
             for (int j = 0; j < i; ++j)
-                gone_on += sorted[j].at % V != eos;
-            if (gone_on < W) {
-                o.next_score[n * W + gone_on] = sc;
-                o.next_beam[n * W + gone_on] = beam;
-                o.next_token[n * W + gone_on] = tok;
+                before += token(j) != eos;
+            if (before < W) {
+                o.next_score[n * W + before] = sc;
+                o.next_beam[n * W + before] = beam;
+                o.next_token[n * W + before] = tok;
             }
         }
     }
@@ -600,7 +621,7 @@ __global__ void __launch_bounds__(kBeamThreads)
         // places that no candidate fills: a dead beam that stays where it is
         int live = 0;
         for (int i = lane; i < kept; i += 32)
-            live += sorted[i].at % V != eos;
+            live += token(i) != eos;
         live = __reduce_add_sync(0xffffffffu, live);
         for (int w = live + lane; w < W; w += 32) {
             o.next_score[n * W + w] = -INFINITY;

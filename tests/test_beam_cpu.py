@@ -48,8 +48,8 @@ def test_select_workspace_bytes():
     assert f(1, 1, 1, 1) == 16 + 8
     assert f(3, 2, 4097, 4) == 3 * 2 * 2 * (16 + 8 * 4)
     assert f(0, 1, 1, 1) == f(1, 65, 1, 1) == f(1, 1, 1, 129) == f(1, 1, 1 << 31, 1) == -1
-    # an entry's candidates are counted in 32 bits
-    assert f(1, 64, (1 << 31) - 1, 128) == -1
+    # the scan's CTAs, at least one per row and 65536 logits, are counted in 32 bits
+    assert f(1 << 20, 64, (1 << 31) - 1, 128) == -1 < f(1, 64, (1 << 31) - 1, 128)
 
 
 def reorder(states=(0x10000,), parents=A, N=2, W=4, es=4096, bs=1024, run=64, outer=(16,), os=(64,)):
