@@ -165,47 +165,75 @@ __global__ void __launch_bounds__(kRowsThreads)
         for (int e = 0; e < 4; ++e)
             acc[n][e] = 0.f;
     const int steps = nsub * nslot;
-    // step t: columns sub t / nslot against adapter t % nslot
-    auto load = [&](int t) {
-        if (t < steps) {
-            const int sub = t / nslot, j = t - sub * nslot;
-            const int64_t c0 = (sub0 + sub) * kRowsSub;
-            if (j == 0) {
-                uint8_t *y = ybuf + (sub % 3) * G::Y_BYTES;
-                for (int k = tid; k < kRowsTokens * (kRowsSub / 8); k += kRowsThreads) {
-                    const int row = k / (kRowsSub / 8), ch = k % (kRowsSub / 8);
-                    const bool in = toks[row] >= 0 && c0 + ch * 8 < Cdim;
-                    cp16(y + row * G::Y_ROW + ch * 16,
-                         in ? Y + static_cast<int64_t>(toks[row]) * Cdim + c0 + ch * 8 : Y, in);
+    // What a thread copies is the same in every step, up to the columns and the
+    // adapter: rows yr, yr + 8, .. of Y at 16-byte unit yc, and P's units tid,
+    // tid + 128, ..; addresses are made once.
+    const int yr = tid >> 4, yc = tid & 15;
+    const __nv_bfloat16 *ysrc[kRowsTokens / 8];
+#pragma unroll
+    for (int i = 0; i < kRowsTokens / 8; ++i) {
+        const int tok = toks[yr + 8 * i];
+        ysrc[i] = tok < 0 ? nullptr : Y + static_cast<int64_t>(tok) * Cdim + sub0 * kRowsSub + yc * 8;
+    }
+    constexpr int UNITS = P_MN ? G::RB / 8 : kRowsSub / 8;  // 16-byte units in a row of P's tile
+    int64_t psrc[2 * NT];                                   // from the adapter's first element of this range
+    bool prank[2 * NT];                                     // a rank below R
+#pragma unroll
+    for (int i = 0; i < 2 * NT; ++i) {
+        const int k = tid + i * kRowsThreads, row = k / UNITS, ch = k % UNITS;
+        if (P_MN) {
+            psrc[i] = (sub0 * kRowsSub + row) * R + r0 + ch * 8;
+            prank[i] = r0 + ch * 8 < R;
+        } else {
+            psrc[i] = static_cast<int64_t>(r0 + row) * Cdim + sub0 * kRowsSub + ch * 8;
+            prank[i] = r0 + row < R;
+        }
+    }
+    const int64_t pstep = P_MN ? static_cast<int64_t>(kRowsSub) * R : kRowsSub;
+    // step: columns `sub` against the tile's adapter j
+    int ls = 0, lj = 0, lt = 0;
+    auto load = [&]() {
+        if (lt < steps) {
+            const int64_t left = Cdim - (sub0 + ls) * kRowsSub;  // columns from here to the end
+            if (lj == 0) {
+                uint8_t *y = ybuf + (ls % 3) * G::Y_BYTES + yr * G::Y_ROW + yc * 16;
+                const bool inc = yc * 8 < left;
+#pragma unroll
+                for (int i = 0; i < kRowsTokens / 8; ++i) {
+                    const bool in = inc && ysrc[i];
+                    cp16(y + i * 8 * G::Y_ROW, in ? ysrc[i] + ls * kRowsSub : Y, in);
                 }
             }
-            uint8_t *pb = pbuf + (t % 3) * G::P_BYTES;
-            const __nv_bfloat16 *base = P + static_cast<int64_t>(list[j]) * R * Cdim;
-            if (P_MN) {
-                for (int k = tid; k < kRowsSub * (G::RB / 8); k += kRowsThreads) {
-                    const int row = k / (G::RB / 8), ch = k % (G::RB / 8);
-                    const bool in = c0 + row < Cdim && r0 + ch * 8 < R;
-                    cp16(pb + row * G::P_ROW + ch * 16, in ? base + (c0 + row) * R + r0 + ch * 8 : P, in);
-                }
-            } else {
-                for (int k = tid; k < G::RB * (kRowsSub / 8); k += kRowsThreads) {
-                    const int row = k / (kRowsSub / 8), ch = k % (kRowsSub / 8);
-                    const bool in = r0 + row < R && c0 + ch * 8 < Cdim;
-                    cp16(pb + row * G::P_ROW + ch * 16, in ? base + (r0 + row) * Cdim + c0 + ch * 8 : P, in);
-                }
+            uint8_t *pb = pbuf + (lt % 3) * G::P_BYTES;
+            const __nv_bfloat16 *base = P + static_cast<int64_t>(list[lj]) * R * Cdim + ls * pstep;
+#pragma unroll
+            for (int i = 0; i < 2 * NT; ++i) {
+                const int k = tid + i * kRowsThreads, row = k / UNITS, ch = k % UNITS;
+                const bool in = prank[i] && (P_MN ? row : ch * 8) < left;
+                cp16(pb + row * G::P_ROW + ch * 16, in ? base + psrc[i] : P, in);
             }
+            if (++lj == nslot) {
+                lj = 0;
+                ++ls;
+            }
+            ++lt;
         }
         cp_commit();
     };
     const int g = lane >> 2;  // this thread's rows of the warp's 16: g and g + 8
     const int id0 = ids[warp * 16 + g], id1 = ids[warp * 16 + g + 8];
-    load(0);
-    load(1);
+    load();
+    load();
+    int sub = 0, j = -1;
     for (int t = 0; t < steps; ++t) {
         cp_wait<1>();
         __syncthreads();  // step t has landed; the buffers of step t - 1 are free
-        load(t + 2);
-        const int sub = t / nslot, a = list[t - sub * nslot];
+        load();
+        if (++j == nslot) {
+            j = 0;
+            ++sub;
+        }
+        const int a = list[j];
         const bool k0 = id0 == a, k1 = id1 == a;
         if (!__any_sync(0xffffffffu, k0 || k1))
             continue;
@@ -518,25 +546,44 @@ __global__ void __launch_bounds__(kColsThreads)
     pdl_launch_dependents();
     const int first = start[a], count = start[a + 1] - first;
     const int steps = (count + kColsTokens - 1) / kColsTokens;
+    // A thread copies unit yc of rows yr, yr + 8, .. of every stage; their tokens are
+    // fetched one stage ahead.
+    const int yr = tid >> 4, yc = tid & 15;
+    const bool inc = c0 + yc * 8 < Cdim;
+    const __nv_bfloat16 *ycol = Y + c0 + yc * 8;
+    int tok[kColsTokens / 8];
+    auto next_tokens = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < kColsTokens / 8; ++i) {
+            const int pos = t * kColsTokens + yr + 8 * i;
+            tok[i] = pos < count ? order[first + pos] : -1;
+        }
+    };
+    next_tokens(0);
     auto load = [&](int t) {
         if (t < steps) {
-            uint8_t *y = ybuf + (t % kColsStages) * G::Y_BYTES;
-            for (int k = tid; k < kColsTokens * (kColsTile / 8); k += kColsThreads) {
-                const int row = k / (kColsTile / 8), ch = k % (kColsTile / 8);
-                const int pos = t * kColsTokens + row;
-                const bool in = pos < count && c0 + ch * 8 < Cdim;
-                cp16(y + row * G::Y_ROW + ch * 16,
-                     in ? Y + static_cast<int64_t>(order[first + pos]) * Cdim + c0 + ch * 8 : Y, in);
+            uint8_t *y = ybuf + (t % kColsStages) * G::Y_BYTES + yr * G::Y_ROW + yc * 16;
+#pragma unroll
+            for (int i = 0; i < kColsTokens / 8; ++i) {
+                const bool in = inc && tok[i] >= 0;
+                cp16(y + i * 8 * G::Y_ROW, in ? ycol + static_cast<int64_t>(tok[i]) * Cdim : Y, in);
             }
             uint8_t *tb = tbuf + (t % kColsStages) * G::T_BYTES;
-            for (int k = tid; k < kColsTokens * 3 * (G::RB / 8); k += kColsThreads) {
-                const int row = k / (3 * (G::RB / 8)), rest = k % (3 * (G::RB / 8));
+            const __nv_bfloat16 *src = parts + (static_cast<int64_t>(first) + t * kColsTokens) * 3 * Rpad + r0;
+            const int left = count - t * kColsTokens;
+            constexpr int UNITS = 3 * (G::RB / 8);
+#pragma unroll
+            for (int k0 = 0; k0 < kColsTokens * UNITS; k0 += kColsThreads) {
+                const int k = k0 + tid;
+                const int row = k / UNITS, rest = k % UNITS;
                 const int part = rest / (G::RB / 8), ch = rest % (G::RB / 8);
-                const int pos = t * kColsTokens + row;
-                const bool in = pos < count && r0 + ch * 8 < Rpad;
-                cp16(tb + row * G::T_ROW + (part * G::RB + ch * 8) * 2,
-                     in ? parts + (static_cast<int64_t>(first + pos) * 3 + part) * Rpad + r0 + ch * 8 : parts, in);
+                if (kColsTokens * UNITS % kColsThreads == 0 || k < kColsTokens * UNITS) {
+                    const bool in = row < left && r0 + ch * 8 < Rpad;
+                    cp16(tb + row * G::T_ROW + (part * G::RB + ch * 8) * 2,
+                         in ? src + (row * 3 + part) * Rpad + ch * 8 : parts, in);
+                }
             }
+            next_tokens(t + 1);
         }
         cp_commit();
     };
