@@ -65,7 +65,7 @@ int64_t rank_pad(int64_t R) { return (R + 15) / 16 * 16; }
 // Byte offsets in the workspace of lmhead_fwd_lora (Cdim = K) and
 // lmhead_bwd_dx_lora (Cdim = V).
 struct GemmSpace {
-    int64_t partial, ux, nslots, slot_id, slot_mask, start, order, bytes;
+    int64_t partial, ux, count, slot, slot_mask, start, order, bytes;
     int64_t tiles, stages, max_slots, slot_stride;
 };
 GemmSpace gemm_space(int64_t M, int64_t Cdim, int64_t R, int64_t N, int bn)
@@ -74,12 +74,12 @@ GemmSpace gemm_space(int64_t M, int64_t Cdim, int64_t R, int64_t N, int bn)
     g.tiles = ceil_div(M, bn);
     g.stages = R <= 32 ? 1 : 2 * ceil_div(R, 64);
     g.max_slots = N < bn ? N : bn;
-    g.slot_stride = (g.max_slots + 3) / 4 * 4;
+    g.slot_stride = (g.max_slots + 1) / 2 * 2;
     g.partial = 0;
     g.ux = align256(row_ranges(M, Cdim, R, N).ranges * M * rank_pad(R) * 4);
-    g.nslots = g.ux + align256(g.tiles * g.stages * bn * 128);
-    g.slot_id = g.nslots + align256(g.tiles * 4);
-    g.slot_mask = g.slot_id + align256(g.tiles * g.slot_stride * 4);
+    g.count = g.ux + align256(g.tiles * g.stages * bn * 128);
+    g.slot = g.count + align256(g.tiles * 8);
+    g.slot_mask = g.slot + align256(g.tiles * g.slot_stride * 8);
     g.start = g.slot_mask + align256(g.tiles * g.max_slots * lmh::kSlotMaskWords * 4);
     g.order = g.start + align256((N + 1) * 4);
     g.bytes = g.order + align256(M * 4);
@@ -245,8 +245,8 @@ lmh_status_t run_rows(const void *Y, const void *P, const float *scale, const in
                      dim3(256), lmh::kExpandTokens * rank_pad(R) * sizeof(float), s, 1u,
                      static_cast<const float *>(partial), static_cast<int32_t>(rr.ranges), adapter, scale, t_out,
                      bn > 128 ? reinterpret_cast<__nv_bfloat16 *>(ws + g.ux) : nullptr,
-                     reinterpret_cast<int32_t *>(ws + g.nslots),
-                     reinterpret_cast<int32_t *>(ws + g.slot_id), reinterpret_cast<uint32_t *>(ws + g.slot_mask),
+                     reinterpret_cast<int2 *>(ws + g.count), reinterpret_cast<int2 *>(ws + g.slot),
+                     reinterpret_cast<uint32_t *>(ws + g.slot_mask),
                      static_cast<int32_t>(bn), static_cast<int32_t>(g.slot_stride), static_cast<int32_t>(g.max_slots),
                      static_cast<int32_t>(g.stages), M, static_cast<int32_t>(R), static_cast<int32_t>(rank_pad(R)),
                      static_cast<int32_t>(N), status);
@@ -257,8 +257,8 @@ LoraParams lora_params(uint8_t *ws, const GemmSpace &g, int64_t R, const void *a
     LoraParams q{};
     q.adapters = static_cast<const __nv_bfloat16 *>(adapters);
     q.t = t;
-    q.nslots = reinterpret_cast<const int32_t *>(ws + g.nslots);
-    q.slot_id = reinterpret_cast<const int32_t *>(ws + g.slot_id);
+    q.count = reinterpret_cast<const int2 *>(ws + g.count);
+    q.slot = reinterpret_cast<const int2 *>(ws + g.slot);
     q.slot_mask = reinterpret_cast<const uint32_t *>(ws + g.slot_mask);
     q.slot_stride = static_cast<int32_t>(g.slot_stride);
     q.max_slots = static_cast<int32_t>(g.max_slots);

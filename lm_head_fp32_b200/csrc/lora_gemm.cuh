@@ -7,13 +7,17 @@
 // with a = the token's adapter.  The adapters' term goes into the same sums:
 // after the k-blocks of the shared product, each output tile takes one more
 // k-block (two per 64 ranks above 32) per adapter that occurs among its tokens
-// ("slot"), each into a tensor-memory accumulator of its own, of which the
-// epilogue adds only the columns of that adapter's tokens.  So the delta never
-// travels to memory and back: separate from the product it would read and
-// write all logits once more (4.2 GB at 4096 x 128256), and an adapter that
-// holds infinities or NaN reaches no other request's tokens.  u is FP32, the
-// tensor cores take BF16: it is split into u_hi + u_lo (2^-18 relative), B_a
-// entering twice.
+// ("slot").  So the delta never travels to memory and back: separate from the
+// product it would read and write all logits once more (4.2 GB at 4096 x
+// 128256).  u is FP32, the tensor cores take BF16: it is split into u_hi + u_lo
+// (2^-18 relative), B_a entering twice.
+//
+// A slot's product is formed for the 32-aligned span of its tokens, and the
+// epilogue adds the columns of those tokens alone: an adapter that holds
+// infinities or NaN reaches no other request's tokens, as a product with zeros
+// would.  The slots' spans are packed into accumulators of their own, since each
+// accumulator handed over costs about 1 us; the one slot of a tile whose tokens
+// all have that adapter goes straight into the shared product's.
 //
 // The sum over the reduction is kept in FP32 as FP32 should be: the tensor
 // cores' own accumulation loses about 2^-24 of the running sum at each MMA,
@@ -46,11 +50,22 @@ __host__ __device__ constexpr int promote_kblocks(int out_bytes) { return out_by
 
 constexpr int kSlotMaskWords = 8;  // one bit per token of a tile of up to 256
 
+// A slot in the table: its adapter, and where its span lies among the tile's
+// tokens (lo, span: multiples of 32) and in its accumulator (off).
+__host__ __device__ constexpr int32_t slot_info(int lo, int span, int off, int last)
+{
+    return lo / 32 | span / 32 << 4 | off / 32 << 8 | last << 12;
+}
+__host__ __device__ constexpr int slot_lo(int32_t i) { return (i & 15) * 32; }
+__host__ __device__ constexpr int slot_span(int32_t i) { return (i >> 4 & 15) * 32; }
+__host__ __device__ constexpr int slot_off(int32_t i) { return (i >> 8 & 15) * 32; }
+__host__ __device__ constexpr bool slot_last(int32_t i) { return i >> 12 & 1; }  // of its accumulator
+
 struct LoraParams {
-    const int32_t *nslots;     // per token tile: adapters among its tokens
-    const int32_t *slot_id;    // [token tile][slot_stride]: their ids
+    const int2 *count;         // per token tile: {slots, accumulators they take; 0: the shared one}
+    const int2 *slot;          // [token tile][slot_stride]: {adapter, slot_info}
     const uint32_t *slot_mask; // [token tile][max_slots][kSlotMaskWords]: their tokens
-    int32_t slot_stride;       // multiple of 4
+    int32_t slot_stride;       // even
     int32_t max_slots;
     int32_t stages_per_slot;   // ring stages of one slot: 1 up to 32 ranks, then 2 per 64
     int32_t rank;
@@ -230,21 +245,21 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
                 if (!slots_there)
                     pdl_wait();
                 slots_there = true;
-                const int ns = q.nslots[nt];
-                const int4 *ids = reinterpret_cast<const int4 *>(q.slot_id + static_cast<int64_t>(nt) * q.slot_stride);
-                for (int s4 = 0; s4 < ns && ok; s4 += 4) {
-                    const int4 four = ids[s4 >> 2];
+                const int ns = q.count[nt].x;
+                const int4 *two = reinterpret_cast<const int4 *>(q.slot + static_cast<int64_t>(nt) * q.slot_stride);
+                for (int s2 = 0; s2 < ns && ok; s2 += 2) {
+                    const int4 e = two[s2 >> 1];
 #pragma unroll 1
-                    for (int s = s4; s < s4 + 4 && s < ns && ok; ++s) {
-                        const int id = (s & 3) == 0 ? four.x : (s & 3) == 1 ? four.y : (s & 3) == 2 ? four.z : four.w;
+                    for (int s = s2; s < s2 + 2 && s < ns && ok; ++s) {
+                        const int id = s & 1 ? e.z : e.x, info = s & 1 ? e.w : e.y;
+                        const int row = slot_lo(info) + static_cast<int>(rank) * (slot_span(info) / C::CTAS);
 #pragma unroll 1
                         for (int j = 0; j < sps; ++j) {
                             if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.wait_limit_ns)) {
                                 ok = false;
                                 break;
                             }
-                            const int urow = (nt * sps + j) * BN + static_cast<int>(rank) * C::BN_CTA;
-                            issue_slot(stage, m0, id, (j >> 1) * 64, urow);
+                            issue_slot(stage, m0, id, (j >> 1) * 64, (nt * sps + j) * BN + row);
                             ++issued;
                             if (++stage == S) {
                                 stage = 0;
@@ -265,6 +280,7 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
             bool slots_there = false;
             // a stage whose copies have landed, its descriptors' bases
             uint32_t sa = 0, sb = 0, d_tmem = 0;
+            uint32_t idesc = C::IDESC;
             auto mma = [&](int ka, int kbb, uint32_t accumulate) {
                 // K-major: 32 bytes along the swizzled row per 16 of the
                 // reduction.  MN-major: 16 rows of 128 bytes.
@@ -272,9 +288,9 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
                                          : smem_desc_sw128(sa + ka * 32, 16, 1024);
                 const uint64_t db = smem_desc_sw128(sb + kbb * 32, 16, 1024);
                 if (PAIR)
-                    mma_bf16_pair(d_tmem, da, db, C::IDESC, accumulate);
+                    mma_bf16_pair(d_tmem, da, db, idesc, accumulate);
                 else
-                    mma_bf16(d_tmem, da, db, C::IDESC, accumulate);
+                    mma_bf16(d_tmem, da, db, idesc, accumulate);
             };
             auto begin_acc = [&]() -> bool {
                 if (!mbar_wait(&acc_empty[acc], acc_phase ^ 1, abort_flag, p.wait_limit_ns))
@@ -315,7 +331,16 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
             for (int t = unit; t < num_tiles && ok; t += num_units) {
                 int mt, nt;
                 tile_coords(t, p, mt, nt);
-                int ns = slots_there && !IN_REGS ? q.nslots[nt] : 0;  // wanted after the shared product
+                // slots, their accumulators and the first two slots, wanted after the
+                // shared product
+                int2 n = {0, 0};
+                int4 two = {0, 0, 0, 0};
+                const int4 *table = reinterpret_cast<const int4 *>(q.slot + static_cast<int64_t>(nt) * q.slot_stride);
+                if (!IN_REGS && slots_there) {
+                    n = q.count[nt];
+                    two = table[0];
+                }
+                idesc = C::IDESC;
                 for (int kb0 = 0; kb0 < num_kb && ok; kb0 += kPromote) {
                     if (!begin_acc()) {
                         ok = false;
@@ -332,20 +357,30 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
                             mma(k, k, (kb != kb0 || k != 0) ? 1u : 0u);
                         end_stage();
                     }
-                    if (ok)
+                    if (!IN_REGS && kb1 == num_kb && !slots_there) {
+                        pdl_wait();
+                        slots_there = true;
+                        n = q.count[nt];
+                        two = table[0];
+                    }
+                    // a slot that takes no accumulator of its own stays with this one
+                    if (ok && !(kb1 == num_kb && n.x > 0 && n.y == 0))
                         end_acc();
                 }
-                if (!IN_REGS && !slots_there) {
-                    pdl_wait();
-                    slots_there = true;
-                    ns = q.nslots[nt];
-                }
+                bool open = n.x > 0 && n.y == 0;  // whether the current accumulator is begun
+                const uint32_t joined = open ? 1u : 0u;
 #pragma unroll 1
-                for (int s = 0; s < ns && ok; ++s) {
-                    if (!begin_acc()) {
+                for (int s = 0; s < n.x && ok; ++s) {
+                    if (s > 0 && (s & 1) == 0)
+                        two = table[s >> 1];
+                    const int info = s & 1 ? two.w : two.y;
+                    if (!open && !begin_acc()) {
                         ok = false;
                         break;
                     }
+                    open = !slot_last(info);
+                    d_tmem = tmem_base + acc * BN + slot_off(info);
+                    idesc = (C::IDESC & ~(0x3fu << 17)) | (static_cast<uint32_t>(slot_span(info)) >> 3) << 17;
 #pragma unroll 1
                     for (int j = 0; j < sps; ++j) {
                         if (!begin_stage()) {
@@ -355,7 +390,7 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
                         if (sps == 1) {
                             // up to 32 ranks: columns 0..31 of u are its high parts,
                             // 32..63 the low ones, against the same ranks of B_a
-                            mma(0, 0, 0u);
+                            mma(0, 0, joined);
                             mma(0, 2, 1u);
                             if (q.rank > 16) {
                                 mma(1, 1, 1u);
@@ -365,11 +400,11 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
                             // 64 ranks: the high parts, then the low ones
                             const int steps = min(4, (q.rank - (j >> 1) * 64 + kUmmaK - 1) / kUmmaK);
                             for (int k = 0; k < steps; ++k)
-                                mma(k, k, (j != 0 || k != 0) ? 1u : 0u);
+                                mma(k, k, (j != 0 || k != 0) ? 1u : joined);
                         }
                         end_stage();
                     }
-                    if (ok)
+                    if (ok && !open)
                         end_acc();
                 }
             }
@@ -403,8 +438,10 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
             const int m = mbase + quarter * 32 + lane;
             const int n0 = nt * BN + half * COLS;
             const int chunks = (num_kb + kPromote - 1) / kPromote;
-            const int ns = q.nslots[nt];
-            const int all = IN_REGS ? chunks : chunks + ns;
+            const int2 n = q.count[nt];
+            const int ns = n.x;
+            const int all = IN_REGS ? chunks : chunks + n.y;
+            const int2 *table = q.slot + static_cast<int64_t>(nt) * q.slot_stride;
             // this warp's columns of the tile's slot masks, one slot ahead
             const uint32_t *masks = q.slot_mask + static_cast<int64_t>(nt) * q.max_slots * kSlotMaskWords +
                                     half * COLS / 32;
@@ -451,7 +488,6 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
                 constexpr int AHEAD = ROOM < 16 ? ROOM : 16;
                 constexpr int RC = 32;  // ranks held in registers at once
                 uint4 *ring = reinterpret_cast<uint4 *>(slots);
-                const int32_t *ids = q.slot_id + static_cast<int64_t>(nt) * q.slot_stride;
                 const int per_slot = q.rank / 8;
                 const int pieces = ns * per_slot;
                 const bool in = m < p.Mdim;
@@ -464,7 +500,7 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
                 auto fetch = [&]() {
                     if (fetched < pieces) {
                         const __nv_bfloat16 *src =
-                            q.adapters + (static_cast<int64_t>(ids[fs]) * p.Mdim + (in ? m : 0)) * q.rank + fr * 8;
+                            q.adapters + (static_cast<int64_t>(table[fs].x) * p.Mdim + (in ? m : 0)) * q.rank + fr * 8;
                         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
                                          smem_u32(ring + (fetched % AHEAD) * 32 + lane)),
                                      "l"(src), "r"(in ? 16 : 0)
@@ -515,7 +551,7 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
                                 }
                             } else {
                                 const __nv_bfloat16 *src =
-                                    q.adapters + (static_cast<int64_t>(ids[s]) * q.rank + r0 + 8 * k) * p.Mdim + (in ? m : 0);
+                                    q.adapters + (static_cast<int64_t>(table[s].x) * q.rank + r0 + 8 * k) * p.Mdim + (in ? m : 0);
 #pragma unroll
                                 for (int j = 0; j < 8; ++j)
                                     b[8 * k + j] = in ? __bfloat162float(src[static_cast<int64_t>(j) * p.Mdim]) : 0.f;
@@ -568,21 +604,22 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
                             sum[c + j] += __uint_as_float(r[j]);
                 }
             }
-            uint32_t ahead[MW];
+            int s = 0;  // the next slot to be added, its place and tokens fetched ahead
+            int32_t info = 0;
+            uint32_t mask[MW] = {};
+            auto fetch_slot = [&]() {
+                if (s < ns) {
+                    info = table[s].y;
 #pragma unroll
-            for (int i = 0; i < MW; ++i)
-                ahead[i] = all > chunks ? masks[i] : 0u;
+                    for (int i = 0; i < MW; ++i)
+                        mask[i] = masks[s * kSlotMaskWords + i];
+                }
+            };
+            if (!IN_REGS && n.y > 0)
+                fetch_slot();
 #pragma unroll 1
             while (ch < all) {
                 const bool shared = IN_REGS || ch < chunks;
-                uint32_t mask[MW] = {};
-                if (!shared) {
-#pragma unroll
-                    for (int i = 0; i < MW; ++i) {
-                        mask[i] = ahead[i];
-                        ahead[i] = ch + 1 < all ? masks[(ch + 1 - chunks) * kSlotMaskWords + i] : 0u;
-                    }
-                }
                 // every lane waits, then the warp agrees, so the .sync.aligned
                 // tensor-memory loads below always run with the full warp
                 const bool got = mbar_wait(&acc_full[acc], acc_phase, abort_flag, p.wait_limit_ns);
@@ -594,21 +631,31 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
                     take_shared();
                 } else {
                     tc_fence_after();
-                    const uint32_t taddr =
-                        tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * BN + half * COLS;
+                    bool last;
+                    do {
+                        last = slot_last(info);
+                        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * BN +
+                                               half * COLS + slot_off(info) - slot_lo(info);
+                        uint32_t now[MW];
 #pragma unroll
-                    for (int c = 0; c < COLS; c += 16) {
-                        const uint32_t m16 = (mask[c / 32] >> (c & 31)) & 0xffffu;
-                        if (m16 == 0)
-                            continue;
-                        uint32_t r[32];
-                        tmem_ld_chunk<16>(taddr + c, r);
-                        tmem_ld_wait();
+                        for (int i = 0; i < MW; ++i)
+                            now[i] = mask[i];
+                        ++s;
+                        fetch_slot();
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            if (m16 >> j & 1u)
-                                sum[c + j] += __uint_as_float(r[j]);
-                    }
+                        for (int c = 0; c < COLS; c += 16) {
+                            const uint32_t m16 = (now[c / 32] >> (c & 31)) & 0xffffu;
+                            if (m16 == 0)
+                                continue;
+                            uint32_t r[32];
+                            tmem_ld_chunk<16>(taddr + c, r);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                if (m16 >> j & 1u)
+                                    sum[c + j] += __uint_as_float(r[j]);
+                        }
+                    } while (!last);
                 }
                 release_acc();
             }

@@ -309,12 +309,12 @@ __device__ __forceinline__ __nv_bfloat16 split_hi(float x, float &rest)
 //   t    [M][R] FP32, scaled: u or g (0 for a token without adapter)
 //   ux   (or NULL) [tile][stages][bn][64] BF16: up to 32 ranks one stage {high 0..31, low
 //        0..31}, above that per 64 ranks a stage of high and one of low parts
-//   nslots, slot_id, slot_mask: see LoraParams (written by part 0)
+//   count, slot_table, slot_mask: see LoraParams (written by part 0)
 __global__ void __launch_bounds__(256)
     lora_expand_kernel(const float *__restrict__ partial, int32_t ranges, const int32_t *__restrict__ adapter,
                        const float *__restrict__ scale, float *__restrict__ t_out,
-                       __nv_bfloat16 *__restrict__ ux, int32_t *__restrict__ nslots,
-                       int32_t *__restrict__ slot_id, uint32_t *__restrict__ slot_mask, int32_t bn,
+                       __nv_bfloat16 *__restrict__ ux, int2 *__restrict__ tile_count,
+                       int2 *__restrict__ slot_table, uint32_t *__restrict__ slot_mask, int32_t bn,
                        int32_t slot_stride, int32_t max_slots, int32_t stages, int64_t M, int32_t R,
                        int32_t Rpad, int32_t N, int32_t *status)
 {
@@ -397,13 +397,15 @@ __global__ void __launch_bounds__(256)
     if (blockIdx.y != 0)
         return;
     // The tile's slots, in the order in which their adapters occur: a hash table
-    // of the ids, each with its first token and the bits of all its tokens.
+    // of the ids, each with its first and last token and the bits of all its tokens.
     constexpr int kBuckets = 512;
-    __shared__ int32_t key[kBuckets], lead[kBuckets];
+    __shared__ int32_t key[kBuckets], lead[kBuckets], tail[kBuckets];
     __shared__ __align__(16) uint32_t bits[kBuckets][kSlotMaskWords];
+    __shared__ int32_t spans[256];  // of each slot: first block of 32 tokens | blocks << 4
     for (int k = tid; k < kBuckets; k += 256) {
         key[k] = -1;
         lead[k] = 256;
+        tail[k] = 0;
         *reinterpret_cast<uint4 *>(&bits[k][0]) = make_uint4(0, 0, 0, 0);
         *reinterpret_cast<uint4 *>(&bits[k][4]) = make_uint4(0, 0, 0, 0);
     }
@@ -419,28 +421,51 @@ __global__ void __launch_bounds__(256)
             h = (h + 1) & (kBuckets - 1);
         }
         atomicMin(&lead[h], tid);
+        atomicMax(&tail[h], tid);
         atomicOr(&bits[h][warp], 1u << lane);
     }
     __syncthreads();
     const bool first = a >= 0 && lead[h] == tid;
     const unsigned b = __ballot_sync(0xffffffffu, first);
+    const unsigned with = __ballot_sync(0xffffffffu, a >= 0);
     if (lane == 0)
-        warp_n[warp] = __popc(b);
+        warp_n[warp] = __popc(b) | __popc(with) << 16;
     __syncthreads();
-    int slot = __popc(b & ((1u << lane) - 1u)), all = 0;
+    int slot = __popc(b & ((1u << lane) - 1u)), all = 0, tokens = 0;
     for (int w = 0; w < 8; ++w) {
         if (w < warp)
-            slot += warp_n[w];
-        all += warp_n[w];
+            slot += warp_n[w] & 0xffff;
+        all += warp_n[w] & 0xffff;
+        tokens += warp_n[w] >> 16;
     }
-    if (tid == 0)
-        nslots[tile] = all;
     if (first) {
-        slot_id[tile * slot_stride + slot] = a;
+        spans[slot] = lead[h] / 32 | (tail[h] / 32 - lead[h] / 32 + 1) << 4;
+        slot_table[tile * slot_stride + slot].x = a;
         uint4 *m = reinterpret_cast<uint4 *>(slot_mask + (tile * max_slots + slot) * kSlotMaskWords);
         m[0] = *reinterpret_cast<uint4 *>(&bits[h][0]);
         m[1] = *reinterpret_cast<uint4 *>(&bits[h][4]);
     }
+    __syncthreads();
+    if (tid != 0)
+        return;
+    // Pack the spans into accumulators of 256 columns, in order.  The only slot of
+    // a tile whose tokens all have it needs none: its span is the whole tile.
+    const int64_t rows = M - i0 < bn ? M - i0 : bn;
+    int packs = 0;
+    if (all == 1 && tokens == rows) {
+        slot_table[tile * slot_stride].y = slot_info(0, 256, 0, 1);
+    } else {
+        int off = 0;
+        for (int s = 0; s < all; ++s) {
+            const int lo = (spans[s] & 15) * 32, span = (spans[s] >> 4) * 32;
+            const int next = s + 1 < all ? (spans[s + 1] >> 4) * 32 : 512;
+            const bool last = off + span + next > 256;
+            slot_table[tile * slot_stride + s].y = slot_info(lo, span, off, last);
+            off = last ? 0 : off + span;
+            packs += last;
+        }
+    }
+    tile_count[tile] = make_int2(all, packs);
 }
 
 // One CTA per adapter: start[a] (tokens of lower adapters) and its tokens in
