@@ -275,7 +275,8 @@ LMH_API lmh_status_t lmhead_bwd_dw_acc(const void *dlogits, const void *X, float
  *   One kernel forms both products in the same sums, FP32 rounded to nearest
  *   every 768 terms of K (4096 for BF16 logits), so the base part is as
  *   lmhead_fwd's but with a smaller error and not bitwise equal to it.  Above 128
- *   tokens u enters the second product as two BF16 parts (2^-18 of u).  An adapter's values reach the tokens that use it and no
+ *   tokens u enters the second product as two BF16 parts (2^-18 of u), or one for
+ *   BF16 logits.  An adapter's values reach the tokens that use it and no
  *   others, infinities and NaN included.  Any order of the tokens; those of one
  *   adapter next to each other cost least (each 256-token tile reads the
  *   adapters that occur in it).

@@ -66,13 +66,14 @@ int64_t rank_pad(int64_t R) { return (R + 15) / 16 * 16; }
 // lmhead_bwd_dx_lora (Cdim = V).
 struct GemmSpace {
     int64_t partial, ux, count, slot, slot_mask, start, order, bytes;
-    int64_t tiles, stages, max_slots, slot_stride;
+    int64_t tiles, parts, stages, max_slots, slot_stride;
 };
-GemmSpace gemm_space(int64_t M, int64_t Cdim, int64_t R, int64_t N, int bn)
+GemmSpace gemm_space(int64_t M, int64_t Cdim, int64_t R, int64_t N, int bn, int32_t out_dtype)
 {
     GemmSpace g;
     g.tiles = ceil_div(M, bn);
-    g.stages = R <= 32 ? 1 : 2 * ceil_div(R, 64);
+    g.parts = out_dtype == LMH_F32 ? 2 : 1;
+    g.stages = R <= 32 ? 1 : g.parts * ceil_div(R, 64);
     g.max_slots = N < bn ? N : bn;
     g.slot_stride = (g.max_slots + 1) / 2 * 2;
     g.partial = 0;
@@ -248,7 +249,7 @@ lmh_status_t run_rows(const void *Y, const void *P, const float *scale, const in
                      reinterpret_cast<int2 *>(ws + g.count), reinterpret_cast<int2 *>(ws + g.slot),
                      reinterpret_cast<uint32_t *>(ws + g.slot_mask),
                      static_cast<int32_t>(bn), static_cast<int32_t>(g.slot_stride), static_cast<int32_t>(g.max_slots),
-                     static_cast<int32_t>(g.stages), M, static_cast<int32_t>(R), static_cast<int32_t>(rank_pad(R)),
+                     static_cast<int32_t>(g.stages), static_cast<int32_t>(g.parts), M, static_cast<int32_t>(R), static_cast<int32_t>(rank_pad(R)),
                      static_cast<int32_t>(N), status);
 }
 
@@ -262,37 +263,26 @@ LoraParams lora_params(uint8_t *ws, const GemmSpace &g, int64_t R, const void *a
     q.slot_mask = reinterpret_cast<const uint32_t *>(ws + g.slot_mask);
     q.slot_stride = static_cast<int32_t>(g.slot_stride);
     q.max_slots = static_cast<int32_t>(g.max_slots);
+    q.parts = static_cast<int32_t>(g.parts);
     q.stages_per_slot = static_cast<int32_t>(g.stages);
     q.rank = static_cast<int32_t>(R);
     return q;
 }
 
-template <int NT, bool OUT_RC>
-lmh_status_t launch_cols(const void *Y, const __nv_bfloat16 *parts, const int32_t *start, const int32_t *order,
-                         float *out, int64_t Cdim, int64_t R, int64_t N, cudaStream_t s)
+template <int NT>
+lmh_status_t launch_cols(const lmh::ColsOp &b, const lmh::ColsOp &a, const int32_t *start, const int32_t *order,
+                         int64_t R, int64_t N, cudaStream_t s)
 {
     using G = lmh::ColsCfg<NT>;
-    auto kern = lmh::lora_cols_kernel<NT, OUT_RC>;
+    auto kern = lmh::lora_cols_kernel<NT>;
     static std::atomic<uint64_t> set{0};
     if (const lmh_status_t r = allow_smem(kern, G::SMEM, set); r != LMH_OK)
         return r;
     return launch_ex(kern,
-                     dim3(static_cast<unsigned>(ceil_div(Cdim, lmh::kColsTile)), static_cast<unsigned>(N),
+                     dim3(static_cast<unsigned>(b.tiles + a.tiles), static_cast<unsigned>(N),
                           static_cast<unsigned>(ceil_div(R, lmh::kRankBlock))),
-                     dim3(lmh::kColsThreads), G::SMEM, s, 1u, static_cast<const __nv_bfloat16 *>(Y), parts, start,
-                     order, out, Cdim, static_cast<int32_t>(R), static_cast<int32_t>(rank_pad(R)));
-}
-
-template <bool OUT_RC>
-lmh_status_t run_cols(const void *Y, const __nv_bfloat16 *parts, const int32_t *start, const int32_t *order,
-                      float *out, int64_t Cdim, int64_t R, int64_t N, cudaStream_t s)
-{
-    switch (R > 48 ? 4 : rank_pad(R) / 16) {
-    case 1: return launch_cols<1, OUT_RC>(Y, parts, start, order, out, Cdim, R, N, s);
-    case 2: return launch_cols<2, OUT_RC>(Y, parts, start, order, out, Cdim, R, N, s);
-    case 3: return launch_cols<3, OUT_RC>(Y, parts, start, order, out, Cdim, R, N, s);
-    default: return launch_cols<4, OUT_RC>(Y, parts, start, order, out, Cdim, R, N, s);
-    }
+                     dim3(lmh::kColsThreads), G::SMEM, s, 1u, b, a, start, order, static_cast<int32_t>(R),
+                     static_cast<int32_t>(rank_pad(R)));
 }
 
 template <typename OutT>
@@ -333,8 +323,8 @@ int64_t lmhead_lora_workspace_bytes(int64_t M, int64_t K, int64_t V, int64_t R, 
 {
     if (!lora_dims_ok(M, K, V, R, N))
         return -1;
-    const int64_t f = gemm_space(M, K, R, N, pick_bn(M, 16)).bytes;
-    const int64_t d = gemm_space(M, V, R, N, pick_bn(M, 64)).bytes;
+    const int64_t f = gemm_space(M, K, R, N, pick_bn(M, 16), LMH_F32).bytes;
+    const int64_t d = gemm_space(M, V, R, N, pick_bn(M, 64), LMH_F32).bytes;
     const int64_t w = grad_space(M, R, N).bytes;
     const int64_t fd = f > d ? f : d;
     return fd > w ? fd : w;
@@ -354,7 +344,7 @@ lmh_status_t lmhead_fwd_lora(const void *X, const void *W, const void *A, const 
         !aligned(logits, out_dtype == LMH_F32 ? 4 : 2))
         return LMH_ERR_MISALIGNED;
     const int bn = pick_bn(M, 16);
-    const GemmSpace g = gemm_space(M, K, R, N, bn);
+    const GemmSpace g = gemm_space(M, K, R, N, bn, out_dtype);
     if (workspace_bytes < g.bytes)
         return LMH_ERR_INVALID_ARG;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -397,7 +387,7 @@ lmh_status_t lmhead_bwd_dx_lora(const void *dlogits, const void *W, const void *
         !aligned(workspace, 256))
         return LMH_ERR_MISALIGNED;
     const int bn = pick_bn(M, 64);
-    const GemmSpace g = gemm_space(M, V, R, N, bn);
+    const GemmSpace g = gemm_space(M, V, R, N, bn, out_dtype);
     if (workspace_bytes < g.bytes)
         return LMH_ERR_INVALID_ARG;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -446,15 +436,22 @@ lmh_status_t lmhead_bwd_lora(const void *dlogits, const void *X, const float *u,
     lmh_status_t r = launch_ex(lmh::lora_group_kernel, dim3(static_cast<unsigned>(N)), dim3(1024), 0, s, 1u, adapter,
                                start, order, M, n32, status);
     const int64_t blocks = ceil_div(M * pad, 256);
-    const dim3 grid(static_cast<unsigned>(blocks < 1184 ? blocks : 1184));
-    for (int i = 0; i < 2 && r == LMH_OK; ++i)
-        r = launch_ex(lmh::lora_split_kernel, grid, dim3(256), 0, s, 1u, i ? g_in : u,
-                      static_cast<const int32_t *>(start), static_cast<const int32_t *>(order), i ? gp : up, n32, r32,
-                      pad);
     if (r == LMH_OK)
-        r = run_cols<true>(X, gp, start, order, dA, K, R, N, s);
-    if (r == LMH_OK)
-        r = run_cols<false>(dlogits, up, start, order, dB, V, R, N, s);
+        r = launch_ex(lmh::lora_split_kernel, dim3(static_cast<unsigned>(blocks < 592 ? blocks : 592), 2), dim3(256),
+                      0, s, 1u, u, g_in, static_cast<const int32_t *>(start), static_cast<const int32_t *>(order),
+                      up, gp, n32, r32, pad);
+    if (r != LMH_OK)
+        return r;
+    const lmh::ColsOp b{static_cast<const __nv_bfloat16 *>(dlogits), up, dB, V,
+                        static_cast<int32_t>(ceil_div(V, lmh::kColsTile)), 0};
+    const lmh::ColsOp a{static_cast<const __nv_bfloat16 *>(X), gp, dA, K,
+                        static_cast<int32_t>(ceil_div(K, lmh::kColsTile)), 1};
+    switch (R > 48 ? 4 : rank_pad(R) / 16) {
+    case 1: r = launch_cols<1>(b, a, start, order, R, N, s); break;
+    case 2: r = launch_cols<2>(b, a, start, order, R, N, s); break;
+    case 3: r = launch_cols<3>(b, a, start, order, R, N, s); break;
+    default: r = launch_cols<4>(b, a, start, order, R, N, s); break;
+    }
     return r;
 }
 

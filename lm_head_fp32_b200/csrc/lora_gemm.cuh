@@ -6,11 +6,13 @@
 //
 // with a = the token's adapter.  The adapters' term goes into the same sums:
 // after the k-blocks of the shared product, each output tile takes one more
-// k-block (two per 64 ranks above 32) per adapter that occurs among its tokens
+// k-block (one or two per 64 ranks) per adapter that occurs among its tokens
 // ("slot").  So the delta never travels to memory and back: separate from the
 // product it would read and write all logits once more (4.2 GB at 4096 x
-// 128256).  u is FP32, the tensor cores take BF16: it is split into u_hi + u_lo
-// (2^-18 relative), B_a entering twice.
+// 128256).  u is FP32, the tensor cores take BF16: for an FP32 output it is split
+// into u_hi + u_lo (2^-18 relative), B_a entering twice; for a BF16 output it is
+// rounded to BF16 once, as X itself is, which is no more than the output's own
+// rounding and takes half the k-blocks.
 //
 // A slot's product is formed for the 32-aligned span of its tokens, and the
 // epilogue adds the columns of those tokens alone: an adapter that holds
@@ -67,7 +69,8 @@ struct LoraParams {
     const uint32_t *slot_mask; // [token tile][max_slots][kSlotMaskWords]: their tokens
     int32_t slot_stride;       // even
     int32_t max_slots;
-    int32_t stages_per_slot;   // ring stages of one slot: 1 up to 32 ranks, then 2 per 64
+    int32_t parts;             // BF16 parts of u: 2, or 1 for a BF16 output
+    int32_t stages_per_slot;   // ring stages of one slot: 1 up to 32 ranks, then `parts` per 64
     int32_t rank;
     const __nv_bfloat16 *adapters;  // [adapter][Mdim][rank], A_MN: [adapter][rank][Mdim]
     const float *t;                 // u (g): [Ndim][rank]
@@ -259,7 +262,7 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
                                 ok = false;
                                 break;
                             }
-                            issue_slot(stage, m0, id, (j >> 1) * 64, (nt * sps + j) * BN + row);
+                            issue_slot(stage, m0, id, j / q.parts * 64, (nt * sps + j) * BN + row);
                             ++issued;
                             if (++stage == S) {
                                 stage = 0;
@@ -387,7 +390,7 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
                             ok = false;
                             break;
                         }
-                        if (sps == 1) {
+                        if (q.parts == 2 && sps == 1) {
                             // up to 32 ranks: columns 0..31 of u are its high parts,
                             // 32..63 the low ones, against the same ranks of B_a
                             mma(0, 0, joined);
@@ -397,8 +400,8 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
                                 mma(1, 3, 1u);
                             }
                         } else {
-                            // 64 ranks: the high parts, then the low ones
-                            const int steps = min(4, (q.rank - (j >> 1) * 64 + kUmmaK - 1) / kUmmaK);
+                            // 64 ranks: the high parts, then, if there are two, the low ones
+                            const int steps = min(4, (q.rank - j / q.parts * 64 + kUmmaK - 1) / kUmmaK);
                             for (int k = 0; k < steps; ++k)
                                 mma(k, k, (j != 0 || k != 0) ? 1u : joined);
                         }

@@ -307,23 +307,26 @@ __device__ __forceinline__ __nv_bfloat16 split_hi(float x, float &rest)
 
 // grid (token tiles of the GEMM, parts of kExpandTokens tokens).
 //   t    [M][R] FP32, scaled: u or g (0 for a token without adapter)
-//   ux   (or NULL) [tile][stages][bn][64] BF16: up to 32 ranks one stage {high 0..31, low
-//        0..31}, above that per 64 ranks a stage of high and one of low parts
+//   ux   (or NULL) [tile][stages][bn][64] BF16.  Of two parts: up to 32 ranks one
+//        stage {high 0..31, low 0..31}, above that per 64 ranks a stage of high and
+//        one of low parts.  Of one part: a stage per 64 ranks
 //   count, slot_table, slot_mask: see LoraParams (written by part 0)
 __global__ void __launch_bounds__(256)
     lora_expand_kernel(const float *__restrict__ partial, int32_t ranges, const int32_t *__restrict__ adapter,
                        const float *__restrict__ scale, float *__restrict__ t_out,
                        __nv_bfloat16 *__restrict__ ux, int2 *__restrict__ tile_count,
                        int2 *__restrict__ slot_table, uint32_t *__restrict__ slot_mask, int32_t bn,
-                       int32_t slot_stride, int32_t max_slots, int32_t stages, int64_t M, int32_t R,
-                       int32_t Rpad, int32_t N, int32_t *status)
+                       int32_t slot_stride, int32_t max_slots, int32_t stages, int32_t parts, int64_t M,
+                       int32_t R, int32_t Rpad, int32_t N, int32_t *status)
 {
     __shared__ int32_t ids[256];
     __shared__ int32_t warp_n[8];
     __shared__ double share[256];
     extern __shared__ float val[];  // [kExpandTokens][Rpad]
-    pdl_wait();
+    // The GEMM may begin with the shared product at once: all that it reads of that
+    // was complete before the row kernel let this one start.
     pdl_launch_dependents();
+    pdl_wait();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t tile = blockIdx.x;
     const int64_t i0 = tile * bn;
@@ -382,8 +385,9 @@ __global__ void __launch_bounds__(256)
         const int tk = tok0 + j;
         if (tk >= bn)
             break;
-        const bool low = stages == 1 ? c0 >= 32 : (st & 1);
-        const int r0 = stages == 1 ? (c0 & 31) : (st >> 1) * 64 + c0;
+        const bool both = parts == 2 && stages == 1;
+        const bool low = both ? c0 >= 32 : parts == 2 && (st & 1);
+        const int r0 = both ? (c0 & 31) : st / parts * 64 + c0;
         __nv_bfloat16 h[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -521,13 +525,16 @@ __global__ void __launch_bounds__(1024)
 
 // parts[pos][3][Rpad] BF16 of t[order[pos]]: x = high + middle + low, exact to
 // FP32's 24 bits (while the low part stays normal); zeros in the padding.
+// grid.y: u, g.
 __global__ void __launch_bounds__(256)
-    lora_split_kernel(const float *__restrict__ t, const int32_t *__restrict__ start,
-                      const int32_t *__restrict__ order, __nv_bfloat16 *__restrict__ parts, int32_t N,
-                      int32_t R, int32_t Rpad)
+    lora_split_kernel(const float *__restrict__ u, const float *__restrict__ g, const int32_t *__restrict__ start,
+                      const int32_t *__restrict__ order, __nv_bfloat16 *__restrict__ u_parts,
+                      __nv_bfloat16 *__restrict__ g_parts, int32_t N, int32_t R, int32_t Rpad)
 {
     pdl_wait();
     pdl_launch_dependents();
+    const float *t = blockIdx.y ? g : u;
+    __nv_bfloat16 *parts = blockIdx.y ? g_parts : u_parts;
     const int64_t total = static_cast<int64_t>(start[N]) * Rpad;
     for (int64_t k = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; k < total;
          k += static_cast<int64_t>(gridDim.x) * 256) {
@@ -553,19 +560,35 @@ struct ColsCfg {
     static constexpr int SMEM = kColsStages * (Y_BYTES + T_BYTES);
 };
 
-// grid (column tiles, adapters, rank blocks).  out: OUT_RC [adapter][R][Cdim]
-// (dA), else [adapter][Cdim][R] (dB), FP32; zeros for an adapter without tokens.
-template <int NT, bool OUT_RC>
+// One of the two products of lora_cols_kernel: Y [tokens][Cdim], the parts of t,
+// and the output [adapter][Cdim][R], or [adapter][R][Cdim] if `rc`.
+struct ColsOp {
+    const __nv_bfloat16 *Y;
+    const __nv_bfloat16 *parts;
+    float *out;
+    int64_t Cdim;
+    int32_t tiles;
+    int32_t rc;
+};
+
+// grid (column tiles of dB and then of dA, adapters, rank blocks).  FP32 outputs;
+// zeros for an adapter without tokens.
+template <int NT>
 __global__ void __launch_bounds__(kColsThreads)
-    lora_cols_kernel(const __nv_bfloat16 *__restrict__ Y, const __nv_bfloat16 *__restrict__ parts,
-                     const int32_t *__restrict__ start, const int32_t *__restrict__ order,
-                     float *__restrict__ out, int64_t Cdim, int32_t R, int32_t Rpad)
+    lora_cols_kernel(const ColsOp op_b, const ColsOp op_a, const int32_t *__restrict__ start,
+                     const int32_t *__restrict__ order, int32_t R, int32_t Rpad)
 {
+    const bool is_b = static_cast<int>(blockIdx.x) < op_b.tiles;
+    const __nv_bfloat16 *__restrict__ Y = is_b ? op_b.Y : op_a.Y;
+    const __nv_bfloat16 *__restrict__ parts = is_b ? op_b.parts : op_a.parts;
+    float *__restrict__ out = is_b ? op_b.out : op_a.out;
+    const int64_t Cdim = is_b ? op_b.Cdim : op_a.Cdim;
+    const bool rc = is_b ? op_b.rc : op_a.rc;
     using G = ColsCfg<NT>;
     extern __shared__ __align__(16) uint8_t smem[];
     uint8_t *ybuf = smem, *tbuf = smem + kColsStages * G::Y_BYTES;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kColsTile;
+    const int64_t c0 = static_cast<int64_t>(blockIdx.x - (is_b ? 0 : op_b.tiles)) * kColsTile;
     const int a = blockIdx.y, r0 = blockIdx.z * kRankBlock;
     pdl_wait();
     pdl_launch_dependents();
@@ -676,7 +699,7 @@ __global__ void __launch_bounds__(kColsThreads)
                 if (r >= R)  // R is a multiple of 8: r + 1 < R as well
                     continue;
                 const float x = acc[m][n][2 * e2], z = acc[m][n][2 * e2 + 1];
-                if (OUT_RC) {
+                if (rc) {
                     float *o = out + (static_cast<int64_t>(a) * R + r) * Cdim + c;
                     o[0] = x;
                     o[Cdim] = z;

@@ -8,8 +8,9 @@ Tolerances, per element, with S the sum of the absolute values of the terms:
     4096 terms (256 MMAs): 2^-23 * (260 + terms / 8192) * S.
   row sums (u, g): the same per 128 terms (8 MMAs), parts added in FP64 or FP32,
     one rounding: 2^-23 * (12 + terms / 256) * S.
-  u in the second product: two BF16 parts (up to 128 tokens none), 2^-17 of
-    sum |u| |B|, beside u's own tolerance carried through B.
+  u in the second product, above 128 tokens: for an FP32 output two BF16 parts,
+    2^-17 of sum |u| |B|, for a BF16 output one, 2^-8 of it; beside u's own
+    tolerance carried through B.
   gradients dA, dB: 256 terms (3 x 16 MMAs) at a time: 2^-23 * (52 + tokens / 512) * S.
   BF16 outputs: half a BF16 step (2^-9 of the value's power of two, so at most
     2^-8 of the value) beside these.
@@ -72,6 +73,10 @@ def gemm_eps(terms, dtype=torch.float32):
     return E23 * (52 + terms / 1536 if dtype == torch.float32 else 260 + terms / 8192)
 
 
+def split_eps(M, dtype):
+    return 2.0 ** -24 if M <= 128 else 2.0 ** -17 if dtype == torch.float32 else 2.0 ** -8
+
+
 def ref_fwd(X, W, A, B, scale, ids, dtype=torch.float32):
     """(u, its tolerance, logits, their tolerance) in FP64."""
     X, W, A, B, scale = (t.double() for t in (X, W, A, B, scale))
@@ -85,7 +90,7 @@ def ref_fwd(X, W, A, B, scale, ids, dtype=torch.float32):
         tu[at] = E23 * (12 + K / 256) * scale[a] * (X[at].abs() @ A[a].abs().T)
         ub = u[at].abs() @ B[a].abs().T
         out[at] += u[at] @ B[a].T
-        tol[at] += tu[at] @ B[a].abs().T + (2.0 ** -17 + E23 * 56) * ub
+        tol[at] += tu[at] @ B[a].abs().T + (split_eps(M, dtype) + E23 * 56) * ub
     return u, tu, out, tol
 
 
@@ -236,7 +241,7 @@ def check_bwd(M, K, V, R, N, order, dtype, seed=0):
         rg[at] = sd[a] * (dd[at] @ Bd[a])
         tg[at] = E23 * (12 + V / 256) * sd[a] * (dd[at].abs() @ Bd[a].abs())
         rX[at] += rg[at] @ Ad[a]
-        tX[at] += tg[at] @ Ad[a].abs() + (2.0 ** -17 + E23 * 56) * (rg[at].abs() @ Ad[a].abs())
+        tX[at] += tg[at] @ Ad[a].abs() + (split_eps(M, dtype) + E23 * 56) * (rg[at].abs() @ Ad[a].abs())
         c = E23 * (52 + at.numel() / 512)
         gf = g[at].double()  # as the call was given it
         close(dA[a], gf.T @ Xd[at], c * (gf.abs().T @ Xd[at].abs()), f"dA[{a}]")
