@@ -56,9 +56,10 @@ lmh_status_t launch_scan(const void *logits, const float *scores, const int32_t 
 template <typename VecT, int MAXW>
 lmh_status_t launch_reorder(const lmh::ReorderParams &p, int64_t N, int num_states, cudaStream_t s)
 {
-    const int64_t need = (static_cast<int64_t>(p.columns) + lmh::kReorderThreads - 1) / lmh::kReorderThreads;
-    // a few waves of blocks over all entries and states; a thread then takes several columns
-    const int64_t cap = (num_sms() * 32 + N * num_states - 1) / (N * num_states);
+    constexpr int64_t per_block = lmh::kReorderThreads * lmh::kReorderColumns;
+    const int64_t need = (static_cast<int64_t>(p.columns) + per_block - 1) / per_block;
+    // several waves of blocks over all entries and states; a thread then takes more columns
+    const int64_t cap = (num_sms() * 64 + N * num_states - 1) / (N * num_states);
     const int64_t grid = need < cap ? need : cap;
     return launch_ex(lmh::beam_reorder_kernel<VecT, MAXW>,
                      dim3(static_cast<unsigned>(grid), static_cast<unsigned>(N),

@@ -34,6 +34,7 @@ constexpr int kBeamPerThread = 16;                         // logits of a batch,
 constexpr int kBeamBatch = kBeamThreads * kBeamPerThread;  // logits of a batch
 constexpr int kBeamMaxBatches = 16;                        // batches of a part, at most
 constexpr int kBeamBuf = 1024;        // candidates at or above the threshold a CTA can hold
+constexpr int kBeamHits = 128;        // sixteens at or above it that a warp can list
 constexpr int kBeamMaxCand = 128;
 constexpr int kBeamMaxWidth = 64;
 constexpr float kBeamMaxLogit = 1e38f;
@@ -76,6 +77,20 @@ __device__ __forceinline__ double warp_sum(double v)
 __device__ __forceinline__ double pow2(float d)
 {
     return d < -1022.f ? 0.0 : __hiloint2double((static_cast<int>(d) + 1023) << 20, 0);
+}
+
+// How many of n keys are ahead of a candidate, counted by eight neighbouring lanes
+// (`part` is the lane's place among them); every lane gets the result.
+template <typename F>
+__device__ __forceinline__ int beam_rank(int part, int n, F is_ahead)
+{
+    int rank = 0;
+    for (int j = part; j < n; j += 8)
+        rank += is_ahead(j);
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1)
+        rank += __shfl_xor_sync(0xffffffffu, rank, o);
+    return rank;
 }
 
 // A value that at least `want` of the block's per-thread maxima reach, found
@@ -247,6 +262,7 @@ __global__ void __launch_bounds__(kBeamThreads, 6)
     __shared__ float red_ref[kBeamWarps];
     __shared__ double red_sum[kBeamWarps];
     __shared__ float noted[kBeamMaxBatches][kBeamThreads];  // maximum of each thread's batch
+    __shared__ uint16_t listed[kBeamWarps][kBeamHits];  // batch << 5 | lane
     __shared__ uint64_t buf[kBeamBuf];
     __shared__ uint64_t win[kBeamWarps];
     __shared__ int count;
@@ -319,24 +335,39 @@ __global__ void __launch_bounds__(kBeamThreads, 6)
         most = fmaxf(most, best);
     }
     const float thr = block_threshold(most, C, red);
-    // The sixteens that reach it, one by one, a lane of the warp per logit.
+    // The sixteens that reach it: listed by the warp, then two at a time, a lane per
+    // logit (the loads are what takes time here).
     static_assert(kBeamPerThread == 16, "half a warp reads one thread's batch");
+    int hits = 0;
     for (int b = 0; b < nb; ++b) {
-        const int64_t v0 = begin + static_cast<int64_t>(b) * kBeamBatch;
         const float mine = noted[b][tid];
-        unsigned hit = __ballot_sync(0xffffffffu, mine >= thr && mine > -INFINITY);
-        for (; hit; hit &= hit - 1) {
-            const int64_t v = beam_token<T>(v0, lane & 15, warp * 32 + __ffs(hit) - 1);
-            const float x = lane < 16 && v < V ? BeamVec<T>::one(x0 + v) : -INFINITY;
-            const bool in = x >= thr && x < kBeamMaxLogit && x > -INFINITY;
-            const unsigned put = __ballot_sync(0xffffffffu, in);
-            int at = 0;
-            if (lane == 0)
-                at = atomicAdd(&count, __popc(put));
-            at = __shfl_sync(0xffffffffu, at, 0) + __popc(put & ((1u << lane) - 1u));
-            if (in && at < kBeamBuf)
-                buf[at] = beam_key(x, v);
-        }
+        const bool hit = mine >= thr && mine > -INFINITY;
+        const unsigned all = __ballot_sync(0xffffffffu, hit);
+        const int place = hits + __popc(all & ((1u << lane) - 1u));
+        if (hit && place < kBeamHits)
+            listed[warp][place] = static_cast<uint16_t>(b << 5 | lane);
+        hits += __popc(all);
+    }
+    __syncwarp();
+    if (hits > kBeamHits) {
+        hits = 0;
+        if (lane == 0)
+            atomicAdd(&count, kBeamBuf + 1);  // as when the buffer is full
+    }
+    for (int i = 0; i < hits; i += 2) {
+        const int mine = i + (lane >> 4);
+        const int at_hit = mine < hits ? listed[warp][mine] : 0;
+        const int64_t v = beam_token<T>(begin + static_cast<int64_t>(at_hit >> 5) * kBeamBatch, lane & 15,
+                                        warp * 32 + (at_hit & 31));
+        const float x = mine < hits && v < V ? BeamVec<T>::one(x0 + v) : -INFINITY;
+        const bool in = x >= thr && x < kBeamMaxLogit && x > -INFINITY;
+        const unsigned put = __ballot_sync(0xffffffffu, in);
+        int at = 0;
+        if (lane == 0)
+            at = atomicAdd(&count, __popc(put));
+        at = __shfl_sync(0xffffffffu, at, 0) + __popc(put & ((1u << lane) - 1u));
+        if (in && at < kBeamBuf)
+            buf[at] = beam_key(x, v);
     }
     if (__any_sync(0xffffffffu, any_bad) && lane == 0 && status)
         atomicOr(status, kBeamDevBadLogit);
@@ -423,12 +454,23 @@ struct BeamOut {
     int64_t *next_token;
 };
 
-// A candidate of the merge: the FP64 total and the place (beam << 32 | token),
-// which orders as w * V + v does.
+// A candidate of the merge: its total as an unsigned integer of the same order, and
+// its place (beam << 32 | token), which orders as w * V + v does.
 struct BeamKey {
-    double total;
+    uint64_t total;
     int64_t at;
 };
+
+__device__ __forceinline__ uint64_t ordered64(double x)
+{
+    const uint64_t u = static_cast<uint64_t>(__double_as_longlong(x + 0.0));  // -0 as 0
+    return u ^ ((u >> 63) ? ~0ull : 0x8000000000000000ull);
+}
+
+__device__ __forceinline__ double from_ordered64(uint64_t k)
+{
+    return __longlong_as_double(static_cast<long long>(k ^ ((k >> 63) ? 0x8000000000000000ull : ~0ull)));
+}
 
 __device__ __forceinline__ bool ahead(const BeamKey &a, const BeamKey &b)
 {
@@ -488,7 +530,7 @@ __global__ void __launch_bounds__(kBeamThreads)
     auto key_of = [&](const Raw &r, BeamKey &k) -> bool {
         if (!(off[r.w] > -INFINITY) || !r.listed)
             return false;
-        k.total = off[r.w] + static_cast<double>(r.c.x);
+        k.total = ordered64(off[r.w] + static_cast<double>(r.c.x));
         k.at = (static_cast<int64_t>(r.w) << 32) | static_cast<uint32_t>(r.c.tok);
         return true;
     };
@@ -502,20 +544,26 @@ __global__ void __launch_bounds__(kBeamThreads)
         if (i < items)
             raw[j] = fetch(i);
     }
+    // A warp per beam.  Its score and a part per lane are fetched together; parts of
+    // beams that were not read hold anything, and are not used.
     for (int w = warp; w < W; w += kBeamWarps) {
+        const BeamPartial *pp = part + (n * W + w) * parts;
         const float sc = scores[n * W + w];
+        float ref = lane < parts ? pp[lane].ref : -INFINITY;
+        double sum = lane < parts ? pp[lane].sum : 0.0;
         double r = -INFINITY;
         if (beam_live(sc)) {
-            const BeamPartial *pp = part + (n * W + w) * parts;
-            float c = -INFINITY;
-            for (int k = lane; k < parts; k += 32)
+            float c = ref;
+            for (int k = lane + 32; k < parts; k += 32)
                 c = fmaxf(c, pp[k].ref);
             c = from_ordered(__reduce_max_sync(0xffffffffu, ordered(c)));
             if (c > -INFINITY) {
-                double s = 0.0;
-                for (int k = lane; k < parts; k += 32)
-                    if (pp[k].ref > -INFINITY)
-                        s += pp[k].sum * pow2(pp[k].ref - c);
+                double s = ref > -INFINITY ? sum * pow2(ref - c) : 0.0;
+                for (int k = lane + 32; k < parts; k += 32) {
+                    ref = pp[k].ref;
+                    if (ref > -INFINITY)
+                        s += pp[k].sum * pow2(ref - c);
+                }
                 s = warp_sum(s);
                 constexpr double kLn2 = 0.69314718055994530942;
                 r = static_cast<double>(sc) - (static_cast<double>(c) + log2(s)) * kLn2;
@@ -534,14 +582,15 @@ __global__ void __launch_bounds__(kBeamThreads)
 #pragma unroll
     for (int j = 0; j < HELD; ++j)
         if (key_of(raw[j], k))
-            best = fmaxf(best, __double2float_rd(k.total));
+            best = fmaxf(best, __double2float_rd(from_ordered64(k.total)));
     for (int i = tid + HELD * kBeamThreads; i < items; i += kBeamThreads)
         if (key_of(fetch(i), k))
-            best = fmaxf(best, __double2float_rd(k.total));
+            best = fmaxf(best, __double2float_rd(from_ordered64(k.total)));
     const float thr = block_threshold(best, C, red);
     if (best >= thr && best > -INFINITY) {
+        const uint64_t least = ordered64(static_cast<double>(thr));
         auto put = [&](const Raw &r) {
-            if (key_of(r, k) && k.total >= static_cast<double>(thr)) {
+            if (key_of(r, k) && k.total >= least) {
                 const int at = atomicAdd(&count, 1);
                 if (at < kBeamBuf)
                     buf[at] = k;
@@ -558,19 +607,18 @@ __global__ void __launch_bounds__(kBeamThreads)
     int kept;
     if (m <= kBeamBuf) {
         kept = m < C ? m : C;
-        for (int i = tid; i < m; i += kBeamThreads) {
-            const BeamKey c = buf[i];
-            int rank = 0;
-            for (int j = 0; j < m; ++j)
-                rank += ahead(buf[j], c);
-            if (rank < C)
+        for (int i0 = 0; i0 < m; i0 += kBeamThreads / 8) {
+            const int i = i0 + (tid >> 3);
+            const BeamKey c = i < m ? buf[i] : BeamKey{0, 0};
+            const int rank = beam_rank(tid & 7, m, [&](int j) { return ahead(buf[j], c); });
+            if (i < m && rank < C && (tid & 7) == 0)
                 sorted[rank] = c;
         }
         __syncthreads();
     } else {
-        BeamKey last{INFINITY, -1};
+        BeamKey last{~0ull, -1};
         for (kept = 0; kept < C; ++kept) {
-            BeamKey b{-INFINITY, INT64_MAX};
+            BeamKey b{0, INT64_MAX};
             for (int i = tid; i < items; i += kBeamThreads)
                 if (key_of(fetch(i), k) && ahead(last, k) && ahead(k, b))
                     b = k;
@@ -589,7 +637,7 @@ __global__ void __launch_bounds__(kBeamThreads)
                 if (ahead(win[i], b))
                     b = win[i];
             __syncthreads();
-            if (b.total == -INFINITY)
+            if (b.total == 0)
                 break;
             last = b;
             if (tid == 0)
@@ -597,44 +645,47 @@ __global__ void __launch_bounds__(kBeamThreads)
         }
         __syncthreads();
     }
-    auto token = [&](int i) -> int64_t { return sorted[i].at & 0xffffffff; };
-    for (int i = tid; i < C; i += kBeamThreads) {
+    // One warp writes, 32 candidates at a time: those that go on are numbered by
+    // the ones before them.
+    if (warp != 0)
+        return;
+    int gone_on = 0;
+    for (int i0 = 0; i0 < C; i0 += 32) {
+        const int i = i0 + lane;
         const bool have = i < kept;
-        const int32_t beam = have ? static_cast<int32_t>(sorted[i].at >> 32) : -1;
-        const int64_t tok = have ? token(i) : -1;
-        const float sc = have ? static_cast<float>(sorted[i].total) : -INFINITY;
-        o.cand_score[n * C + i] = sc;
-        o.cand_beam[n * C + i] = beam;
-        o.cand_token[n * C + i] = tok;
-        if (o.next_score && have && tok != eos) {
-            int before = 0;  // candidates ahead of this one that do not end their sequence
-            for (int j = 0; j < i; ++j)
-                before += token(j) != eos;
-            if (before < W) {
-                o.next_score[n * W + before] = sc;
-                o.next_beam[n * W + before] = beam;
-                o.next_token[n * W + before] = tok;
-            }
+        const BeamKey c = have ? sorted[i] : BeamKey{0, -1};
+        const int32_t beam = have ? static_cast<int32_t>(c.at >> 32) : -1;
+        const int64_t tok = have ? c.at & 0xffffffff : -1;
+        const float sc = have ? static_cast<float>(from_ordered64(c.total)) : -INFINITY;
+        if (i < C) {
+            o.cand_score[n * C + i] = sc;
+            o.cand_beam[n * C + i] = beam;
+            o.cand_token[n * C + i] = tok;
         }
+        const bool on = have && tok != eos;
+        const unsigned all = __ballot_sync(0xffffffffu, on);
+        const int place = gone_on + __popc(all & ((1u << lane) - 1u));
+        if (o.next_score && on && place < W) {
+            o.next_score[n * W + place] = sc;
+            o.next_beam[n * W + place] = beam;
+            o.next_token[n * W + place] = tok;
+        }
+        gone_on += __popc(all);
     }
-    if (o.next_score && warp == 0) {
+    if (o.next_score)
         // places that no candidate fills: a dead beam that stays where it is
-        int live = 0;
-        for (int i = lane; i < kept; i += 32)
-            live += token(i) != eos;
-        live = __reduce_add_sync(0xffffffffu, live);
-        for (int w = live + lane; w < W; w += 32) {
+        for (int w = gone_on + lane; w < W; w += 32) {
             o.next_score[n * W + w] = -INFINITY;
             o.next_beam[n * W + w] = w;
             o.next_token[n * W + w] = eos < 0 ? 0 : eos;
         }
-    }
 }
 
 // ---------------------------------------------------------------- reorder
 
 constexpr int kReorderMaxStates = 128;
 constexpr int kReorderThreads = 256;
+constexpr int kReorderColumns = 2;  // columns a thread has under way at once
 
 struct ReorderParams {
     uint8_t *state[kReorderMaxStates];
@@ -649,10 +700,12 @@ struct ReorderParams {
 };
 
 // state[.., n, w, ..] = old state[.., n, parents[n][w], ..], in place: a thread
-// owns one vector-wide column of an entry, reads what every beam whose parent
+// owns vector-wide columns of an entry, reads what every beam whose parent
 // is another takes over, and only then writes.  No row that stays is touched,
 // and a row that several beams take is read from memory once (L1 serves the
-// rest), so the traffic is the rows wanted plus the rows changed.
+// rest), so the traffic is the rows wanted plus the rows changed: bound by HBM (16
+// caches of 16 x 4 beams, 2.8 GB moved: 395 us; 489 us with one column under way
+// per thread instead of two).
 // MAXW bounds W at compile time, so that the column's values stay in registers:
 // vectors of 16 bytes up to 16 beams, 8 up to 32, 4 up to 64.
 template <typename VecT, int MAXW>
@@ -678,23 +731,33 @@ __global__ void __launch_bounds__(kReorderThreads)
     if (!__syncthreads_or(moves))
         return;
     uint8_t *base = p.state[blockIdx.z] + n * p.entry_stride;
-    for (uint32_t c = blockIdx.x * kReorderThreads + threadIdx.x; c < p.columns;
-         c += gridDim.x * kReorderThreads) {
-        uint32_t r = c / p.run_vecs;
-        const uint32_t v = c - r * p.run_vecs;
-        const uint32_t r1 = r / p.outer[0], i0 = r - r1 * p.outer[0];
-        const uint32_t i2 = r1 / p.outer[1], i1 = r1 - i2 * p.outer[1];
-        uint8_t *col = base + i0 * p.outer_stride[0] + i1 * p.outer_stride[1] + i2 * p.outer_stride[2] +
-                       static_cast<int64_t>(v) * sizeof(VecT);
-        VecT x[MAXW];
+    constexpr int U = kReorderColumns;
+    const uint32_t step = gridDim.x * kReorderThreads;
+    for (uint32_t c0 = blockIdx.x * kReorderThreads + threadIdx.x; c0 < p.columns; c0 += U * step) {
+        uint8_t *col[U];
+        VecT x[U][MAXW];
 #pragma unroll
-        for (int w = 0; w < MAXW; ++w)
-            if (w < p.W && from[w] != w)
-                x[w] = *reinterpret_cast<const VecT *>(col + from[w] * p.beam_stride);
+        for (int k = 0; k < U; ++k) {
+            const uint32_t c = c0 + k * step;
+            const uint32_t r = c / p.run_vecs, v = c - r * p.run_vecs;
+            const uint32_t r1 = r / p.outer[0], i0 = r - r1 * p.outer[0];
+            const uint32_t i2 = r1 / p.outer[1], i1 = r1 - i2 * p.outer[1];
+            col[k] = c < p.columns ? base + i0 * p.outer_stride[0] + i1 * p.outer_stride[1] +
+                                         i2 * p.outer_stride[2] + static_cast<int64_t>(v) * sizeof(VecT)
+                                   : nullptr;
+        }
 #pragma unroll
-        for (int w = 0; w < MAXW; ++w)
-            if (w < p.W && from[w] != w)
-                *reinterpret_cast<VecT *>(col + w * p.beam_stride) = x[w];
+        for (int k = 0; k < U; ++k)
+#pragma unroll
+            for (int w = 0; w < MAXW; ++w)
+                if (col[k] && w < p.W && from[w] != w)
+                    x[k][w] = *reinterpret_cast<const VecT *>(col[k] + from[w] * p.beam_stride);
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+#pragma unroll
+            for (int w = 0; w < MAXW; ++w)
+                if (col[k] && w < p.W && from[w] != w)
+                    *reinterpret_cast<VecT *>(col[k] + w * p.beam_stride) = x[k][w];
     }
 }
 

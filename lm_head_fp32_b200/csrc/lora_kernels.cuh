@@ -80,14 +80,19 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 // eight rows of an ldmatrix lie in different banks.
 constexpr int pad_row(int elems) { return elems * 2 + 16; }
 
+// Column blocks under way: as many as leave room for two CTAs per SM (three of the
+// smallest).
+constexpr int rows_stages(int nt) { return nt == 2 ? 4 : 3; }
+
 template <bool P_MN, int NT>
 struct RowsCfg {
+    static constexpr int STAGES = rows_stages(NT);
     static constexpr int RB = NT * 16;
     static constexpr int Y_ROW = pad_row(kRowsSub);
     static constexpr int Y_BYTES = kRowsTokens * Y_ROW;
     static constexpr int P_ROW = P_MN ? pad_row(RB) : pad_row(kRowsSub);
     static constexpr int P_BYTES = (P_MN ? kRowsSub : RB) * P_ROW;
-    static constexpr int SMEM = 3 * (Y_BYTES + P_BYTES);
+    static constexpr int SMEM = STAGES * (Y_BYTES + P_BYTES);
 };
 
 // partial[range][i][r]: the range's share of t.  Y [M][Cdim] BF16; P_MN: P
@@ -111,7 +116,7 @@ __global__ void __launch_bounds__(kRowsThreads)
     __shared__ int32_t toks[kRowsTokens];
     __shared__ int32_t list[kRowsTokens];
     __shared__ int warp_n[2];
-    uint8_t *ybuf = smem, *pbuf = smem + 3 * G::Y_BYTES;
+    uint8_t *ybuf = smem, *pbuf = smem + G::STAGES * G::Y_BYTES;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t i0 = static_cast<int64_t>(blockIdx.y) * kRowsTokens;
     const int r0 = static_cast<int>(blockIdx.z) / groups * kRankBlock;
@@ -196,7 +201,7 @@ __global__ void __launch_bounds__(kRowsThreads)
         if (lt < steps) {
             const int64_t left = Cdim - (sub0 + ls) * kRowsSub;  // columns from here to the end
             if (lj == 0) {
-                uint8_t *y = ybuf + (ls % 3) * G::Y_BYTES + yr * G::Y_ROW + yc * 16;
+                uint8_t *y = ybuf + (ls % G::STAGES) * G::Y_BYTES + yr * G::Y_ROW + yc * 16;
                 const bool inc = yc * 8 < left;
 #pragma unroll
                 for (int i = 0; i < kRowsTokens / 8; ++i) {
@@ -204,7 +209,7 @@ __global__ void __launch_bounds__(kRowsThreads)
                     cp16(y + i * 8 * G::Y_ROW, in ? ysrc[i] + ls * kRowsSub : Y, in);
                 }
             }
-            uint8_t *pb = pbuf + (lt % 3) * G::P_BYTES;
+            uint8_t *pb = pbuf + (lt % G::STAGES) * G::P_BYTES;
             const __nv_bfloat16 *base = P + static_cast<int64_t>(list[lj]) * R * Cdim + ls * pstep;
 #pragma unroll
             for (int i = 0; i < 2 * NT; ++i) {
@@ -222,11 +227,12 @@ __global__ void __launch_bounds__(kRowsThreads)
     };
     const int g = lane >> 2;  // this thread's rows of the warp's 16: g and g + 8
     const int id0 = ids[warp * 16 + g], id1 = ids[warp * 16 + g + 8];
-    load();
-    load();
+#pragma unroll
+    for (int i = 0; i < G::STAGES - 1; ++i)
+        load();
     int sub = 0, j = -1;
     for (int t = 0; t < steps; ++t) {
-        cp_wait<1>();
+        cp_wait<G::STAGES - 2>();
         __syncthreads();  // step t has landed; the buffers of step t - 1 are free
         load();
         if (++j == nslot) {
@@ -237,8 +243,8 @@ __global__ void __launch_bounds__(kRowsThreads)
         const bool k0 = id0 == a, k1 = id1 == a;
         if (!__any_sync(0xffffffffu, k0 || k1))
             continue;
-        const uint8_t *y = ybuf + (sub % 3) * G::Y_BYTES;
-        const uint8_t *pb = pbuf + (t % 3) * G::P_BYTES;
+        const uint8_t *y = ybuf + (sub % G::STAGES) * G::Y_BYTES;
+        const uint8_t *pb = pbuf + (t % G::STAGES) * G::P_BYTES;
         float part[2 * NT][4];
 #pragma unroll
         for (int n = 0; n < 2 * NT; ++n)
