@@ -282,7 +282,7 @@ LMH_API lmh_status_t lmhead_bwd_dw_acc(const void *dlogits, const void *X, float
  *   adapters that occur in it).
  *   workspace: device scratch of lmhead_lora_workspace_bytes(M, K, V, R, N)
  *   bytes, 256-byte aligned; its contents do not matter before or after.
- *   Requirements: K % 8 == 0, R % 8 == 0, R <= 256, N <= 65535, M <= 4194240;
+ *   Requirements: K % 8 == 0, R % 8 == 0, R <= 256, N <= 65535, M <= 4194240, M N <= 2^34;
  *   X, W, A, B, u 16-byte aligned; logits aligned to its element.
  *   Deterministic. */
 LMH_API lmh_status_t lmhead_fwd_lora(const void *X, const void *W, const void *A, const void *B,
@@ -298,7 +298,8 @@ LMH_API int64_t lmhead_lora_workspace_bytes(int64_t M, int64_t K, int64_t V, int
 /* The input gradient of lmhead_fwd_lora:
  *   g[i,:]  = scale[a] dlogits[i,:] . B_a          (written, [M,R] FP32)
  *   dX[i,:] = dlogits[i,:] . W + g[i,:] . A_a      (FP32 or BF16)
- * summed as in lmhead_fwd_lora.  Requirements as there, and V % 8 == 0,
+ * summed as in lmhead_fwd_lora (FP32 dX: every 512 terms of V).  Requirements
+ * as there, and V % 8 == 0,
  * dlogits, g and dX 16-byte aligned.  Deterministic. */
 LMH_API lmh_status_t lmhead_bwd_dx_lora(const void *dlogits, const void *W, const void *A,
                                         const void *B, const float *scale, const int32_t *adapter,

@@ -42,13 +42,18 @@
 
 namespace lmh {
 
-// k-blocks of 64 per tensor-memory accumulation.  FP32 outputs: 12 (768 terms)
-// keep the error of a product at 7.1e-7 of its norm at any length (8: 4.7e-7,
-// 16: 1.0e-6, one accumulation of 4096 terms: 4.4e-6, of 32768: 3.8e-5; an FP32
-// product on the CUDA cores: 6.1e-7 at 4096).  A switch of accumulators costs the
-// tensor pipe about 0.2 us: 4096 x 4096 x 128256 takes 3163, 3101, 3043 us with 8,
-// 12, 16 and 2966 without.  BF16 outputs round at 2e-3, so 64 (4e-6) do.
-__host__ __device__ constexpr int promote_kblocks(int out_bytes) { return out_bytes == 4 ? 12 : 64; }
+// k-blocks of 64 per tensor-memory accumulation.  FP32 logits: 12 (768 terms) keep
+// the error of a product at 7.1e-7 of its norm at any length (8: 4.7e-7, 16:
+// 1.0e-6, one accumulation of 4096 terms: 4.4e-6, of 32768: 3.8e-5; an FP32 product
+// on the CUDA cores: 6.1e-7 at 4096).  A switch of accumulators costs the tensor
+// pipe about 0.2 us: 4096 x 4096 x 128256 takes 3163, 3101, 3043 us with 8, 12, 16
+// and 2966 without.  FP32 dX: 8, because dlogits has one large term per row, the
+// target's, after which every MMA loses its share of the whole sum (9.8e-7 with
+// 12).  BF16 outputs round at 2e-3, so 64 (4e-6) do.
+__host__ __device__ constexpr int promote_kblocks(int out_bytes, bool gradient)
+{
+    return out_bytes == 4 ? (gradient ? 8 : 12) : 64;
+}
 
 constexpr int kSlotMaskWords = 8;  // one bit per token of a tile of up to 256
 
@@ -102,7 +107,7 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
     constexpr bool IN_REGS = BN <= 128;
     constexpr uint32_t TMEM_COLS = lora_tmem_cols(BN);
     static_assert(RES * TMEM_COLS <= 512, "tensor memory of the resident CTAs");
-    constexpr int kPromote = promote_kblocks(sizeof(OutT));
+    constexpr int kPromote = promote_kblocks(sizeof(OutT), A_MN);
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));

@@ -4,8 +4,10 @@
 //   cols   D_a[c, r]    = sum_{i of a} Y[i, c] t[i, r] one matrix per adapter: dB = dl^T u, dA = g^T X
 //
 // Both stream Y (dlogits: 1 GB at 4096 x 128256) through shared memory once with
-// cp.async and are bound by that: 2 to 8 MMAs per 512 bytes read, so mma.sync on
-// register fragments keeps up, and nothing needs tensor memory.
+// cp.async.  With 2 to 12 MMAs per 512 bytes read, mma.sync on register fragments
+// nearly keeps up with that stream and needs no tensor memory (rank 32 at that
+// size: rows 236 us, columns 294 us, 4.5 and 3.6 TB/s; the columns' three parts
+// keep the mma.sync pipe half busy).
 //
 //   lora_rows_kernel    64 tokens x a range of c; a partial t per range.  For
 //                       each adapter among the tokens the product of all 64 is
@@ -35,7 +37,7 @@ constexpr int kRankBlock = 64;     // ranks of one CTA (grid.z takes the others)
 constexpr int kColsTile = 128;     // columns of Y of one lora_cols_kernel CTA
 constexpr int kColsTokens = 32;    // tokens staged at once
 constexpr int kColsThreads = 128;
-constexpr int kColsStages = 4;
+constexpr int kColsStages = 3;
 constexpr int kColsPromote = 8;    // stages (256 tokens) summed in the MMAs
 constexpr int kExpandTokens = 4;  // tokens of one lora_expand_kernel CTA
 constexpr int kDevBadAdapter = 0x8;  // LMH_DEV_BAD_ADAPTER
@@ -80,13 +82,9 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 // eight rows of an ldmatrix lie in different banks.
 constexpr int pad_row(int elems) { return elems * 2 + 16; }
 
-// Column blocks under way: as many as leave room for two CTAs per SM (three of the
-// smallest).
-constexpr int rows_stages(int nt) { return nt == 2 ? 4 : 3; }
-
 template <bool P_MN, int NT>
 struct RowsCfg {
-    static constexpr int STAGES = rows_stages(NT);
+    static constexpr int STAGES = 2;  // blocks under way; a third costs a resident CTA
     static constexpr int RB = NT * 16;
     static constexpr int Y_ROW = pad_row(kRowsSub);
     static constexpr int Y_BYTES = kRowsTokens * Y_ROW;

@@ -253,9 +253,7 @@ def gemm_watchdog_selftest(X: torch.Tensor, W: torch.Tensor, logits: torch.Tenso
     assert W.shape[1] == K and tuple(logits.shape) == (M, V) and logits.dtype == torch.float32
     _check(lib().lmh_gemm_watchdog_selftest(_ptr(X), _ptr(W), _ptr(logits), M, K, V,
                                             int(limit_ns), _ptr(status), _stream(stream)),
-           "lmh_gemm_watchdog_selftest", "beam_select", "beam_select_workspace_bytes",
-           "beam_reorder", "lmhead_fwd_lora", "lmhead_lora_workspace_bytes", "lmhead_bwd_dx_lora",
-           "lmhead_bwd_lora")
+           "lmh_gemm_watchdog_selftest")
 
 
 def lmhead_bwd_dw_acc(dlogits: torch.Tensor, X: torch.Tensor, dW: torch.Tensor,

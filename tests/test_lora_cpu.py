@@ -29,7 +29,7 @@ def grad(**kw):
 
 
 BAD_DIMS = [dict(M=0), dict(K=0), dict(V=0), dict(R=0), dict(N=0), dict(R=264), dict(N=65536),
-            dict(M=65535 * 64 + 1), dict(V=1 << 31), dict(nbytes=1000)]
+            dict(M=65535 * 64 + 1), dict(M=1 << 20, N=1 << 15), dict(V=1 << 31), dict(nbytes=1000)]
 
 
 @pytest.mark.parametrize("fn", ["lmhead_fwd_lora", "lmhead_bwd_dx_lora"])

@@ -4,8 +4,9 @@ Tolerances, per element, with S the sum of the absolute values of the terms:
 
   GEMM sums, FP32 output: per 768 terms (48 MMAs) the tensor cores lose at most
     2^-23 of the running sum per MMA and about four such inside one, then the
-    parts are added in FP32: 2^-23 * (52 + terms / 1536) * S.  BF16 output: per
-    4096 terms (256 MMAs): 2^-23 * (260 + terms / 8192) * S.
+    parts are added in FP32: 2^-23 * (52 + terms / 1536) * S; dX per 512 terms (32
+    MMAs): 2^-23 * (36 + terms / 1024) * S.  BF16 output: per 4096 terms (256
+    MMAs): 2^-23 * (260 + terms / 8192) * S.
   row sums (u, g): the same per 128 terms (8 MMAs), parts added in FP64 or FP32,
     one rounding: 2^-23 * (12 + terms / 256) * S.
   u in the second product, above 128 tokens: for an FP32 output two BF16 parts,
@@ -69,8 +70,9 @@ def per_token(ids, N):
             yield a, at
 
 
-def gemm_eps(terms, dtype=torch.float32):
-    return E23 * (52 + terms / 1536 if dtype == torch.float32 else 260 + terms / 8192)
+def gemm_eps(terms, dtype=torch.float32, chunk=768):
+    chunk = chunk if dtype == torch.float32 else 4096
+    return E23 * (chunk / 16 + 4 + terms / (2 * chunk))
 
 
 def split_eps(M, dtype):
@@ -121,6 +123,22 @@ def test_forward(M, K, V, R, N, order, dtype):
     close(u, ru, tu, "u")
     close(logits, rl, tl, "logits")
     assert int(st.item()) == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("R", [8, 32, 64, 136])
+def test_forward_tiles_of_one_adapter(R, dtype):
+    """Tiles whose tokens all have one adapter take it in the shared product's sums, the
+    last one with fewer tokens than columns; others beside them do not."""
+    M, K, V = 1100, 264, 1030
+    X, W, A, B, scale, _ = make(M, K, V, R, 3)
+    ids = torch.zeros(M, dtype=torch.int32, device=DEV)
+    for i, a in ((256, 1), (512, 2), (700, -1), (768, 1)):  # tiles 0, 1, 3 and 4 of one adapter
+        ids[i:] = a
+    logits, u = fwd(X, W, A, B, scale, ids, dtype)
+    ru, tu, rl, tl = ref_fwd(X, W, A, B, scale, ids, dtype)
+    close(u, ru, tu, "u")
+    close(logits, rl, tl, "logits")
 
 
 @pytest.mark.parametrize("M,K", [(300, 4096), (20, 4096), (256, 16384), (64, 8192)])
@@ -235,7 +253,7 @@ def check_bwd(M, K, V, R, N, order, dtype, seed=0):
     assert int(st.item()) == 0
     Xd, Wd, Ad, Bd, sd, dd, ud = (t.double() for t in (X, W, A, B, scale, dl, u))
     rg, tg = (torch.zeros((M, R), dtype=torch.float64, device=DEV) for _ in range(2))
-    rX, tX = dd @ Wd, gemm_eps(V, dtype) * (dd.abs() @ Wd.abs())
+    rX, tX = dd @ Wd, gemm_eps(V, dtype, 512) * (dd.abs() @ Wd.abs())
     for a in range(N):
         at = torch.nonzero(ids == a).view(-1)
         rg[at] = sd[a] * (dd[at] @ Bd[a])
@@ -258,6 +276,7 @@ def check_bwd(M, K, V, R, N, order, dtype, seed=0):
     (64, 1024, 2048, 16, 64), (129, 264, 512, 16, 9), (300, 136, 256, 48, 300), (513, 512, 776, 128, 4),
     (260, 72, 1280, 256, 2), (1000, 320, 4096, 72, 6), (70, 128, 20000, 64, 3), (1100, 256, 1024, 16, 1),
     (530, 64, 65536, 24, 7),  # the rows taken adapter by adapter
+    (1500, 4096, 512, 16, 2),  # several tiles per CTA, tiles of one adapter
 ])
 def test_backward(M, K, V, R, N, order):
     check_bwd(M, K, V, R, N, order, torch.bfloat16 if M % 2 else torch.float32)
