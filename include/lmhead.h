@@ -353,7 +353,7 @@ LMH_API lmh_status_t beam_select(const void *logits, int32_t logits_dtype, const
                                  int32_t *status, lmh_stream_t stream);
 
 /* Scratch bytes beam_select needs: 16 + 8 C bytes per part of a row, a part being
- * 4096 to 65536 logits, the longer the more rows there are.  -1 for sizes out of
+ * 4096 to 32768 logits, the longer the more rows there are.  -1 for sizes out of
  * range. */
 LMH_API int64_t beam_select_workspace_bytes(int64_t N, int64_t W, int64_t V, int64_t C);
 

@@ -32,8 +32,8 @@ constexpr int kBeamThreads = 256;
 constexpr int kBeamWarps = kBeamThreads / 32;
 constexpr int kBeamPerThread = 16;                         // logits of a batch, per thread
 constexpr int kBeamBatch = kBeamThreads * kBeamPerThread;  // logits of a batch
-constexpr int kBeamMaxBatches = 16;                        // batches of a part, at most
-constexpr int kBeamBuf = 1024;        // candidates at or above the threshold a CTA can hold
+constexpr int kBeamMaxBatches = 8;                        // batches of a part, at most
+constexpr int kBeamBuf = 512;        // candidates at or above the threshold a CTA can hold
 constexpr int kBeamHits = 128;        // sixteens at or above it that a warp can list
 constexpr int kBeamMaxCand = 128;
 constexpr int kBeamMaxWidth = 64;

@@ -386,7 +386,7 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, cand_score: torch.Te
         ("next_score", next_score, nw, _F32), ("next_beam", next_beam, nw, _I32),
         ("next_token", next_token, nw, _I64), ("status", status, (1,), _I32))
     code = _on(dev, stream, lib().beam_select, lg, F32 if logits.dtype is torch.float32 else BF16,
-               *ptrs, wp, wn, N, W, V, nc[1], eos, st)
+               *ptrs, wp, wn, N, W, V, nc[1], int(eos), st)
     if code:
         raise LmhError(code, "beam_select")
     return cand_score, cand_beam, cand_token, next_score, next_beam, next_token
@@ -438,9 +438,12 @@ def beam_reorder(states, parents: torch.Tensor, entry_dim: int = 0,
     if 0 in shape:
         return states
     run, outer, outer_strides = _state_geometry(shape, strides, es, entry_dim)
+    addresses = [t.data_ptr() for t in states]
+    if len(set(addresses)) < len(addresses):
+        raise ValueError("a state is given twice")
     for i in range(0, len(states), 128):
-        part = states[i:i + 128]
-        ptrs = (ctypes.c_void_p * len(part))(*[t.data_ptr() for t in part])
+        part = addresses[i:i + 128]
+        ptrs = (ctypes.c_void_p * len(part))(*part)
         code = _on(dev, stream, lib().beam_reorder, ptrs, len(part), pp, N, W, strides[entry_dim] * es,
                    strides[entry_dim + 1] * es, run, outer, outer_strides, len(outer), sp)
         if code:

@@ -161,7 +161,8 @@ def lm_head_lora_cross_entropy(X: torch.Tensor, W: torch.Tensor, A: torch.Tensor
     bfloat16, scale: [N] float32 (no gradient), adapter: [M] int32, -1 for a token
     without adapter.  The backward gives X, A, B and, where it asks for one (a frozen
     head does not), W bfloat16 gradients; the adapters' are summed in FP32 and
-    rounded once."""
+    rounded once.  A backward that accumulates into .grad can be captured into a CUDA
+    graph while no eager graph of the same leaves is alive (autograd's own limit)."""
     _check_inputs(X, W, target)
     if A.dim() != 3 or B.dim() != 3 or A.dtype != torch.bfloat16 or B.dtype != torch.bfloat16:
         raise ValueError("expected bfloat16 A [N,R,K] and B [N,V,R]")

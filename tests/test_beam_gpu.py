@@ -107,6 +107,28 @@ def test_equal_logits_fall_by_place(V):
     check(x, torch.zeros(2, 3, device=DEV), 6, eos=1)
 
 
+def test_equal_logits_in_long_parts():
+    # parts of several batches: more sixteens at the threshold than a warp can list
+    N, V, C = 64, 300001, 6
+    got = run_select(torch.full((N, 1, V), -0.5, device=DEV), torch.zeros(N, 1, device=DEV), C)
+    lse = -0.5 + torch.tensor(float(V)).double().log()
+    assert torch.equal(got[2].cpu(), torch.arange(C).repeat(N, 1)) and not got[1].any()
+    assert ((got[0].cpu().double() - (-0.5 - lse)).abs() <= 2.0 ** -24 * 13 + 2e-6).all()
+
+
+def test_few_tokens_allowed_in_long_parts():
+    N, V, C = 64, 300001, 4
+    x = torch.full((N, 1, V), NEG, device=DEV)
+    at = torch.tensor([3, 70000, 299999], device=DEV) + torch.arange(N, device=DEV)[:, None] % 2
+    x.scatter_(2, at[:, None], torch.tensor([1.0, 3.0, 2.0], device=DEV).expand(N, 1, 3).contiguous())
+    got = run_select(x, torch.zeros(N, 1, device=DEV), C)
+    ref = torch.tensor([3.0, 2.0, 1.0]).double().log_softmax(0)
+    for n in range(N):
+        assert got[2][n].tolist() == [int(at[n, 1]), int(at[n, 2]), int(at[n, 0]), -1]
+        assert ((got[0][n, :3].cpu().double() - ref).abs() <= 2.0 ** -24 * 3 + 2e-6).all()
+        assert got[0][n, 3].item() == NEG
+
+
 @pytest.mark.parametrize("V", [4001, 32771])
 def test_equal_beams_fall_by_beam(V):
     x, _ = data(2, 1, V, 3)
@@ -277,7 +299,7 @@ def test_overlapping_state_is_refused():
     t = torch.zeros(8, device=DEV)
     with pytest.raises(lmhead.LmhError):
         lmhead.beam_reorder(t.expand(2, 3, 8), par)
-    with pytest.raises(lmhead.LmhError):
+    with pytest.raises(ValueError, match="twice"):
         lmhead.beam_reorder([torch.zeros((2, 3, 8), device=DEV)] * 2, par)
 
 

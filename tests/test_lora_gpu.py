@@ -105,6 +105,7 @@ def close(got, ref, tol, what):
 
 
 SHAPES = [  # M, K, V, R, N
+    (2, 8, 1, 8, 1), (130, 8, 9, 8, 2),
     (1, 64, 256, 8, 1), (1, 4096, 1000, 16, 3), (3, 72, 130, 8, 2), (16, 512, 300, 24, 5),
     (17, 200, 515, 16, 4), (33, 520, 1031, 32, 40), (64, 1024, 2048, 16, 64), (100, 256, 700, 40, 7),
     (128, 640, 384, 64, 3), (129, 264, 512, 16, 9), (256, 4096, 512, 8, 2), (300, 136, 255, 48, 300),
@@ -272,6 +273,7 @@ def check_bwd(M, K, V, R, N, order, dtype, seed=0):
 
 @pytest.mark.parametrize("order", ["random", "runs"])
 @pytest.mark.parametrize("M,K,V,R,N", [
+    (2, 8, 8, 8, 1), (130, 8, 16, 8, 2),
     (1, 64, 256, 8, 1), (3, 72, 136, 8, 2), (16, 512, 304, 24, 5), (33, 520, 1032, 32, 40),
     (64, 1024, 2048, 16, 64), (129, 264, 512, 16, 9), (300, 136, 256, 48, 300), (513, 512, 776, 128, 4),
     (260, 72, 1280, 256, 2), (1000, 320, 4096, 72, 6), (70, 128, 20000, 64, 3), (1100, 256, 1024, 16, 1),
