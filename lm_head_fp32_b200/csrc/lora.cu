@@ -108,6 +108,34 @@ GradSpace grad_space(int64_t M, int64_t R, int64_t N)
     return g;
 }
 
+// The tiles of dX's last wave that are split in two, each unit (CTA pair) that the
+// wave leaves idle taking `rounds` short parts: as lmhead_bwd_dx, where the rule is
+// explained and measured.
+struct DxSplit {
+    int64_t tiles = 0, kb = 0, rounds = 0;
+    int64_t scratch_bytes() const { return tiles * 2 * 256 * 256 * 4; }
+};
+constexpr int64_t kMaxSplitRounds = 8;
+DxSplit dx_split(int64_t M, int64_t K, int64_t V)
+{
+    DxSplit s;
+    if (M <= 128 || K < 256)
+        return s;
+    const int64_t units = num_sms() / 2, tiles = ceil_div(K, 256) * ceil_div(M, 256);
+    const int64_t rem = tiles % units, num_kb = ceil_div(V, lmh::kBlockK);
+    if (num_kb < 2 || rem == 0)
+        return s;
+    const int64_t spare = units - rem, k = ceil_div(rem, spare);
+    const int64_t B = (num_kb * k + k) / (k + 1);  // ceil(num_kb k / (k + 1))
+    const int64_t span = B > k * (num_kb - B) ? B : k * (num_kb - B);
+    if ((k == 1 || tiles > units) && k <= kMaxSplitRounds && B < num_kb && 10 * span <= 9 * num_kb) {
+        s.tiles = rem;
+        s.kb = B;
+        s.rounds = k;
+    }
+    return s;
+}
+
 bool lora_dims_ok(int64_t M, int64_t K, int64_t V, int64_t R, int64_t N)
 {
     return dims_ok(M, K, V) && M <= kMaxTokens && R >= 1 && R <= kMaxRank && N >= 1 && N <= kMaxAdapters &&
@@ -151,11 +179,13 @@ struct AdapterOperands {
     uint64_t inner, mid, N;
     const void *ux;           // the split u of every token tile
     uint64_t ux_rows;
+    float *scratch;           // the parts of split tiles
 };
 
 template <int BN, bool A_MN, typename OutT, bool TMA_STORE, bool PAIR, int RES>
 lmh_status_t launch_impl(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &tc, const CUtensorMap &ts,
-                         const CUtensorMap &tu, GemmParams p, const LoraParams &q, cudaStream_t stream)
+                         const CUtensorMap &tu, const CUtensorMap &tp, GemmParams p, const LoraParams &q,
+                         cudaStream_t stream)
 {
     constexpr int EW = lmh::lora_epi_warps(BN);
     using C = GemmCfg<BN, A_MN, false, PAIR, RES, EW>;
@@ -170,18 +200,19 @@ lmh_status_t launch_impl(const CUtensorMap &ta, const CUtensorMap &tb, const CUt
     if (tiles > kMaxDim)
         return LMH_ERR_INVALID_ARG;
     const int64_t units = RES == 1 ? num_sms() / C::CTAS : tiles;
-    const int grid = static_cast<int>((tiles < units ? tiles : units) * C::CTAS);
+    const int64_t items = p.split_tiles > 0 ? tiles - p.split_tiles + units * p.split_rounds : tiles;
+    const int grid = static_cast<int>((items < units ? items : units) * C::CTAS);
     return launch_ex(kern, dim3(grid), dim3(C::THREADS), C::SMEM_BYTES, stream, PAIR ? 2u : 1u, ta, tb, tc, ts,
-                     tu, p, q);
+                     tu, tp, p, q);
 }
 
 // A: the shared weights [outer][inner], MN-major (dX) or K-major; B: [Ndim][Kdim].
 template <int BN, bool A_MN, typename OutT, bool PAIR, int RES = 1>
 lmh_status_t launch_lora(const void *a, uint64_t a_inner, uint64_t a_outer, const void *b, const AdapterOperands &ad,
-                         const GemmParams &p, const LoraParams &q, cudaStream_t stream)
+                         GemmParams p, const LoraParams &q, cudaStream_t stream)
 {
     using C = GemmCfg<BN, A_MN, false, PAIR, RES, lmh::lora_epi_warps(BN)>;
-    CUtensorMap ta, tb, tc, ts, tu;
+    CUtensorMap ta, tb, tc, ts, tu, tp;
     if (!make_map(&ta, a, a_inner, a_outer, 64, A_MN ? lmh::kBlockK : lmh::kBlockM) ||
         !make_map(&tb, b, static_cast<uint64_t>(p.Kdim), static_cast<uint64_t>(p.Ndim), lmh::kBlockK, C::BN_CTA))
         return LMH_ERR_CUDA;
@@ -190,13 +221,28 @@ lmh_status_t launch_lora(const void *a, uint64_t a_inner, uint64_t a_outer, cons
     if (BN > 128 && (!make_map3(&ts, ad.base, ad.inner, ad.mid, ad.N, A_MN ? lmh::kBlockK : lmh::kBlockM) ||
                      !make_map(&tu, ad.ux, 64, ad.ux_rows, 64, C::BN_CTA)))
         return LMH_ERR_CUDA;
+    std::memset(&tp, 0, sizeof tp);
+    if constexpr (!(A_MN && PAIR))
+        p.split_tiles = 0;
+    if (p.split_tiles > 0 && !make_out_map(&tp, ad.scratch, false, 256, static_cast<uint64_t>(p.split_tiles) * 2 * 256,
+                                           256, C::EPI_CHUNK))
+        return LMH_ERR_CUDA;
     if (make_out_map(&tc, p.out, sizeof(OutT) == 2, static_cast<uint64_t>(p.Mdim), static_cast<uint64_t>(p.Ndim),
                      static_cast<uint64_t>(p.ldo), C::EPI_CHUNK))
-        return launch_impl<BN, A_MN, OutT, true, PAIR, RES>(ta, tb, tc, ts, tu, p, q, stream);
+    {
+        const lmh_status_t r = launch_impl<BN, A_MN, OutT, true, PAIR, RES>(ta, tb, tc, ts, tu, tp, p, q, stream);
+        if (r != LMH_OK || p.split_tiles == 0)
+            return r;
+        p.num_m_tiles = static_cast<int32_t>(ceil_div(p.Mdim, 256));
+        p.num_n_tiles = static_cast<int32_t>(ceil_div(p.Ndim, 256));
+        return launch_ex(lmh::lora_join_kernel<OutT>, dim3(static_cast<unsigned>(p.split_tiles), 256 / lmh::kJoinRows),
+                         dim3(256), 0, stream, 1u, static_cast<const float *>(ad.scratch), static_cast<OutT *>(p.out), p,
+                         p.num_m_tiles * p.num_n_tiles - p.split_tiles);
+    }
     if constexpr (A_MN)
         return LMH_ERR_MISALIGNED;  // dX rows are multiples of 16 bytes and its base is checked
     std::memset(&tc, 0, sizeof tc);
-    return launch_impl<BN, A_MN, OutT, A_MN, PAIR, RES>(ta, tb, tc, ts, tu, p, q, stream);
+    return launch_impl<BN, A_MN, OutT, A_MN, PAIR, RES>(ta, tb, tc, ts, tu, tp, p, q, stream);
 }
 
 template <bool P_MN, int NT>
@@ -330,7 +376,7 @@ int64_t lmhead_lora_workspace_bytes(int64_t M, int64_t K, int64_t V, int64_t R, 
     if (!lora_dims_ok(M, K, V, R, N))
         return -1;
     const int64_t f = gemm_space(M, K, R, N, pick_bn(M, 16), LMH_F32).bytes;
-    const int64_t d = gemm_space(M, V, R, N, pick_bn(M, 64), LMH_F32).bytes;
+    const int64_t d = gemm_space(M, V, R, N, pick_bn(M, 64), LMH_F32).bytes + dx_split(M, K, V).scratch_bytes();
     const int64_t w = grad_space(M, R, N).bytes;
     const int64_t fd = f > d ? f : d;
     return fd > w ? fd : w;
@@ -370,7 +416,7 @@ lmh_status_t lmhead_fwd_lora(const void *X, const void *W, const void *A, const 
     p.l2_out = 1;
     p.status = status;
     const AdapterOperands ad{B, static_cast<uint64_t>(R), static_cast<uint64_t>(V), static_cast<uint64_t>(N),
-                             ws + g.ux, static_cast<uint64_t>(g.tiles * g.stages * bn)};
+                             ws + g.ux, static_cast<uint64_t>(g.tiles * g.stages * bn), nullptr};
     const LoraParams q = lora_params(ws, g, R, B, u);
     const bool pair = V >= 256;
     const uint64_t k = static_cast<uint64_t>(K), v = static_cast<uint64_t>(V);
@@ -394,7 +440,8 @@ lmh_status_t lmhead_bwd_dx_lora(const void *dlogits, const void *W, const void *
         return LMH_ERR_MISALIGNED;
     const int bn = pick_bn(M, 64);
     const GemmSpace g = gemm_space(M, V, R, N, bn, out_dtype);
-    if (workspace_bytes < g.bytes)
+    const DxSplit split = dx_split(M, K, V);
+    if (workspace_bytes < g.bytes + split.scratch_bytes())
         return LMH_ERR_INVALID_ARG;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
@@ -411,8 +458,12 @@ lmh_status_t lmhead_bwd_dx_lora(const void *dlogits, const void *W, const void *
     p.l2_a = 2;  // as lmhead_bwd_dx
     p.l2_b = 2;
     p.status = status;
+    p.split_tiles = static_cast<int32_t>(split.tiles);
+    p.split_kb = static_cast<int32_t>(split.kb);
+    p.split_rounds = static_cast<int32_t>(split.rounds);
     const AdapterOperands ad{A, static_cast<uint64_t>(K), static_cast<uint64_t>(R), static_cast<uint64_t>(N),
-                             ws + g.ux, static_cast<uint64_t>(g.tiles * g.stages * bn)};
+                             ws + g.ux, static_cast<uint64_t>(g.tiles * g.stages * bn),
+                             reinterpret_cast<float *>(ws + g.bytes)};
     const LoraParams q = lora_params(ws, g, R, A, g_out);
     const bool pair = K >= 256;
     const uint64_t k = static_cast<uint64_t>(K), v = static_cast<uint64_t>(V);

@@ -99,7 +99,8 @@ template <int BN, bool A_MN, typename OutT, bool TMA_STORE, bool PAIR, int RES =
 __global__ void __launch_bounds__(64 + 32 * EW, RES)
     lora_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmS,
-                     const __grid_constant__ CUtensorMap tmU, const GemmParams p, const LoraParams q)
+                     const __grid_constant__ CUtensorMap tmU, const __grid_constant__ CUtensorMap tmP,
+                     const GemmParams p, const LoraParams q)
 {
     using C = GemmCfg<BN, A_MN, false, PAIR, RES, EW>;
     constexpr int S = C::STAGES;
@@ -131,6 +132,32 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
     const int num_units = PAIR ? static_cast<int>(gridDim.x >> 1) : static_cast<int>(gridDim.x);
     const int num_tiles = p.num_m_tiles * p.num_n_tiles;
     const int num_kb = (p.Kdim + kBlockK - 1) / kBlockK;
+    // dX with 256-token tiles: the tiles of a last wave that would leave many units
+    // idle are split in two along the reduction, as in gemm_tc_kernel (long part
+    // [0, split_kb) on the unit that would have run the tile, short part, with the
+    // slots, on an idle one).  Both parts go to scratch (tmP) in FP32, and
+    // lora_join_kernel adds them.
+    constexpr bool SPLIT = A_MN && PAIR;
+    const int split_first = SPLIT ? num_tiles - p.split_tiles : num_tiles;
+    const int num_items = SPLIT && p.split_tiles > 0 ? split_first + num_units * p.split_rounds : num_tiles;
+    // item -> tile and k-blocks: -1 a whole tile, 0 or 1 a part, 2 nothing to do
+    auto item_of = [&](int it, int &t, int &kb0, int &kb1) -> int {
+        t = it;
+        kb0 = 0;
+        kb1 = num_kb;
+        if (!SPLIT || it < split_first)
+            return -1;
+        const int j = it - split_first, r = j / num_units, u = j - r * num_units;
+        if (u < p.split_tiles) {
+            t = split_first + u;
+            kb1 = p.split_kb;
+            return r == 0 ? 0 : 2;
+        }
+        const int idx = (u - p.split_tiles) + r * (num_units - p.split_tiles);
+        t = split_first + idx;
+        kb0 = p.split_kb;
+        return idx < p.split_tiles ? 1 : 2;
+    };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
@@ -153,6 +180,8 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
         }
         if (TMA_STORE)
             tma_prefetch_desc(&tmC);
+        if (SPLIT && p.split_tiles > 0)
+            tma_prefetch_desc(&tmP);
     }
     if (warp == 1) {
         if (PAIR)
@@ -231,12 +260,14 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
             uint32_t issued = 0;
             bool ok = true;
             bool slots_there = false;
-            for (int t = unit; t < num_tiles && ok; t += num_units) {
-                int mt, nt;
+            for (int it = unit; it < num_items && ok; it += num_units) {
+                int t, kb0, kb1, mt, nt;
+                if (item_of(it, t, kb0, kb1) == 2)
+                    continue;
                 tile_coords(t, p, mt, nt);
                 const int m0 = mt * C::TILE_M + static_cast<int>(rank) * kBlockM;
                 const int nb0 = nt * BN + static_cast<int>(rank) * C::BN_CTA;
-                for (int kb = 0; kb < num_kb; ++kb) {
+                for (int kb = kb0; kb < kb1; ++kb) {
                     if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.wait_limit_ns)) {
                         ok = false;
                         break;
@@ -248,7 +279,7 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
                         phase ^= 1;
                     }
                 }
-                if (IN_REGS)
+                if (IN_REGS || kb1 != num_kb)
                     continue;
                 if (!slots_there)
                     pdl_wait();
@@ -336,25 +367,28 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
                     phase ^= 1;
                 }
             };
-            for (int t = unit; t < num_tiles && ok; t += num_units) {
-                int mt, nt;
+            for (int it = unit; it < num_items && ok; it += num_units) {
+                int t, kb_first, kb_end, mt, nt;
+                if (item_of(it, t, kb_first, kb_end) == 2)
+                    continue;
                 tile_coords(t, p, mt, nt);
+                const bool slots = !IN_REGS && kb_end == num_kb;
                 // slots, their accumulators and the first two slots, wanted after the
                 // shared product
                 int2 n = {0, 0};
                 int4 two = {0, 0, 0, 0};
                 const int4 *table = reinterpret_cast<const int4 *>(q.slot + static_cast<int64_t>(nt) * q.slot_stride);
-                if (!IN_REGS && slots_there) {
+                if (slots && slots_there) {
                     n = q.count[nt];
                     two = table[0];
                 }
                 idesc = C::IDESC;
-                for (int kb0 = 0; kb0 < num_kb && ok; kb0 += kPromote) {
+                for (int kb0 = kb_first; kb0 < kb_end && ok; kb0 += kPromote) {
                     if (!begin_acc()) {
                         ok = false;
                         break;
                     }
-                    const int kb1 = min(num_kb, kb0 + kPromote);
+                    const int kb1 = min(kb_end, kb0 + kPromote);
                     for (int kb = kb0; kb < kb1; ++kb) {
                         if (!begin_stage()) {
                             ok = false;
@@ -365,14 +399,14 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
                             mma(k, k, (kb != kb0 || k != 0) ? 1u : 0u);
                         end_stage();
                     }
-                    if (!IN_REGS && kb1 == num_kb && !slots_there) {
+                    if (slots && kb1 == kb_end && !slots_there) {
                         pdl_wait();
                         slots_there = true;
                         n = q.count[nt];
                         two = table[0];
                     }
                     // a slot that takes no accumulator of its own stays with this one
-                    if (ok && !(kb1 == num_kb && n.x > 0 && n.y == 0))
+                    if (ok && !(kb1 == kb_end && n.x > 0 && n.y == 0))
                         end_acc();
                 }
                 bool open = n.x > 0 && n.y == 0;  // whether the current accumulator is begun
@@ -439,14 +473,17 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
         uint32_t acc = 0, acc_phase = 0;
         bool ok = true;
         pdl_wait();
-        for (int t = unit; t < num_tiles && ok; t += num_units) {
-            int mt, nt;
+        for (int it = unit; it < num_items && ok; it += num_units) {
+            int t, kb0, kb1, mt, nt;
+            const int part = item_of(it, t, kb0, kb1);
+            if (part == 2)
+                continue;
             tile_coords(t, p, mt, nt);
             const int mbase = mt * C::TILE_M + static_cast<int>(rank) * kBlockM;
             const int m = mbase + quarter * 32 + lane;
             const int n0 = nt * BN + half * COLS;
-            const int chunks = (num_kb + kPromote - 1) / kPromote;
-            const int2 n = q.count[nt];
+            const int chunks = (kb1 - kb0 + kPromote - 1) / kPromote;
+            const int2 n = kb1 == num_kb ? q.count[nt] : make_int2(0, 0);
             const int ns = n.x;
             const int all = IN_REGS ? chunks : chunks + n.y;
             const int2 *table = q.slot + static_cast<int64_t>(nt) * q.slot_stride;
@@ -669,6 +706,30 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
             }
             if (!ok)
                 break;
+            if (SPLIT && part >= 0) {
+                const int y = ((t - split_first) * 2 + part) * BN + half * COLS;  // scratch row
+                float *fslots = reinterpret_cast<float *>(slots);
+#pragma unroll
+                for (int c = 0; c < COLS; c += CH) {
+                    if (n0 + c < p.Ndim) {
+                        if (lane == 0)
+                            bulk_wait_read<C::NSLOT - 1>();
+                        __syncwarp();
+                        float *buf = fslots + slot * (C::EPI_SLOT_BYTES / 4);
+#pragma unroll
+                        for (int j = 0; j < CH; ++j)
+                            buf[j * 32 + lane] = sum[c + j];
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            tma_store_2d(&tmP, buf, static_cast<int>(rank) * kBlockM + quarter * 32, y + c);
+                            bulk_commit();
+                        }
+                        slot = slot + 1 == C::NSLOT ? 0 : slot + 1;
+                    }
+                }
+                continue;
+            }
 #pragma unroll
             for (int c = 0; c < COLS; c += CH) {
                 if (TMA_STORE) {
@@ -752,6 +813,36 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
     }
     if (threadIdx.x == 0 && *abort_flag && p.status)
         atomicOr(p.status, 2);
+}
+
+// out = long part + short part of the split tiles.  grid (split tiles, row groups);
+// Mdim is a multiple of 8.
+constexpr int kJoinRows = 8;
+
+template <typename OutT>
+__global__ void __launch_bounds__(256)
+    lora_join_kernel(const float *__restrict__ scratch, OutT *__restrict__ out, const GemmParams p, int32_t split_first)
+{
+    pdl_wait();
+    pdl_launch_dependents();
+    int mt, nt;
+    tile_coords(split_first + static_cast<int>(blockIdx.x), p, mt, nt);
+    const int m = mt * 256 + (threadIdx.x & 63) * 4;
+    if (m >= p.Mdim)
+        return;
+    for (int r = threadIdx.x >> 6; r < kJoinRows; r += 4) {
+        const int row = blockIdx.y * kJoinRows + r;
+        const int64_t n = static_cast<int64_t>(nt) * 256 + row;
+        if (n >= p.Ndim)
+            return;
+        const float *s = scratch + ((static_cast<int64_t>(blockIdx.x) * 2) * 256 + row) * 256 + (threadIdx.x & 63) * 4;
+        const float4 a = *reinterpret_cast<const float4 *>(s), b = *reinterpret_cast<const float4 *>(s + 256 * 256);
+        OutT *o = out + n * p.ldo + m;
+        store_out(o, __float_as_uint(a.x + b.x));
+        store_out(o + 1, __float_as_uint(a.y + b.y));
+        store_out(o + 2, __float_as_uint(a.z + b.z));
+        store_out(o + 3, __float_as_uint(a.w + b.w));
+    }
 }
 
 }  // namespace lmh

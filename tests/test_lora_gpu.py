@@ -278,7 +278,8 @@ def check_bwd(M, K, V, R, N, order, dtype, seed=0):
     (64, 1024, 2048, 16, 64), (129, 264, 512, 16, 9), (300, 136, 256, 48, 300), (513, 512, 776, 128, 4),
     (260, 72, 1280, 256, 2), (1000, 320, 4096, 72, 6), (70, 128, 20000, 64, 3), (1100, 256, 1024, 16, 1),
     (530, 64, 65536, 24, 7),  # the rows taken adapter by adapter
-    (1500, 4096, 512, 16, 2),  # several tiles per CTA, tiles of one adapter
+    (1500, 4096, 512, 16, 2),  # several tiles per CTA, tiles of one adapter, the last wave in halves
+    (2000, 4096, 520, 40, 3),  # the last wave with three short parts per idle unit
 ])
 def test_backward(M, K, V, R, N, order):
     check_bwd(M, K, V, R, N, order, torch.bfloat16 if M % 2 else torch.float32)
