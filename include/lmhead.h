@@ -9,6 +9,9 @@
  *                  rounded to the output dtype only at the store
  *   lmhead_bwd_dx  dX[M,K] = dlogits[M,V] . W[V,K]
  *   lmhead_bwd_dw  dW[V,K] = dlogits[M,V]^T . X[M,K]
+ * and, for serving and fine-tuning beside it, the same projection with a
+ * low-rank adapter per token (lmhead_fwd_lora, lmhead_bwd_dx_lora,
+ * lmhead_bwd_lora) and beam search over its logits (beam_select, beam_reorder).
  *
  * Sources (page title, section):
  *   [P1] Megatron-LM PR #6252 "Add mixed-precision (FP32) LM output logits":

@@ -58,8 +58,9 @@ RowRanges row_ranges(int64_t M, int64_t Cdim, int64_t R, int64_t N)
 // Whether the row kernel takes the tokens adapter by adapter: where the matrix it
 // reads is large, the tokens are more than one tile, and the grouping, which reads
 // the ids once per adapter, is small beside it.  (4096 tokens in random order, 8
-// adapters of rank 32, dlogits of 128256: 1.92 ms as they come, 0.49 ms grouped, the
-// grouping 7 us; below 64 MB of Y the whole row kernel takes no longer than that.)
+// adapters of rank 32, dlogits of 128256, the row kernel in its first form: 1.92 ms
+// as they come, 0.49 ms grouped, the grouping 7 us; below 64 MB of Y the whole row
+// kernel takes no longer than that.)
 bool rows_sorted(int64_t M, int64_t Cdim, int64_t N)
 {
     return M > lmh::kRowsTokens && N > 1 && M * Cdim >= (int64_t{1} << 25) && N * 64 <= Cdim;

@@ -1,4 +1,4 @@
-"""ctypes binding of liblmhead.so: the five calls of include/lmhead.h.
+"""ctypes binding of liblmhead.so: the calls of include/lmhead.h.
 
 Argument marshalling only: shapes, dtypes and device pointers are read off
 torch tensors and passed to the C ABI on the caller's current CUDA stream.
