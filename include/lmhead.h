@@ -280,9 +280,10 @@ LMH_API lmh_status_t lmhead_bwd_dw_acc(const void *dlogits, const void *X, float
  *   lmhead_fwd's but with a smaller error and not bitwise equal to it.  Above 128
  *   tokens u enters the second product as two BF16 parts (2^-18 of u), or one for
  *   BF16 logits.  An adapter's values reach the tokens that use it and no
- *   others, infinities and NaN included.  Any order of the tokens; those of one
- *   adapter next to each other cost least (each 256-token tile reads the
- *   adapters that occur in it).
+ *   others, infinities and NaN included (for its own tokens an infinity may come
+ *   out as NaN, since the parts of u multiply it one by one).  Any order of the
+ *   tokens; those of one adapter next to each other cost least (each 256-token
+ *   tile reads the adapters that occur in it).
  *   workspace: device scratch of lmhead_lora_workspace_bytes(M, K, V, R, N)
  *   bytes, 256-byte aligned; its contents do not matter before or after.
  *   Requirements: K % 8 == 0, R % 8 == 0, R <= 256, N <= 65535, M <= 4194240, M N <= 2^34;
@@ -335,9 +336,10 @@ LMH_API lmh_status_t lmhead_bwd_lora(const void *dlogits, const void *X, const f
  *           (-inf, -1, -1).
  *   cand_score / cand_beam / cand_token [N,C] (FP32, int32, int64): the C best
  *           continuations, best first, compared by the FP64 value of total and,
- *           where equal, by the lower w * V + v.  A logit or score of -inf
+ *           where equal, by the lower w, the higher logit, the lower v.  A logit or score of -inf
  *           forbids a continuation: where fewer than C are possible the rest is
- *           (-inf, -1, -1).
+ *           (-inf, -1, -1).  Logits as low as the type goes are continuations like
+ *           any other; a total below FP32's range counts as -inf.
  *   next_score / next_beam / next_token [N,W], all three or none (NULL): the
  *           first W candidates whose token is not eos (eos = -1: none is), in
  *           order.  Places that no candidate fills get (-inf, w, eos, or 0 for

@@ -17,10 +17,12 @@
 //                      logit and 103 us)
 //   beam_merge_kernel  one CTA per batch entry: lse of every beam, the best C
 //                      of all beams' candidates, the beams that go on
-// Continuations are compared by the FP64 value of total, ties by the lower
-// w * V + v: an FP32 total has a step of 1e-6 at -15, which the gaps between
+// Continuations are compared by the FP64 value of total, ties by the lower beam, then
+// the higher logit (where FP64 cannot tell totals apart that differ), then the lower
+// token: an FP32 total has a step of 1e-6 at -15, which the gaps between
 // candidates of a large batch do meet.
 #pragma once
+#include <cfloat>
 #include <cstdint>
 #include <cuda_bf16.h>
 
@@ -38,13 +40,18 @@ constexpr int kBeamHits = 128;        // sixteens at or above it that a warp can
 constexpr int kBeamMaxCand = 128;
 constexpr int kBeamMaxWidth = 64;
 constexpr float kBeamMaxLogit = 1e38f;
+// A reference beyond this (a largest logit beyond about 2^29 either way, as where a
+// mask of the type's lowest value covers a part) is too coarse an FP32 number to
+// stand in for the largest logit.
+constexpr float kBeamMaxRef = 7.7e8f;
 constexpr int kBeamDevBadLogit = 0x4;   // LMH_DEV_BAD_LOGIT
 constexpr int kBeamDevBadParent = 0x10; // LMH_DEV_BAD_PARENT
 
 // A part's share of its row.
 struct BeamPartial {
     double sum;     // sum of 2^(x log2(e) - ref)
-    float ref;      // integer-valued: rint(max * log2(e)); -inf if no finite logit
+    float ref;      // integer-valued: rint(max * log2(e)); -inf if no finite logit;
+                    // FLT_MAX, -FLT_MAX beyond kBeamMaxRef: then sum of exp(x - max)
     int32_t count;  // candidates in the part's list
 };
 
@@ -230,10 +237,10 @@ __device__ __forceinline__ int64_t beam_token(int64_t v0, int i, int tid)
     return v0 + ((i / VN) * kBeamThreads + tid) * VN + i % VN;
 }
 
-// Higher is better: the logit first, then the lower token.
+// Higher is better: the logit first (-0 as 0), then the lower token.
 __device__ __forceinline__ uint64_t beam_key(float x, int64_t tok)
 {
-    return (static_cast<uint64_t>(ordered(x)) << 32) | (0xffffffffu - static_cast<uint32_t>(tok));
+    return (static_cast<uint64_t>(ordered(x + 0.f)) << 32) | (0xffffffffu - static_cast<uint32_t>(tok));
 }
 
 // Makes unusable logits -inf; whether there were any.
@@ -247,6 +254,42 @@ __device__ __forceinline__ bool beam_clean(float (&x)[kBeamPerThread])
         x[i] = ok ? x[i] : -INFINITY;
     }
     return bad;
+}
+
+// The sum of a part whose largest logit is beyond kBeamMaxRef's: again, against that
+// logit, the first of its list.  All threads of the part's CTA; a call, and all it
+// needs made anew, so that the scan has its registers to itself (in line: 512 x 151936
+// takes 3 % longer).
+template <typename T>
+__device__ __noinline__ void beam_sum_far(const T *logits, const BeamCand *cand, BeamPartial *part, int64_t V,
+                                          int32_t C, int32_t parts, int32_t batches, double *red_sum)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t row = blockIdx.x / static_cast<unsigned>(parts);
+    const T *x0 = logits + row * V;
+    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(x0) & 15);
+    const int64_t begin = (static_cast<int64_t>(blockIdx.x) - row * parts) * batches * kBeamBatch;
+    __syncthreads();  // the list is written, the first sums are read
+    const float m = *const_cast<const volatile float *>(&cand[static_cast<int64_t>(blockIdx.x) * C].x);
+    double s = 0.0;
+    for (int b = 0; b < batches && begin + b * kBeamBatch < V; ++b) {
+        float x[kBeamPerThread];
+        beam_load(x0, begin + b * kBeamBatch, V, off, x);
+        beam_clean(x);
+#pragma unroll
+        for (int i = 0; i < kBeamPerThread; ++i)
+            s += static_cast<double>(expf(x[i] - m));
+    }
+    s = warp_sum(s);
+    if (lane == 0)
+        red_sum[warp] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int i = 1; i < kBeamWarps; ++i)
+            s += red_sum[i];
+        part[blockIdx.x].sum = s;
+        part[blockIdx.x].ref = copysignf(FLT_MAX, m);
+    }
 }
 
 // One CTA per part (`batches` batches) of a row.  Rows of beams that cannot go on
@@ -286,7 +329,7 @@ __global__ void __launch_bounds__(kBeamThreads, 6)
     // then rounded once per term, near its own size (log2(e) as two floats, so that
     // large logits keep their last places), and a new ref scales the sum exactly.
     // A new ref is taken only when a term would pass 2^8.  FP32 sums of 16 terms,
-    // joined in FP64, leave lse good to about 1e-8.
+    // joined in FP64, leave lse good to about 1e-8 (for logits up to 1e7).
     constexpr float kLh = 1.44269502162933349609f, kLl = 1.92596303e-8f, kSlack = 8.f / kLh;
     float ref = -INFINITY, top = -INFINITY, most = -INFINITY;
     double sum = 0.0;
@@ -298,7 +341,7 @@ __global__ void __launch_bounds__(kBeamThreads, 6)
         float best;
         auto add = [&]() -> float {
             if (best > top) {
-                const float r = rintf(best * kLh);
+                const float r = fmaxf(rintf(best * kLh), -FLT_MAX);
                 // the first time ref is -inf and the sum 0
                 sum = ref > -INFINITY ? sum * pow2(ref - r) : 0.0;
                 ref = r;
@@ -431,11 +474,11 @@ __global__ void __launch_bounds__(kBeamThreads, 6)
                                      static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(b))};
         }
     }
-    if (tid == 0) {
-        float r = red_ref[0];
+    float r = red_ref[0];
 #pragma unroll
-        for (int i = 1; i < kBeamWarps; ++i)
-            r = fmaxf(r, red_ref[i]);
+    for (int i = 1; i < kBeamWarps; ++i)
+        r = fmaxf(r, red_ref[i]);
+    if (tid == 0) {
         double s = 0.0;
 #pragma unroll
         for (int i = 0; i < kBeamWarps; ++i)
@@ -443,6 +486,9 @@ __global__ void __launch_bounds__(kBeamThreads, 6)
                 s += red_sum[i] * pow2(red_ref[i] - r);
         part[row * parts + pt] = BeamPartial{s, r, kept};
     }
+    // (threads whose logits lie that far below the part's largest added nothing)
+    if (fabsf(r) > kBeamMaxRef && r > -INFINITY)
+        beam_sum_far(logits, cand, part, V, C, parts, batches, red_sum);
 }
 
 struct BeamOut {
@@ -455,11 +501,12 @@ struct BeamOut {
 };
 
 // A candidate of the merge: its total as an unsigned integer of the same order, and
-// its place (beam << 32 | token), which orders as w * V + v does.
+// what decides between equal totals, lower first: beam (6 bits), logit (32, the
+// higher first), part (19) and place in its list (7), which order as the token does.
 struct BeamKey {
-    uint64_t total;
-    int64_t at;
+    uint64_t total, at;
 };
+static_assert(kBeamMaxWidth <= 1 << 6 && kBeamMaxCand <= 1 << 7, "bits of BeamKey::at");
 
 __device__ __forceinline__ uint64_t ordered64(double x)
 {
@@ -485,11 +532,16 @@ __global__ void __launch_bounds__(kBeamThreads)
                       const BeamCand *cand, BeamOut o, int32_t W, int32_t C, int32_t parts, int64_t eos,
                       int32_t *status)
 {
-    __shared__ double off[kBeamMaxWidth];   // score - lse; -inf for a beam with no continuation
+    // total = (x - base) + off.  off: score - lse, -inf for a beam with no continuation.
+    // base: 0, or the row's largest logit beyond kBeamMaxRef, which off then leaves out
+    // (lse would swallow the logarithm of the sum).
+    __shared__ double off[kBeamMaxWidth];
+    __shared__ float base[kBeamMaxWidth];
     __shared__ uint32_t red[kBeamWarps];
     __shared__ BeamKey buf[kBeamBuf];
     __shared__ BeamKey win[kBeamWarps];
     __shared__ BeamKey sorted[kBeamMaxCand];
+    __shared__ int32_t buf_tok[kBeamBuf], sorted_tok[kBeamMaxCand];
     __shared__ int count;
     pdl_wait();
     pdl_launch_dependents();
@@ -518,21 +570,23 @@ __global__ void __launch_bounds__(kBeamThreads)
     // a list's end, or belongs to a beam whose row was not read, is not used.
     struct Raw {
         BeamCand c;
-        int32_t w;
+        int32_t w, place;  // place: part << 7 | rank
         bool listed;
     };
     auto fetch = [&](int i) -> Raw {
         const unsigned list = static_cast<unsigned>(i) / static_cast<unsigned>(C);  // of the entry
         const int j = i - static_cast<int>(list) * C;
         const int64_t rc = n * W * parts + list;
-        return Raw{cand[rc * C + j], static_cast<int32_t>(list / static_cast<unsigned>(parts)), j < part[rc].count};
+        const int32_t w = static_cast<int32_t>(list / static_cast<unsigned>(parts));
+        return Raw{cand[rc * C + j], w, (static_cast<int32_t>(list) - w * parts) << 7 | j, j < part[rc].count};
     };
     auto key_of = [&](const Raw &r, BeamKey &k) -> bool {
         if (!(off[r.w] > -INFINITY) || !r.listed)
             return false;
-        k.total = ordered64(off[r.w] + static_cast<double>(r.c.x));
-        k.at = (static_cast<int64_t>(r.w) << 32) | static_cast<uint32_t>(r.c.tok);
-        return true;
+        k.total = ordered64((static_cast<double>(r.c.x) - static_cast<double>(base[r.w])) + off[r.w]);
+        k.at = static_cast<uint64_t>(r.w) << 58 | static_cast<uint64_t>(~ordered(r.c.x)) << 26 |
+               static_cast<uint32_t>(r.place);
+        return k.total >= ordered64(-static_cast<double>(FLT_MAX));  // FP32 has no room for less
     };
     constexpr int HELD = 4;  // candidates a thread keeps, under way while lse is made
     Raw raw[HELD];
@@ -540,7 +594,7 @@ __global__ void __launch_bounds__(kBeamThreads)
     for (int j = 0; j < HELD; ++j) {
         const int i = tid + j * kBeamThreads;
         raw[j].listed = false;
-        raw[j].w = 0;
+        raw[j].w = raw[j].place = 0;
         if (i < items)
             raw[j] = fetch(i);
     }
@@ -552,12 +606,27 @@ __global__ void __launch_bounds__(kBeamThreads)
         float ref = lane < parts ? pp[lane].ref : -INFINITY;
         double sum = lane < parts ? pp[lane].sum : 0.0;
         double r = -INFINITY;
+        float from = 0.f;
         if (beam_live(sc)) {
             float c = ref;
             for (int k = lane + 32; k < parts; k += 32)
                 c = fmaxf(c, pp[k].ref);
             c = from_ordered(__reduce_max_sync(0xffffffffu, ordered(c)));
-            if (c > -INFINITY) {
+            if (fabsf(c) == FLT_MAX) {
+                // sums against the largest logit of each part, the first of its list
+                const BeamCand *first = cand + (n * W + w) * parts * C;
+                from = -INFINITY;
+                for (int k = lane; k < parts; k += 32)
+                    if (pp[k].ref == c)
+                        from = fmaxf(from, first[static_cast<int64_t>(k) * C].x);
+                from = from_ordered(__reduce_max_sync(0xffffffffu, ordered(from)));
+                double s = 0.0;
+                for (int k = lane; k < parts; k += 32)
+                    if (pp[k].ref == c)
+                        s += pp[k].sum * exp(static_cast<double>(first[static_cast<int64_t>(k) * C].x) -
+                                             static_cast<double>(from));
+                r = static_cast<double>(sc) - log(warp_sum(s));
+            } else if (c > -INFINITY) {
                 double s = ref > -INFINITY ? sum * pow2(ref - c) : 0.0;
                 for (int k = lane + 32; k < parts; k += 32) {
                     ref = pp[k].ref;
@@ -571,8 +640,10 @@ __global__ void __launch_bounds__(kBeamThreads)
         } else if (lane == 0 && status && !(sc < INFINITY)) {
             atomicOr(status, kBeamDevBadLogit);  // a score of NaN or +inf
         }
-        if (lane == 0)
+        if (lane == 0) {
             off[w] = r;
+            base[w] = from;
+        }
     }
     __syncthreads();
 
@@ -592,8 +663,10 @@ __global__ void __launch_bounds__(kBeamThreads)
         auto put = [&](const Raw &r) {
             if (key_of(r, k) && k.total >= least) {
                 const int at = atomicAdd(&count, 1);
-                if (at < kBeamBuf)
+                if (at < kBeamBuf) {
                     buf[at] = k;
+                    buf_tok[at] = r.c.tok;
+                }
             }
         };
 #pragma unroll
@@ -611,14 +684,16 @@ __global__ void __launch_bounds__(kBeamThreads)
             const int i = i0 + (tid >> 3);
             const BeamKey c = i < m ? buf[i] : BeamKey{0, 0};
             const int rank = beam_rank(tid & 7, m, [&](int j) { return ahead(buf[j], c); });
-            if (i < m && rank < C && (tid & 7) == 0)
+            if (i < m && rank < C && (tid & 7) == 0) {
                 sorted[rank] = c;
+                sorted_tok[rank] = buf_tok[i];
+            }
         }
         __syncthreads();
     } else {
-        BeamKey last{~0ull, -1};
+        BeamKey last{~0ull, 0};
         for (kept = 0; kept < C; ++kept) {
-            BeamKey b{0, INT64_MAX};
+            BeamKey b{0, ~0ull};
             for (int i = tid; i < items; i += kBeamThreads)
                 if (key_of(fetch(i), k) && ahead(last, k) && ahead(k, b))
                     b = k;
@@ -640,8 +715,11 @@ __global__ void __launch_bounds__(kBeamThreads)
             if (b.total == 0)
                 break;
             last = b;
-            if (tid == 0)
+            if (tid == 0) {
                 sorted[kept] = b;
+                const int64_t list = (n * W + (b.at >> 58)) * parts + (b.at >> 7 & 0x7ffff);
+                sorted_tok[kept] = cand[list * C + (b.at & 127)].tok;
+            }
         }
         __syncthreads();
     }
@@ -653,9 +731,9 @@ __global__ void __launch_bounds__(kBeamThreads)
     for (int i0 = 0; i0 < C; i0 += 32) {
         const int i = i0 + lane;
         const bool have = i < kept;
-        const BeamKey c = have ? sorted[i] : BeamKey{0, -1};
-        const int32_t beam = have ? static_cast<int32_t>(c.at >> 32) : -1;
-        const int64_t tok = have ? c.at & 0xffffffff : -1;
+        const BeamKey c = have ? sorted[i] : BeamKey{0, 0};
+        const int32_t beam = have ? static_cast<int32_t>(c.at >> 58) : -1;
+        const int64_t tok = have ? sorted_tok[i] : -1;
         const float sc = have ? static_cast<float>(from_ordered64(c.total)) : -INFINITY;
         if (i < C) {
             o.cand_score[n * C + i] = sc;

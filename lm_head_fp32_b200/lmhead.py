@@ -371,7 +371,7 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, cand_score: torch.Te
                 stream=None):
     """One step of beam search: the C best continuations of logits[N,W,V] (FP32 or
     BF16) with beam scores[N,W] into cand_*[N,C] (score FP32, beam int32, token
-    int64; best first, ties to the lower beam * V + token), and the first W whose
+    int64; best first, ties to the lower beam and token), and the first W whose
     token is not `eos` into next_*[N,W] (all three None to skip).  Entries with
     done[n] != 0 (int32) are not read and keep their beams."""
     if logits.dim() != 3 or cand_score.dim() != 2:

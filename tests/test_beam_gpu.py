@@ -27,8 +27,11 @@ def plain_select(logits, scores, C, eos, done=None):
     m = x.amax(2, keepdim=True)
     m0 = torch.where(m > NEG, m, torch.zeros_like(m))
     lse = (x - m0).exp().sum(2, keepdim=True).log() + m0
-    total = torch.where(x > NEG, s[:, :, None] + x - lse, x).view(N, W * V)
-    val, at = total.sort(dim=1, descending=True, stable=True)
+    total = torch.where(x > NEG, s[:, :, None] + x - lse, x)
+    # equal totals: the lower beam, the higher logit, the lower token
+    by_logit = x.sort(dim=2, descending=True, stable=True)[1]
+    val, at = total.gather(2, by_logit).view(N, W * V).sort(dim=1, descending=True, stable=True)
+    at = (at // V) * V + by_logit.view(N, W * V).gather(1, at)
     cs = torch.full((N, C), NEG, dtype=torch.float64)
     cb, ct = torch.full((N, C), -1), torch.full((N, C), -1)
     ns, nb = torch.full((N, W), NEG, dtype=torch.float64), torch.arange(W).repeat(N, 1)
@@ -208,6 +211,90 @@ def test_shapes_of_rows(kind):
     # a logit of 1e4 enters lse exactly (its product with log2 e is rounded at the
     # size of the difference to the maximum), so the bound is the usual one
     assert ((got[0].cpu().double() - ref[0]).abs() <= 2.0 ** -24 * ref[0].abs() + 2e-6).all()
+
+
+LOWEST = torch.finfo(torch.float32).min
+
+
+def far_rows(kind, dtype):
+    """Rows whose largest logit is far from zero, or that mask with such logits."""
+    V = 20001
+    x, s = data(2, 3, V, 21, dtype)
+    low = float(torch.finfo(dtype).min)
+    if kind == "lowest":          # nothing but masked tokens: all equally likely
+        x[:] = low
+    elif kind == "one row lowest":
+        x[0, 1] = low
+        x[1, 2, 1:] = low
+    elif kind == "parts lowest":  # whole parts of a row, and the first
+        x[:, :, :13000] = low
+    elif kind == "few and lowest":
+        x, s = x[:, :1].contiguous(), s[:, :1].contiguous()
+        keep = torch.zeros(V, dtype=torch.bool, device=DEV)
+        keep[[4097, 9000, 20000]] = True
+        x[:, :, ~keep] = low
+    elif kind == "-1e10":
+        x[0] = -1e10
+        x[1, :, :19000] = -1e10
+    elif kind == "1e10":
+        x = (x.float() * 4e9).to(dtype)
+    elif kind == "1e37":
+        x = (x.float() * 1e36).to(dtype)
+    elif kind == "lowest and -inf":
+        x[:, :, ::2] = NEG
+        x[:, :, 1::2] = low
+    elif kind == "lowest score":
+        s[:] = LOWEST
+        s[1, 1] = -2.0
+    else:                         # about where the sums change their reference
+        c = {"-2^29": -1.0, "2^29": 1.0}[kind] * 2.0 ** 29
+        g = torch.Generator().manual_seed(22)
+        x = (c + 32.0 * torch.randint(-3, 4, x.shape, generator=g).double()).to(dtype).to(DEV)
+    return x, s
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("kind", ["lowest", "one row lowest", "parts lowest", "few and lowest", "-1e10", "1e10",
+                                  "1e37", "lowest and -inf", "lowest score", "-2^29", "2^29"])
+def test_rows_far_from_zero(kind, dtype):
+    x, s = far_rows(kind, dtype)
+    # the softmax does not change when the row is shifted by its maximum, exact in
+    # FP64 where it matters; without it x - lse would lose the logarithm of the sum
+    m = x.double().amax(2, keepdim=True)
+    C = 6
+    ref = plain_select(x.double() - torch.where(m > NEG, m, torch.zeros_like(m)), s, C, 2)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got = run_select(x, s, C, 2, status=status)
+    assert int(status.item()) == 0
+    for i in (1, 2, 4, 5):
+        assert torch.equal(got[i].cpu().long(), ref[i]), i
+    for i in (0, 3):
+        g, r = got[i].cpu().double(), ref[i]
+        fin = torch.isfinite(r)
+        assert torch.equal(torch.isfinite(g), fin)
+        # near 2^29 the exponent's argument reaches 64: two roundings of 2^-24 * 64,
+        # times ln 2, in place of those of the usual bound
+        assert ((g - r).abs()[fin] <= 2.0 ** -24 * r.abs()[fin] + 2e-6 + 2 * 64 * 2.0 ** -24 * 0.7).all()
+
+
+def test_zeros_of_both_signs_are_equal():
+    x = torch.zeros((1, 2, 9000), device=DEV)
+    x[:, :, :4] = -0.0
+    x[:, 0, 5::3] = -1.0
+    s = torch.tensor([[-1.0, -1.25]], device=DEV)
+    check(x, s, 12, eos=1)
+
+
+def test_totals_below_the_range_are_no_candidates():
+    x, s = data(1, 2, 300, 23)
+    x[:, :, 3:] = LOWEST
+    s[:] = LOWEST
+    got = run_select(x, s, 8, 2)
+    # 2 x 3 continuations at the lowest value; the others would be at twice that
+    assert torch.isfinite(got[0][0, :6]).all() and (got[0][0, 6:] == NEG).all()
+    # their totals are equal in FP64: by beam, then by logit
+    order = x[0, :, :3].argsort(1, descending=True).flatten().tolist()
+    assert got[1][0].tolist() == [0, 0, 0, 1, 1, 1, -1, -1] and got[2][0].tolist() == order + [-1, -1]
 
 
 def test_select_twice_the_same_and_on_a_stream():
