@@ -297,6 +297,22 @@ def test_totals_below_the_range_are_no_candidates():
     assert got[1][0].tolist() == [0, 0, 0, 1, 1, 1, -1, -1] and got[2][0].tolist() == order + [-1, -1]
 
 
+def test_logits_beyond_32_bit_offsets():
+    N, W, V, C = 2200, 8, 128001, 16     # 2.25e9 logits
+    g = torch.Generator(device=DEV).manual_seed(24)
+    x = torch.empty((N, W, V), dtype=torch.bfloat16, device=DEV)
+    for n in range(0, N, 100):
+        x[n:n + 100] = torch.randn((100, W, V), generator=g, device=DEV).mul_(2.5)
+    s = -torch.rand((N, W), generator=g, device=DEV) * 6
+    got = run_select(x, s, C, 2)
+    at = [0, 1, 2047, 2048, 2097, 2098, N - 1]
+    ref = plain_select(x[at], s[at], C, 2)
+    for i in (1, 2, 4, 5):
+        assert torch.equal(got[i][at].cpu().long(), ref[i]), i
+    for i in (0, 3):
+        assert ((got[i][at].cpu().double() - ref[i]).abs() <= 2.0 ** -24 * ref[i].abs() + 2e-6).all()
+
+
 def test_select_twice_the_same_and_on_a_stream():
     x, s = data(4, 4, 40000, 16)
     a = run_select(x, s, 8, 2)
@@ -340,6 +356,18 @@ def test_reorder(N, W, e, shape, dtype):
         for i, s in enumerate(states):
             assert torch.equal(s.cpu(), plain_reorder((t0.long() + i).to(dtype), p, e))
         assert int(st.item()) == 0
+
+
+def test_reorder_beyond_32_bit_offsets():
+    L, N, W, H, S, D = 2, 16, 4, 8, 20000, 128   # 5.2 GB, and the filled part of as much
+    g = torch.Generator(device=DEV).manual_seed(25)
+    parents = torch.randint(0, W, (N, W), generator=g, device=DEV, dtype=torch.int32)
+    t = torch.randint(0, 256, (L, N, W, H, S, 2 * D), generator=g, device=DEV, dtype=torch.uint8)
+    view = t[:, :, :, :, :19999]
+    ref = plain_reorder(view, parents, 1)
+    lmhead.beam_reorder(view, parents, 1)
+    torch.cuda.synchronize()
+    assert torch.equal(view, ref)
 
 
 def test_reorder_leaves_the_unfilled_part():

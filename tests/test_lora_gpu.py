@@ -167,6 +167,67 @@ def test_forward_exact_on_integers(M, K, V, R, N):
     assert torch.equal(u.double(), ru) and torch.equal(logits.double(), rl)
 
 
+def pick(t, rows):
+    return t[rows].double()
+
+
+@pytest.mark.parametrize("M", [5, 260])
+def test_adapters_beyond_32_bit_offsets(M):
+    K, V, R, N = 256, 32776, 128, 600   # B has 2.5e9 elements
+    g = torch.Generator(device=DEV).manual_seed(M)
+    b16 = torch.bfloat16
+    X = torch.randn((M, K), generator=g, device=DEV).to(b16)
+    W = (torch.randn((V, K), generator=g, device=DEV) * 0.02).to(b16)
+    A = (torch.randn((N, R, K), generator=g, device=DEV) * K ** -0.5).to(b16)
+    B = torch.empty((N, V, R), dtype=b16, device=DEV)
+    for a in range(0, N, 50):
+        B[a:a + 50] = torch.randn((50, V, R), generator=g, device=DEV).mul_(0.02)
+    scale = torch.ones(N, device=DEV)
+    ids = torch.full((M,), 599, dtype=torch.int32, device=DEV)
+    ids[:2], ids[-1] = 598, 0
+    dl = torch.randn((M, V), generator=g, device=DEV).mul_(0.01).to(b16)
+    logits, u = fwd(X, W, A, B, scale, ids)
+    ws = workspace(M, K, V, R, N)
+    gt, dX = guarded_empty((M, R)), guarded_empty((M, K))
+    lmhead.lmhead_bwd_dx_lora(dl, W, A, B, scale, ids, gt, dX, ws)
+    dA = torch.empty((N, R, K), device=DEV)
+    dB = torch.empty((N, V, R), device=DEV)
+    lmhead.lmhead_bwd_lora(dl, X, u, gt, ids, dA, dB, ws)
+    torch.cuda.synchronize()
+    for a, at in per_token(ids, N):
+        x, d, Aa, Ba = pick(X, at), pick(dl, at), A[a].double(), B[a].double()
+        ut, gg = x @ Aa.T, d @ Ba
+        tu = E23 * (12 + K / 256) * (x.abs() @ Aa.abs().T)
+        tg = E23 * (12 + V / 256) * (d.abs() @ Ba.abs())
+        close(u[at], ut, tu, "u")
+        close(gt[at], gg, tg, "g")
+        close(logits[at], x @ W.double().T + ut @ Ba.T,
+              gemm_eps(K) * (x.abs() @ W.double().abs().T) + tu @ Ba.abs().T
+              + (split_eps(M, torch.float32) + E23 * 56) * (ut.abs() @ Ba.abs().T), "logits")
+        close(dX[at], d @ W.double() + gg @ Aa,
+              gemm_eps(V, chunk=512) * (d.abs() @ W.double().abs()) + tg @ Aa.abs()
+              + (split_eps(M, torch.float32) + E23 * 56) * (gg.abs() @ Aa.abs()), "dX")
+        sum_tol = E23 * (52 + M / 512)
+        close(dA[a], gg.T @ x, tg.T @ x.abs() + sum_tol * (gg.abs().T @ x.abs()), "dA")
+        close(dB[a], d.T @ ut, d.abs().T @ tu + sum_tol * (d.abs().T @ ut.abs()), "dB")
+    for a in (1, 300, 597):
+        assert not dA[a].any() and not dB[a].any()
+
+
+@pytest.mark.parametrize("V", [131080, 131083])
+def test_logits_beyond_32_bit_offsets(V):
+    M, K, R, N = 16500, 64, 8, 3       # 2.16e9 logits
+    X, W, A, B, scale, ids = make(M, K, V, R, N)
+    logits, u = fwd(X, W, A, B, scale, ids, torch.bfloat16)
+    rows = torch.tensor([0, 1, 255, 256, 8191, 16383, 16384, 16385, M - 2, M - 1], device=DEV)
+    ru, tu, ref, tol = ref_fwd(X[rows], W, A, B, scale, ids[rows], torch.bfloat16)
+    # ten rows alone would take u in FP32; the whole batch takes it as one BF16 part
+    for a, at in per_token(ids[rows], N):
+        tol[at] += 2.0 ** -8 * (ru[at].abs() @ B[a].double().abs().T)
+    close(u[rows], ru, tu, "u")
+    close(logits[rows], ref, tol, "logits")
+
+
 def test_adapter_order_does_not_matter_and_is_deterministic():
     X, W, A, B, scale, ids = make(300, 512, 1024, 16, 6, none=True)
     one, u1 = fwd(X, W, A, B, scale, ids)
