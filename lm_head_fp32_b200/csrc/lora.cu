@@ -25,7 +25,6 @@ constexpr int64_t kMaxRank = 256;
 constexpr int64_t kMaxAdapters = 65535;              // a grid dimension
 constexpr int64_t kMaxTokens = 65535ll * lmh::kRowsTokens;  // likewise
 constexpr int64_t kMaxGrouping = int64_t{1} << 34;   // tokens x adapters: the grouping looks at each id per adapter
-constexpr int64_t kRowsCtas = 1480;  // row-kernel CTAs aimed at: ten per SM
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
@@ -36,7 +35,9 @@ int pick_bn(int64_t M, int least) { return M <= least ? least : M <= 32 ? 32 : M
 
 // Ranges the columns of a row kernel are cut into: enough CTAs that the last ones
 // leave few SMs idle (dlogits of 4096 x 128256, rank 32: 424, 296, 253 us with 384,
-// 832, 1728), and no more, since each range writes a partial result.
+// 832, 1728), and no more, since each range writes a partial result, which is most of
+// the work with few tokens (60 x 792 x 73312, rank 16, both gradients: 74 us with 1480,
+// 71 with 740, 72 with 296).
 struct RowRanges {
     int64_t subs, ranges, groups;
 };
@@ -44,13 +45,14 @@ RowRanges row_ranges(int64_t M, int64_t Cdim, int64_t R, int64_t N)
 {
     const int64_t nsub = ceil_div(Cdim, lmh::kRowsSub);
     const int64_t base = ceil_div(M, lmh::kRowsTokens) * ceil_div(R, lmh::kRankBlock);
-    int64_t want = kRowsCtas / base;
+    const int64_t ctas = base < 32 ? 740 : 1480;  // aimed at: five or ten per SM
+    int64_t want = ctas / base;
     want = want < 1 ? 1 : want > nsub ? nsub : want;
     const int64_t subs = ceil_div(nsub, want);
     const int64_t ranges = ceil_div(nsub, subs);
     // CTAs still to spare: the adapters of a tile are dealt out to several
     const int64_t most = N < M ? (N < lmh::kRowsTokens ? N : lmh::kRowsTokens) : (M < lmh::kRowsTokens ? M : lmh::kRowsTokens);
-    int64_t groups = kRowsCtas / (base * ranges);
+    int64_t groups = ctas / (base * ranges);
     groups = groups < 1 ? 1 : groups > most ? most : groups;
     return {subs, ranges, groups};
 }
@@ -109,30 +111,54 @@ GradSpace grad_space(int64_t M, int64_t R, int64_t N)
     return g;
 }
 
-// The tiles of dX's last wave that are split in two, each unit (CTA pair) that the
-// wave leaves idle taking `rounds` short parts: as lmhead_bwd_dx, where the rule is
-// explained and measured.
+// How dX is split along its reduction.  Either every tile into `parts` parts of
+// `part_kb` k-blocks, or `tiles` tiles of the last wave in two, each unit (CTA pair)
+// that the wave leaves idle taking `rounds` short parts: as lmhead_bwd_dx, where that
+// rule is explained and measured.
 struct DxSplit {
+    int64_t parts = 0, part_kb = 0;
     int64_t tiles = 0, kb = 0, rounds = 0;
-    int64_t scratch_bytes() const { return tiles * 2 * 256 * 256 * 4; }
+    int64_t scratch = 0;  // bytes
 };
 constexpr int64_t kMaxSplitRounds = 8;
+constexpr int64_t kMinPartKb = 16;
 DxSplit dx_split(int64_t M, int64_t K, int64_t V)
 {
     DxSplit s;
-    if (M <= 128 || K < 256)
+    const int64_t bn = pick_bn(M, 64), tile_m = bn == 256 && K >= 256 ? 256 : 128;
+    const int64_t units = num_sms() / (tile_m / 128), tiles = ceil_div(K, tile_m) * ceil_div(M, bn);
+    const int64_t num_kb = ceil_div(V, lmh::kBlockK);
+    if (tiles <= units) {
+        // The number of parts that takes the least time, counted in k-blocks on the
+        // busiest unit, each part with what handing it over costs (about 3 us for the
+        // 256 KB of a pair's tile, a k-block 0.3 us; narrow tiles a quarter of that).
+        const int64_t cost = bn == 256 ? 20 : 8;
+        int64_t best = num_kb;
+        for (int64_t n = 2; n * kMinPartKb <= num_kb && n * tiles <= 2 * units; ++n) {
+            const int64_t kb = ceil_div(ceil_div(num_kb, n), 8) * 8, parts = ceil_div(num_kb, kb);
+            const int64_t t = ceil_div(tiles * parts, units) * (kb + cost);
+            if (parts > 1 && t < best) {
+                best = t;
+                s.parts = parts;
+                s.part_kb = kb;
+            }
+        }
+        s.scratch = tiles * s.parts * bn * tile_m * 4;
         return s;
-    const int64_t units = num_sms() / 2, tiles = ceil_div(K, 256) * ceil_div(M, 256);
-    const int64_t rem = tiles % units, num_kb = ceil_div(V, lmh::kBlockK);
+    }
+    if (tile_m != 256)
+        return s;
+    const int64_t rem = tiles % units;
     if (num_kb < 2 || rem == 0)
         return s;
     const int64_t spare = units - rem, k = ceil_div(rem, spare);
     const int64_t B = (num_kb * k + k) / (k + 1);  // ceil(num_kb k / (k + 1))
     const int64_t span = B > k * (num_kb - B) ? B : k * (num_kb - B);
-    if ((k == 1 || tiles > units) && k <= kMaxSplitRounds && B < num_kb && 10 * span <= 9 * num_kb) {
+    if (k <= kMaxSplitRounds && B < num_kb && 10 * span <= 9 * num_kb) {
         s.tiles = rem;
         s.kb = B;
         s.rounds = k;
+        s.scratch = rem * 2 * 256 * 256 * 4;
     }
     return s;
 }
@@ -201,7 +227,8 @@ lmh_status_t launch_impl(const CUtensorMap &ta, const CUtensorMap &tb, const CUt
     if (tiles > kMaxDim)
         return LMH_ERR_INVALID_ARG;
     const int64_t units = RES == 1 ? num_sms() / C::CTAS : tiles;
-    const int64_t items = p.split_tiles > 0 ? tiles - p.split_tiles + units * p.split_rounds : tiles;
+    const int64_t items = q.split_parts > 0 ? tiles * q.split_parts
+                          : p.split_tiles > 0 ? tiles - p.split_tiles + units * p.split_rounds : tiles;
     const int grid = static_cast<int>((items < units ? items : units) * C::CTAS);
     return launch_ex(kern, dim3(grid), dim3(C::THREADS), C::SMEM_BYTES, stream, PAIR ? 2u : 1u, ta, tb, tc, ts,
                      tu, tp, p, q);
@@ -223,22 +250,24 @@ lmh_status_t launch_lora(const void *a, uint64_t a_inner, uint64_t a_outer, cons
                      !make_map(&tu, ad.ux, 64, ad.ux_rows, 64, C::BN_CTA)))
         return LMH_ERR_CUDA;
     std::memset(&tp, 0, sizeof tp);
-    if constexpr (!(A_MN && PAIR))
-        p.split_tiles = 0;
-    if (p.split_tiles > 0 && !make_out_map(&tp, ad.scratch, false, 256, static_cast<uint64_t>(p.split_tiles) * 2 * 256,
-                                           256, C::EPI_CHUNK))
+    // split tiles and their parts
+    const int64_t split = q.split_parts > 0 ? ceil_div(p.Mdim, C::TILE_M) * ceil_div(p.Ndim, BN) : p.split_tiles;
+    const int64_t parts = q.split_parts > 0 ? q.split_parts : 2;
+    if (split > 0 && !make_out_map(&tp, ad.scratch, false, C::TILE_M, static_cast<uint64_t>(split * parts * BN),
+                                   C::TILE_M, C::EPI_CHUNK))
         return LMH_ERR_CUDA;
     if (make_out_map(&tc, p.out, sizeof(OutT) == 2, static_cast<uint64_t>(p.Mdim), static_cast<uint64_t>(p.Ndim),
                      static_cast<uint64_t>(p.ldo), C::EPI_CHUNK))
     {
         const lmh_status_t r = launch_impl<BN, A_MN, OutT, true, PAIR, RES>(ta, tb, tc, ts, tu, tp, p, q, stream);
-        if (r != LMH_OK || p.split_tiles == 0)
+        if (r != LMH_OK || split == 0)
             return r;
-        p.num_m_tiles = static_cast<int32_t>(ceil_div(p.Mdim, 256));
-        p.num_n_tiles = static_cast<int32_t>(ceil_div(p.Ndim, 256));
-        return launch_ex(lmh::lora_join_kernel<OutT>, dim3(static_cast<unsigned>(p.split_tiles), 256 / lmh::kJoinRows),
-                         dim3(256), 0, stream, 1u, static_cast<const float *>(ad.scratch), static_cast<OutT *>(p.out), p,
-                         p.num_m_tiles * p.num_n_tiles - p.split_tiles);
+        p.num_m_tiles = static_cast<int32_t>(ceil_div(p.Mdim, C::TILE_M));
+        p.num_n_tiles = static_cast<int32_t>(ceil_div(p.Ndim, BN));
+        return launch_ex(lmh::lora_join_kernel<OutT>, dim3(static_cast<unsigned>(split), BN / lmh::kJoinRows), dim3(256),
+                         0, stream, 1u, static_cast<const float *>(ad.scratch), static_cast<OutT *>(p.out), p,
+                         static_cast<int32_t>(static_cast<int64_t>(p.num_m_tiles) * p.num_n_tiles - split),
+                         static_cast<int32_t>(parts), BN, C::TILE_M);
     }
     if constexpr (A_MN)
         return LMH_ERR_MISALIGNED;  // dX rows are multiples of 16 bytes and its base is checked
@@ -294,16 +323,18 @@ lmh_status_t run_rows(const void *Y, const void *P, const float *scale, const in
     }
     if (r != LMH_OK)
         return r;
+    // up to 128 tokens a CTA each, whose threads then share the ranges
+    const int64_t tokens = bn <= 128 ? 1 : lmh::kExpandTokens;
     return launch_ex(lmh::lora_expand_kernel,
-                     dim3(static_cast<unsigned>(g.tiles), static_cast<unsigned>(ceil_div(bn, lmh::kExpandTokens))),
-                     dim3(256), lmh::kExpandTokens * rank_pad(R) * sizeof(float), s, 1u,
+                     dim3(static_cast<unsigned>(g.tiles), static_cast<unsigned>(ceil_div(bn, tokens))),
+                     dim3(256), tokens * rank_pad(R) * sizeof(float), s, 1u,
                      static_cast<const float *>(partial), static_cast<int32_t>(rr.ranges), adapter, scale, t_out,
                      bn > 128 ? reinterpret_cast<__nv_bfloat16 *>(ws + g.ux) : nullptr,
                      reinterpret_cast<int2 *>(ws + g.count), reinterpret_cast<int2 *>(ws + g.slot),
                      reinterpret_cast<uint32_t *>(ws + g.slot_mask),
                      static_cast<int32_t>(bn), static_cast<int32_t>(g.slot_stride), static_cast<int32_t>(g.max_slots),
                      static_cast<int32_t>(g.stages), static_cast<int32_t>(g.parts), M, static_cast<int32_t>(R), static_cast<int32_t>(rank_pad(R)),
-                     static_cast<int32_t>(N), status);
+                     static_cast<int32_t>(N), static_cast<int32_t>(tokens), status);
 }
 
 LoraParams lora_params(uint8_t *ws, const GemmSpace &g, int64_t R, const void *adapters, const float *t)
@@ -377,7 +408,7 @@ int64_t lmhead_lora_workspace_bytes(int64_t M, int64_t K, int64_t V, int64_t R, 
     if (!lora_dims_ok(M, K, V, R, N))
         return -1;
     const int64_t f = gemm_space(M, K, R, N, pick_bn(M, 16), LMH_F32).bytes;
-    const int64_t d = gemm_space(M, V, R, N, pick_bn(M, 64), LMH_F32).bytes + dx_split(M, K, V).scratch_bytes();
+    const int64_t d = gemm_space(M, V, R, N, pick_bn(M, 64), LMH_F32).bytes + dx_split(M, K, V).scratch;
     const int64_t w = grad_space(M, R, N).bytes;
     const int64_t fd = f > d ? f : d;
     return fd > w ? fd : w;
@@ -442,7 +473,7 @@ lmh_status_t lmhead_bwd_dx_lora(const void *dlogits, const void *W, const void *
     const int bn = pick_bn(M, 64);
     const GemmSpace g = gemm_space(M, V, R, N, bn, out_dtype);
     const DxSplit split = dx_split(M, K, V);
-    if (workspace_bytes < g.bytes + split.scratch_bytes())
+    if (workspace_bytes < g.bytes + split.scratch)
         return LMH_ERR_INVALID_ARG;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
@@ -465,7 +496,9 @@ lmh_status_t lmhead_bwd_dx_lora(const void *dlogits, const void *W, const void *
     const AdapterOperands ad{A, static_cast<uint64_t>(K), static_cast<uint64_t>(R), static_cast<uint64_t>(N),
                              ws + g.ux, static_cast<uint64_t>(g.tiles * g.stages * bn),
                              reinterpret_cast<float *>(ws + g.bytes)};
-    const LoraParams q = lora_params(ws, g, R, A, g_out);
+    LoraParams q = lora_params(ws, g, R, A, g_out);
+    q.split_parts = static_cast<int32_t>(split.parts);
+    q.part_kb = static_cast<int32_t>(split.part_kb);
     const bool pair = K >= 256;
     const uint64_t k = static_cast<uint64_t>(K), v = static_cast<uint64_t>(V);
     return out_dtype == LMH_F32 ? dispatch_dx<float>(bn, pair, W, k, v, dlogits, ad, p, q, s)

@@ -77,6 +77,8 @@ struct LoraParams {
     int32_t parts;             // BF16 parts of u: 2, or 1 for a BF16 output
     int32_t stages_per_slot;   // ring stages of one slot: 1 up to 32 ranks, then `parts` per 64
     int32_t rank;
+    int32_t split_parts;       // dX: parts every tile's reduction is cut into (0: whole tiles)
+    int32_t part_kb;           // k-blocks of such a part (the last may have fewer)
     const __nv_bfloat16 *adapters;  // [adapter][Mdim][rank], A_MN: [adapter][rank][Mdim]
     const float *t;                 // u (g): [Ndim][rank]
 };
@@ -132,31 +134,44 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
     const int num_units = PAIR ? static_cast<int>(gridDim.x >> 1) : static_cast<int>(gridDim.x);
     const int num_tiles = p.num_m_tiles * p.num_n_tiles;
     const int num_kb = (p.Kdim + kBlockK - 1) / kBlockK;
-    // dX with 256-token tiles: the tiles of a last wave that would leave many units
-    // idle are split in two along the reduction, as in gemm_tc_kernel (long part
-    // [0, split_kb) on the unit that would have run the tile, short part, with the
-    // slots, on an idle one).  Both parts go to scratch (tmP) in FP32, and
-    // lora_join_kernel adds them.
-    constexpr bool SPLIT = A_MN && PAIR;
-    const int split_first = SPLIT ? num_tiles - p.split_tiles : num_tiles;
+    // dX, split along the reduction, the parts in FP32 to scratch (tmP), where
+    // lora_join_kernel adds them; the last part takes the slots.
+    // - Fewer tiles than units (few tokens, a narrow model): every tile into
+    //   split_parts parts, so that most units have one.  Where the epilogue warps form
+    //   the adapters' term, each part takes that of its share of the tokens.
+    // - Several waves: the tiles of a last wave that would leave many units idle in
+    //   two, as in gemm_tc_kernel: long part [0, split_kb) on the unit that would have
+    //   run the tile, short part on an idle one.
+    constexpr bool SPLIT = A_MN;
+    const bool all_split = SPLIT && q.split_parts > 0;
+    const int split_first = !SPLIT ? num_tiles : all_split ? 0 : num_tiles - p.split_tiles;
+    constexpr bool ROTATE = !A_MN && BN > 128;  // logits of several token tiles
     const int waves = (num_tiles + num_units - 1) / num_units;
-    const int num_items = !A_MN ? waves * num_units
-                          : SPLIT && p.split_tiles > 0 ? split_first + num_units * p.split_rounds : num_tiles;
-    // item -> tile and k-blocks: -1 a whole tile, 0 or 1 a part, 2 nothing to do
-    // Logits of several token tiles: the units that share a panel of W have to stay in
-    // step for L2 to serve all but one of them, while tiles take longer the more
-    // adapters their tokens have.  Each wave starts one tile further on, so that every
-    // unit comes by every token tile in turn (with 74 units and 16 token tiles, it
-    // would only see those of one parity: 4096 x 4096 x 128256 with 8 adapters read
-    // 4.2 GB from DRAM instead of 2.2 and took 3.45 ms instead of 3.28).
+    const int num_items = ROTATE ? waves * num_units
+                          : all_split ? num_tiles * q.split_parts
+                          : p.split_tiles > 0 ? split_first + num_units * p.split_rounds : num_tiles;
+    // item -> tile and k-blocks: -1 a whole tile, from 0 on a part, -2 nothing to do
+    // ROTATE: the units that share a panel of W have to stay in step for L2 to serve
+    // all but one of them, while tiles take longer the more adapters their tokens
+    // have.  Each wave starts one tile further on, so that every unit comes by every
+    // token tile in turn (with 74 units and 16 token tiles, it would only see those
+    // of one parity: 4096 x 4096 x 128256 with 8 adapters read 4.2 GB from DRAM instead
+    // of 2.2 and took 3.45 ms instead of 3.28).  With one token tile there is nothing
+    // to gain, and the index arithmetic costs (128 x 2048 x 32768: 76 against 64 us).
     auto item_of = [&](int it, int &t, int &kb0, int &kb1) -> int {
         t = it;
         kb0 = 0;
         kb1 = num_kb;
-        if (!A_MN) {
+        if (ROTATE) {
             const int w = it / num_units, u = it - w * num_units;
             t = w * num_units + (u + w) % num_units;
-            return t < num_tiles ? -1 : 2;
+            return t < num_tiles ? -1 : -2;
+        }
+        if (all_split) {
+            t = it / q.split_parts;
+            kb0 = (it - t * q.split_parts) * q.part_kb;
+            kb1 = min(num_kb, kb0 + q.part_kb);
+            return it - t * q.split_parts;
         }
         if (!SPLIT || it < split_first)
             return -1;
@@ -164,12 +179,12 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
         if (u < p.split_tiles) {
             t = split_first + u;
             kb1 = p.split_kb;
-            return r == 0 ? 0 : 2;
+            return r == 0 ? 0 : -2;
         }
         const int idx = (u - p.split_tiles) + r * (num_units - p.split_tiles);
         t = split_first + idx;
         kb0 = p.split_kb;
-        return idx < p.split_tiles ? 1 : 2;
+        return idx < p.split_tiles ? 1 : -2;
     };
 
     if (threadIdx.x == 0) {
@@ -193,7 +208,7 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
         }
         if (TMA_STORE)
             tma_prefetch_desc(&tmC);
-        if (SPLIT && p.split_tiles > 0)
+        if (all_split || (SPLIT && p.split_tiles > 0))
             tma_prefetch_desc(&tmP);
     }
     if (warp == 1) {
@@ -275,7 +290,7 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
             bool slots_there = false;
             for (int it = unit; it < num_items && ok; it += num_units) {
                 int t, kb0, kb1, mt, nt;
-                if (item_of(it, t, kb0, kb1) == 2)
+                if (item_of(it, t, kb0, kb1) == -2)
                     continue;
                 tile_coords(t, p, mt, nt);
                 const int m0 = mt * C::TILE_M + static_cast<int>(rank) * kBlockM;
@@ -382,7 +397,7 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
             };
             for (int it = unit; it < num_items && ok; it += num_units) {
                 int t, kb_first, kb_end, mt, nt;
-                if (item_of(it, t, kb_first, kb_end) == 2)
+                if (item_of(it, t, kb_first, kb_end) == -2)
                     continue;
                 tile_coords(t, p, mt, nt);
                 const bool slots = !IN_REGS && kb_end == num_kb;
@@ -489,14 +504,14 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
         for (int it = unit; it < num_items && ok; it += num_units) {
             int t, kb0, kb1, mt, nt;
             const int part = item_of(it, t, kb0, kb1);
-            if (part == 2)
+            if (part == -2)
                 continue;
             tile_coords(t, p, mt, nt);
             const int mbase = mt * C::TILE_M + static_cast<int>(rank) * kBlockM;
             const int m = mbase + quarter * 32 + lane;
             const int n0 = nt * BN + half * COLS;
             const int chunks = (kb1 - kb0 + kPromote - 1) / kPromote;
-            const int2 n = kb1 == num_kb ? q.count[nt] : make_int2(0, 0);
+            const int2 n = kb1 == num_kb || (IN_REGS && all_split) ? q.count[nt] : make_int2(0, 0);
             const int ns = n.x;
             const int all = IN_REGS ? chunks : chunks + n.y;
             const int2 *table = q.slot + static_cast<int64_t>(nt) * q.slot_stride;
@@ -538,6 +553,9 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
                 }
                 ++ch;
             };
+            // where the adapters' term waits, and for which tokens there is one
+            const uint32_t stash = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + 2 * BN + half * COLS;
+            uint32_t has[MW] = {};
             if constexpr (IN_REGS) {
                 // A piece is 8 ranks of one slot: 16 bytes per lane, its row of the
                 // adapter, through the lane's own places in the staging slots (free
@@ -549,8 +567,17 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
                 const int per_slot = q.rank / 8;
                 const int pieces = ns * per_slot;
                 const bool in = m < p.Mdim;
-                const uint32_t stash = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + 2 * BN + half * COLS;
-                uint32_t has[MW] = {};
+                uint32_t own[MW];  // this part's tokens
+#pragma unroll
+                for (int i = 0; i < MW; ++i)
+                    own[i] = 0xffffffffu;
+                if (all_split) {
+                    const int lo = part * BN / q.split_parts, hi = (part + 1) * BN / q.split_parts;
+                    auto below = [](int x) -> uint32_t { return x <= 0 ? 0u : x >= 32 ? 0xffffffffu : (1u << x) - 1u; };
+#pragma unroll
+                    for (int i = 0; i < MW; ++i)
+                        own[i] = below(hi - half * COLS - i * 32) & ~below(lo - half * COLS - i * 32);
+                }
                 int fs = 0, fr = 0, fetched = 0;  // slot and rank block of the next fetch
                 if (lane == 0)
                     bulk_wait_read<0>();  // the last tile's stores have left the slots
@@ -583,12 +610,15 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
                         take_shared();
                         release_acc();
                     }
-                    uint32_t mask[MW];
+                    uint32_t mask[MW], any = 0;
 #pragma unroll
                     for (int i = 0; i < MW; ++i) {
-                        mask[i] = masks[s * kSlotMaskWords + i];
+                        mask[i] = masks[s * kSlotMaskWords + i] & own[i];
                         has[i] |= mask[i];
+                        any |= mask[i];
                     }
+                    if (A_MN && any == 0)
+                        continue;
 #pragma unroll 1
                     for (int r0 = 0; r0 < q.rank; r0 += RC) {
                         const int n8 = min(RC / 8, (q.rank - r0) / 8);
@@ -648,19 +678,6 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
                 asm volatile("cp.async.wait_group 0;" ::: "memory");
                 tmem_st_wait();
                 __syncwarp();
-#pragma unroll
-                for (int c = 0; c < COLS; c += 16) {
-                    const uint32_t m16 = (has[c / 32] >> (c & 31)) & 0xffffu;
-                    if (m16 == 0)
-                        continue;
-                    uint32_t r[32];
-                    tmem_ld_chunk<16>(stash + c, r);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (m16 >> j & 1u)
-                            sum[c + j] += __uint_as_float(r[j]);
-                }
             }
             int s = 0;  // the next slot to be added, its place and tokens fetched ahead
             int32_t info = 0;
@@ -719,8 +736,25 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
             }
             if (!ok)
                 break;
+            if constexpr (IN_REGS) {
+                // last, whenever the accumulators came, so that the order is always the same
+#pragma unroll
+                for (int c = 0; c < COLS; c += 16) {
+                    const uint32_t m16 = (has[c / 32] >> (c & 31)) & 0xffffu;
+                    if (m16 == 0)
+                        continue;
+                    uint32_t r[32];
+                    tmem_ld_chunk<16>(stash + c, r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (m16 >> j & 1u)
+                            sum[c + j] += __uint_as_float(r[j]);
+                }
+            }
             if (SPLIT && part >= 0) {
-                const int y = ((t - split_first) * 2 + part) * BN + half * COLS;  // scratch row
+                const int parts = all_split ? q.split_parts : 2;
+                const int y = ((t - split_first) * parts + part) * BN + half * COLS;  // scratch row
                 float *fslots = reinterpret_cast<float *>(slots);
 #pragma unroll
                 for (int c = 0; c < COLS; c += CH) {
@@ -828,33 +862,40 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
         atomicOr(p.status, 2);
 }
 
-// out = long part + short part of the split tiles.  grid (split tiles, row groups);
-// Mdim is a multiple of 8.
+// out = the parts of the split tiles added in order.  grid (split tiles, row groups);
+// Mdim is a multiple of 8.  scratch [tile][part][bn][tile_m].
 constexpr int kJoinRows = 8;
 
 template <typename OutT>
 __global__ void __launch_bounds__(256)
-    lora_join_kernel(const float *__restrict__ scratch, OutT *__restrict__ out, const GemmParams p, int32_t split_first)
+    lora_join_kernel(const float *__restrict__ scratch, OutT *__restrict__ out, const GemmParams p, int32_t split_first,
+                     int32_t parts, int32_t bn, int32_t tile_m)
 {
     pdl_wait();
     pdl_launch_dependents();
     int mt, nt;
     tile_coords(split_first + static_cast<int>(blockIdx.x), p, mt, nt);
-    const int m = mt * 256 + (threadIdx.x & 63) * 4;
+    const int lanes = tile_m / 4, c = static_cast<int>(threadIdx.x) % lanes * 4;
+    const int m = mt * tile_m + c;
     if (m >= p.Mdim)
         return;
-    for (int r = threadIdx.x >> 6; r < kJoinRows; r += 4) {
+    for (int r = threadIdx.x / lanes; r < kJoinRows; r += 256 / lanes) {
         const int row = blockIdx.y * kJoinRows + r;
-        const int64_t n = static_cast<int64_t>(nt) * 256 + row;
+        const int64_t n = static_cast<int64_t>(nt) * bn + row;
         if (n >= p.Ndim)
             return;
-        const float *s = scratch + ((static_cast<int64_t>(blockIdx.x) * 2) * 256 + row) * 256 + (threadIdx.x & 63) * 4;
-        const float4 a = *reinterpret_cast<const float4 *>(s), b = *reinterpret_cast<const float4 *>(s + 256 * 256);
+        const float *s = scratch + (static_cast<int64_t>(blockIdx.x) * parts * bn + row) * tile_m + c;
+        float4 a = *reinterpret_cast<const float4 *>(s);
+#pragma unroll 8
+        for (int k = 1; k < parts; ++k) {
+            const float4 b = *reinterpret_cast<const float4 *>(s + static_cast<int64_t>(k) * bn * tile_m);
+            a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
+        }
         OutT *o = out + n * p.ldo + m;
-        store_out(o, __float_as_uint(a.x + b.x));
-        store_out(o + 1, __float_as_uint(a.y + b.y));
-        store_out(o + 2, __float_as_uint(a.z + b.z));
-        store_out(o + 3, __float_as_uint(a.w + b.w));
+        store_out(o, __float_as_uint(a.x));
+        store_out(o + 1, __float_as_uint(a.y));
+        store_out(o + 2, __float_as_uint(a.z));
+        store_out(o + 3, __float_as_uint(a.w));
     }
 }
 

@@ -39,7 +39,7 @@ constexpr int kColsTokens = 32;    // tokens staged at once
 constexpr int kColsThreads = 128;
 constexpr int kColsStages = 3;
 constexpr int kColsPromote = 8;    // stages (256 tokens) summed in the MMAs
-constexpr int kExpandTokens = 4;  // tokens of one lora_expand_kernel CTA
+constexpr int kExpandTokens = 4;  // tokens of one lora_expand_kernel CTA, at most
 constexpr int kDevBadAdapter = 0x8;  // LMH_DEV_BAD_ADAPTER
 
 // 16 bytes global -> shared; zeros where `in` is false (nothing is read then).
@@ -310,7 +310,7 @@ __device__ __forceinline__ __nv_bfloat16 split_hi(float x, float &rest)
     return h;
 }
 
-// grid (token tiles of the GEMM, parts of kExpandTokens tokens).
+// grid (token tiles of the GEMM, parts of `tokens` tokens).
 //   t    [M][R] FP32, scaled: u or g (0 for a token without adapter)
 //   ux   (or NULL) [tile][stages][bn][64] BF16.  Of two parts: up to 32 ranks one
 //        stage {high 0..31, low 0..31}, above that per 64 ranks a stage of high and
@@ -322,12 +322,12 @@ __global__ void __launch_bounds__(256)
                        __nv_bfloat16 *__restrict__ ux, int2 *__restrict__ tile_count,
                        int2 *__restrict__ slot_table, uint32_t *__restrict__ slot_mask, int32_t bn,
                        int32_t slot_stride, int32_t max_slots, int32_t stages, int32_t parts, int64_t M,
-                       int32_t R, int32_t Rpad, int32_t N, int32_t *status)
+                       int32_t R, int32_t Rpad, int32_t N, int32_t tokens, int32_t *status)
 {
     __shared__ int32_t ids[256];
     __shared__ int32_t warp_n[8];
     __shared__ double share[256];
-    extern __shared__ float val[];  // [kExpandTokens][Rpad]
+    extern __shared__ float val[];  // [tokens][Rpad]
     // The GEMM may begin with the shared product at once: all that it reads of that
     // was complete before the row kernel let this one start.
     pdl_launch_dependents();
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(256)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t tile = blockIdx.x;
     const int64_t i0 = tile * bn;
-    const int tok0 = blockIdx.y * kExpandTokens;
+    const int tok0 = blockIdx.y * tokens;
     if (tid < bn) {
         int32_t a = i0 + tid < M ? adapter[i0 + tid] : -1;
         if (a < -1 || a >= N) {
@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(256)
 
     // Sums over the ranges: `lanes` threads take every lanes-th range of an item
     // (token, rank), and the first of them adds theirs in order.
-    const int items = kExpandTokens * Rpad;
+    const int items = tokens * Rpad;
     const int lanes = items >= 256 ? 1 : 256 / items;
     const int per_pass = 256 / lanes;
     for (int k0 = 0; k0 < items; k0 += per_pass) {
@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(256)
     __syncthreads();
     // the split parts of this CTA's tokens, eight columns per store
     const int per_token = stages * 8;
-    for (int k = tid; ux && k < kExpandTokens * per_token; k += 256) {
+    for (int k = tid; ux && k < tokens * per_token; k += 256) {
         const int j = k / per_token, rest = k % per_token;
         const int st = rest >> 3, c0 = (rest & 7) * 8;
         const int tk = tok0 + j;
@@ -440,12 +440,12 @@ __global__ void __launch_bounds__(256)
     if (lane == 0)
         warp_n[warp] = __popc(b) | __popc(with) << 16;
     __syncthreads();
-    int slot = __popc(b & ((1u << lane) - 1u)), all = 0, tokens = 0;
+    int slot = __popc(b & ((1u << lane) - 1u)), all = 0, having = 0;
     for (int w = 0; w < 8; ++w) {
         if (w < warp)
             slot += warp_n[w] & 0xffff;
         all += warp_n[w] & 0xffff;
-        tokens += warp_n[w] >> 16;
+        having += warp_n[w] >> 16;
     }
     if (first) {
         spans[slot] = lead[h] / 32 | (tail[h] / 32 - lead[h] / 32 + 1) << 4;
@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(256)
     // a tile whose tokens all have it needs none: its span is the whole tile.
     const int64_t rows = M - i0 < bn ? M - i0 : bn;
     int packs = 0;
-    if (all == 1 && tokens == rows) {
+    if (all == 1 && having == rows) {
         slot_table[tile * slot_stride].y = slot_info(0, 256, 0, 1);
     } else {
         int off = 0;

@@ -239,6 +239,22 @@ def test_adapter_order_does_not_matter_and_is_deterministic():
     assert torch.equal(one[perm], three) and torch.equal(u1[perm], u3)
 
 
+@pytest.mark.parametrize("M,N,R", [(1, 3, 16), (16, 9, 16), (64, 16, 64), (128, 40, 16)])
+def test_forward_is_the_same_beside_other_work(M, N, R):
+    X, W, A, B, scale, ids = make(M, 4096, 9000, R, N, none=True)
+    one, u1 = fwd(X, W, A, B, scale, ids)
+    busy, side = torch.randn((2048, 2048), device=DEV), torch.cuda.Stream()
+    for i in range(20):
+        with torch.cuda.stream(side):
+            for _ in range(i % 4):
+                busy @ busy
+        two, u2 = fwd(X, W, A, B, scale, ids)
+        assert torch.equal(one, two) and torch.equal(u1, u2)
+    perm = torch.randperm(M, generator=torch.Generator().manual_seed(4)).to(DEV)
+    two, u2 = fwd(X[perm].contiguous(), W, A, B, scale, ids[perm].contiguous())
+    assert torch.equal(one[perm], two) and torch.equal(u1[perm], u2)
+
+
 @pytest.mark.parametrize("M", [5, 70, 300])
 def test_bad_values_stay_with_their_adapter(M):
     X, W, A, B, scale, ids = make(M, 256, 515, 16, 3, none=True)
@@ -344,6 +360,36 @@ def check_bwd(M, K, V, R, N, order, dtype, seed=0):
 ])
 def test_backward(M, K, V, R, N, order):
     check_bwd(M, K, V, R, N, order, torch.bfloat16 if M % 2 else torch.float32)
+
+
+@pytest.mark.parametrize("order", ["random", "runs"])
+@pytest.mark.parametrize("M,K,V,R,N", [  # every tile of dX cut along the vocabulary
+    (1, 8, 4096, 8, 1), (16, 512, 2056, 8, 3), (60, 792, 9000, 16, 4), (37, 136, 40000, 24, 40),
+    (64, 2048, 8192, 256, 5), (100, 1024, 16392, 48, 90), (128, 256, 5000, 16, 2), (127, 4096, 6000, 8, 1),
+    (200, 200, 9000, 40, 6), (300, 1032, 12296, 32, 7), (513, 256, 33000, 64, 3), (257, 3000, 4104, 16, 257),
+])
+def test_backward_cut_along_the_vocabulary(M, K, V, R, N, order):
+    check_bwd(M, K, V, R, N, order, torch.bfloat16 if V % 16 else torch.float32)
+
+
+@pytest.mark.parametrize("M", [40, 120, 300])
+def test_cut_backward_is_deterministic_and_keeps_bad_values_apart(M):
+    V = 6000
+    X, W, A, B, scale, ids = make(M, 512, V, 16, 3)
+    ids[::3] = 1
+    gen = torch.Generator().manual_seed(4)
+    dl = torch.randn((M, V), generator=gen).to(torch.bfloat16).to(DEV)
+    u = torch.randn((M, 16), generator=gen).to(DEV)
+    ref = bwd(dl, X, W, A, B, scale, ids, u)
+    for _ in range(20):
+        for p, q in zip(ref, bwd(dl, X, W, A, B, scale, ids, u)):
+            assert torch.equal(p, q)
+    A2, B2 = A.clone(), B.clone()
+    A2[1], B2[1, 100:200] = float("nan"), float("inf")
+    got = bwd(dl, X, W, A2, B2, scale, ids, u)
+    o = ids != 1
+    assert torch.equal(got[0][o], ref[0][o]) and torch.equal(got[1][o], ref[1][o])
+    assert torch.isnan(got[1][~o]).all()
 
 
 def test_backward_long_reduction_norm():
