@@ -323,8 +323,8 @@ lmh_status_t run_rows(const void *Y, const void *P, const float *scale, const in
     }
     if (r != LMH_OK)
         return r;
-    // up to 128 tokens a CTA each, whose threads then share the ranges
-    const int64_t tokens = bn <= 128 ? 1 : lmh::kExpandTokens;
+    // few tokens and many ranges: a CTA per token, whose threads share the ranges
+    const int64_t tokens = bn <= 128 && rr.ranges > 64 ? 1 : lmh::kExpandTokens;
     return launch_ex(lmh::lora_expand_kernel,
                      dim3(static_cast<unsigned>(g.tiles), static_cast<unsigned>(ceil_div(bn, tokens))),
                      dim3(256), tokens * rank_pad(R) * sizeof(float), s, 1u,

@@ -156,15 +156,17 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
     // have.  Each wave starts one tile further on, so that every unit comes by every
     // token tile in turn (with 74 units and 16 token tiles, it would only see those
     // of one parity: 4096 x 4096 x 128256 with 8 adapters read 4.2 GB from DRAM instead
-    // of 2.2 and took 3.45 ms instead of 3.28).  With one token tile there is nothing
-    // to gain, and the index arithmetic costs (128 x 2048 x 32768: 76 against 64 us).
+    // of 2.2 and took 3.45 ms instead of 3.28).  The last wave's tiles, fewer than the
+    // units, go to the first ones: the last ones start late, where the row kernel ran
+    // (200 x 2048 x 60000: 98 against 89 us).  With one narrow token tile there is nothing
+    // to gain, and the index arithmetic costs (64 x 4096 x 32768, rank 64: 121 against 107 us).
     auto item_of = [&](int it, int &t, int &kb0, int &kb1) -> int {
         t = it;
         kb0 = 0;
         kb1 = num_kb;
         if (ROTATE) {
             const int w = it / num_units, u = it - w * num_units;
-            t = w * num_units + (u + w) % num_units;
+            t = w * num_units + (w + 1 < waves ? (u + w) % num_units : u);
             return t < num_tiles ? -1 : -2;
         }
         if (all_split) {
