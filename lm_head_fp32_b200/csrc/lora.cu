@@ -111,41 +111,57 @@ GradSpace grad_space(int64_t M, int64_t R, int64_t N)
     return g;
 }
 
-// How dX is split along its reduction.  Either every tile into `parts` parts of
-// `part_kb` k-blocks, or `tiles` tiles of the last wave in two, each unit (CTA pair)
-// that the wave leaves idle taking `rounds` short parts: as lmhead_bwd_dx, where that
-// rule is explained and measured.
-struct DxSplit {
+// How the tiles are split along the reduction.  Either every tile into `parts` parts
+// of `part_kb` k-blocks, or (dX) `tiles` tiles of the last wave in two, each unit (CTA
+// pair) that the wave leaves idle taking `rounds` short parts: as lmhead_bwd_dx, where
+// that rule is explained and measured.
+struct Split {
     int64_t parts = 0, part_kb = 0;
     int64_t tiles = 0, kb = 0, rounds = 0;
     int64_t scratch = 0;  // bytes
 };
-constexpr int64_t kMaxSplitRounds = 8;
-constexpr int64_t kMinPartKb = 16;
-DxSplit dx_split(int64_t M, int64_t K, int64_t V)
+// Fewer tiles than units: the number of parts that takes the least time, counted in
+// k-blocks on the busiest unit, each part with what handing it over costs (about 3 us
+// for the 256 KB of a pair's tile, a k-block 0.3 us; narrow tiles a third of that) and
+// `join` for the second kernel.
+Split split_all(int64_t tiles, int64_t units, int64_t num_kb, int64_t bn, int64_t tile_m, int64_t join)
 {
-    DxSplit s;
+    Split s;
+    const int64_t cost = bn == 256 ? 20 : 8;
+    int64_t best = num_kb;
+    for (int64_t n = 2; n * 8 <= num_kb && n * tiles <= 2 * units; ++n) {
+        const int64_t kb = ceil_div(ceil_div(num_kb, n), 8) * 8, parts = ceil_div(num_kb, kb);
+        const int64_t t = ceil_div(tiles * parts, units) * (kb + cost) + join;
+        if (parts > 1 && t < best) {
+            best = t;
+            s.parts = parts;
+            s.part_kb = kb;
+        }
+    }
+    if (s.parts > 0)
+        s.scratch = tiles * lmh::split_slabs(static_cast<int>(bn), static_cast<int>(s.parts)) * bn * tile_m * 4;
+    return s;
+}
+
+constexpr int64_t kJoinKb = 8;  // the second kernel, in k-blocks
+Split fwd_split(int64_t M, int64_t K, int64_t V)
+{
+    const int64_t bn = pick_bn(M, 16), tile_m = bn == 256 ? 256 : 128;
+    if (V < tile_m)
+        return {};
+    const int64_t units = num_sms() / (tile_m / 128), tiles = ceil_div(V, tile_m) * ceil_div(M, bn);
+    return tiles <= units ? split_all(tiles, units, ceil_div(K, lmh::kBlockK), bn, tile_m, kJoinKb) : Split{};
+}
+
+constexpr int64_t kMaxSplitRounds = 8;
+Split dx_split(int64_t M, int64_t K, int64_t V)
+{
     const int64_t bn = pick_bn(M, 64), tile_m = bn == 256 && K >= 256 ? 256 : 128;
     const int64_t units = num_sms() / (tile_m / 128), tiles = ceil_div(K, tile_m) * ceil_div(M, bn);
     const int64_t num_kb = ceil_div(V, lmh::kBlockK);
-    if (tiles <= units) {
-        // The number of parts that takes the least time, counted in k-blocks on the
-        // busiest unit, each part with what handing it over costs (about 3 us for the
-        // 256 KB of a pair's tile, a k-block 0.3 us; narrow tiles a quarter of that).
-        const int64_t cost = bn == 256 ? 20 : 8;
-        int64_t best = num_kb;
-        for (int64_t n = 2; n * kMinPartKb <= num_kb && n * tiles <= 2 * units; ++n) {
-            const int64_t kb = ceil_div(ceil_div(num_kb, n), 8) * 8, parts = ceil_div(num_kb, kb);
-            const int64_t t = ceil_div(tiles * parts, units) * (kb + cost);
-            if (parts > 1 && t < best) {
-                best = t;
-                s.parts = parts;
-                s.part_kb = kb;
-            }
-        }
-        s.scratch = tiles * s.parts * bn * tile_m * 4;
-        return s;
-    }
+    if (tiles <= units)
+        return split_all(tiles, units, num_kb, bn, tile_m, kJoinKb);
+    Split s;
     if (tile_m != 256)
         return s;
     const int64_t rem = tiles % units;
@@ -209,14 +225,14 @@ struct AdapterOperands {
     float *scratch;           // the parts of split tiles
 };
 
-template <int BN, bool A_MN, typename OutT, bool TMA_STORE, bool PAIR, int RES>
+template <int BN, bool A_MN, typename OutT, bool TMA_STORE, bool PAIR, int RES, bool SPLIT = A_MN>
 lmh_status_t launch_impl(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &tc, const CUtensorMap &ts,
                          const CUtensorMap &tu, const CUtensorMap &tp, GemmParams p, const LoraParams &q,
                          cudaStream_t stream)
 {
     constexpr int EW = lmh::lora_epi_warps(BN);
     using C = GemmCfg<BN, A_MN, false, PAIR, RES, EW>;
-    auto kern = lmh::lora_gemm_kernel<BN, A_MN, OutT, TMA_STORE, PAIR, RES, EW>;
+    auto kern = lmh::lora_gemm_kernel<BN, A_MN, OutT, TMA_STORE, PAIR, RES, EW, SPLIT>;
     static std::atomic<uint64_t> set{0};
     if (const lmh_status_t r = allow_smem(kern, C::SMEM_BYTES, set); r != LMH_OK)
         return r;
@@ -226,16 +242,18 @@ lmh_status_t launch_impl(const CUtensorMap &ta, const CUtensorMap &tb, const CUt
     const int64_t tiles = static_cast<int64_t>(p.num_m_tiles) * p.num_n_tiles;
     if (tiles > kMaxDim)
         return LMH_ERR_INVALID_ARG;
-    const int64_t units = RES == 1 ? num_sms() / C::CTAS : tiles;
+    const int64_t ctas = num_sms() / C::CTAS;
     const int64_t items = q.split_parts > 0 ? tiles * q.split_parts
-                          : p.split_tiles > 0 ? tiles - p.split_tiles + units * p.split_rounds : tiles;
+                          : p.split_tiles > 0 ? tiles - p.split_tiles + ctas * p.split_rounds : tiles;
+    const int64_t units = RES == 1 ? ctas : items;
     const int grid = static_cast<int>((items < units ? items : units) * C::CTAS);
     return launch_ex(kern, dim3(grid), dim3(C::THREADS), C::SMEM_BYTES, stream, PAIR ? 2u : 1u, ta, tb, tc, ts,
                      tu, tp, p, q);
 }
 
 // A: the shared weights [outer][inner], MN-major (dX) or K-major; B: [Ndim][Kdim].
-template <int BN, bool A_MN, typename OutT, bool PAIR, int RES = 1>
+// SPLIT: see lora_gemm_kernel.
+template <int BN, bool A_MN, typename OutT, bool PAIR, int RES = 1, bool SPLIT = A_MN>
 lmh_status_t launch_lora(const void *a, uint64_t a_inner, uint64_t a_outer, const void *b, const AdapterOperands &ad,
                          GemmParams p, const LoraParams &q, cudaStream_t stream)
 {
@@ -252,27 +270,32 @@ lmh_status_t launch_lora(const void *a, uint64_t a_inner, uint64_t a_outer, cons
     std::memset(&tp, 0, sizeof tp);
     // split tiles and their parts
     const int64_t split = q.split_parts > 0 ? ceil_div(p.Mdim, C::TILE_M) * ceil_div(p.Ndim, BN) : p.split_tiles;
-    const int64_t parts = q.split_parts > 0 ? q.split_parts : 2;
+    const int64_t parts = q.split_parts > 0 ? lmh::split_slabs(BN, q.split_parts) : 2;
     if (split > 0 && !make_out_map(&tp, ad.scratch, false, C::TILE_M, static_cast<uint64_t>(split * parts * BN),
                                    C::TILE_M, C::EPI_CHUNK))
         return LMH_ERR_CUDA;
-    if (make_out_map(&tc, p.out, sizeof(OutT) == 2, static_cast<uint64_t>(p.Mdim), static_cast<uint64_t>(p.Ndim),
-                     static_cast<uint64_t>(p.ldo), C::EPI_CHUNK))
-    {
-        const lmh_status_t r = launch_impl<BN, A_MN, OutT, true, PAIR, RES>(ta, tb, tc, ts, tu, tp, p, q, stream);
-        if (r != LMH_OK || split == 0)
-            return r;
-        p.num_m_tiles = static_cast<int32_t>(ceil_div(p.Mdim, C::TILE_M));
-        p.num_n_tiles = static_cast<int32_t>(ceil_div(p.Ndim, BN));
-        return launch_ex(lmh::lora_join_kernel<OutT>, dim3(static_cast<unsigned>(split), BN / lmh::kJoinRows), dim3(256),
-                         0, stream, 1u, static_cast<const float *>(ad.scratch), static_cast<OutT *>(p.out), p,
-                         static_cast<int32_t>(static_cast<int64_t>(p.num_m_tiles) * p.num_n_tiles - split),
-                         static_cast<int32_t>(parts), BN, C::TILE_M);
+    const bool tma = make_out_map(&tc, p.out, sizeof(OutT) == 2, static_cast<uint64_t>(p.Mdim),
+                                  static_cast<uint64_t>(p.Ndim), static_cast<uint64_t>(p.ldo), C::EPI_CHUNK);
+    lmh_status_t r;
+    if constexpr (SPLIT && !A_MN) {
+        // logits: no tile is stored whole
+        r = launch_impl<BN, false, float, true, PAIR, RES, true>(ta, tb, tp, ts, tu, tp, p, q, stream);
+    } else if (tma) {
+        r = launch_impl<BN, A_MN, OutT, true, PAIR, RES>(ta, tb, tc, ts, tu, tp, p, q, stream);
+    } else {
+        if constexpr (A_MN)
+            return LMH_ERR_MISALIGNED;  // dX rows are multiples of 16 bytes and its base is checked
+        std::memset(&tc, 0, sizeof tc);
+        r = launch_impl<BN, A_MN, OutT, A_MN, PAIR, RES>(ta, tb, tc, ts, tu, tp, p, q, stream);
     }
-    if constexpr (A_MN)
-        return LMH_ERR_MISALIGNED;  // dX rows are multiples of 16 bytes and its base is checked
-    std::memset(&tc, 0, sizeof tc);
-    return launch_impl<BN, A_MN, OutT, A_MN, PAIR, RES>(ta, tb, tc, ts, tu, tp, p, q, stream);
+    if (r != LMH_OK || split == 0)
+        return r;
+    p.num_m_tiles = static_cast<int32_t>(ceil_div(p.Mdim, C::TILE_M));
+    p.num_n_tiles = static_cast<int32_t>(ceil_div(p.Ndim, BN));
+    const int64_t whole = static_cast<int64_t>(p.num_m_tiles) * p.num_n_tiles - split;
+    return launch_ex(lmh::lora_join_kernel<OutT>, dim3(static_cast<unsigned>(split), BN / lmh::kJoinRows), dim3(256), 0,
+                     stream, 1u, static_cast<const float *>(ad.scratch), static_cast<OutT *>(p.out), p,
+                     static_cast<int32_t>(whole), static_cast<int32_t>(parts), BN, C::TILE_M);
 }
 
 template <bool P_MN, int NT>
@@ -369,20 +392,23 @@ lmh_status_t launch_cols(const lmh::ColsOp &b, const lmh::ColsOp &a, const int32
                      static_cast<int32_t>(rank_pad(R)));
 }
 
-template <typename OutT>
+// SPLIT: the tiles are split along K.
+template <typename OutT, bool SPLIT>
 lmh_status_t dispatch_fwd(int bn, bool pair, const void *W, uint64_t K, uint64_t V, const void *X,
                           const AdapterOperands &ad, const GemmParams &p, const LoraParams &q, cudaStream_t s)
 {
     switch (bn) {
     // one token tile: bound by W.  Two CTAs resident per SM where tensor memory has
     // room for both
-    case 16: return launch_lora<16, false, OutT, false, 2>(W, K, V, X, ad, p, q, s);
-    case 32: return launch_lora<32, false, OutT, false, 2>(W, K, V, X, ad, p, q, s);
-    case 64: return launch_lora<64, false, OutT, false, 2>(W, K, V, X, ad, p, q, s);
-    case 128: return launch_lora<128, false, OutT, false>(W, K, V, X, ad, p, q, s);
+    case 16: return launch_lora<16, false, OutT, false, 2, SPLIT>(W, K, V, X, ad, p, q, s);
+    case 32: return launch_lora<32, false, OutT, false, 2, SPLIT>(W, K, V, X, ad, p, q, s);
+    case 64: return launch_lora<64, false, OutT, false, 2, SPLIT>(W, K, V, X, ad, p, q, s);
+    case 128: return launch_lora<128, false, OutT, false, 1, SPLIT>(W, K, V, X, ad, p, q, s);
     default:
-        return pair ? launch_lora<256, false, OutT, true>(W, K, V, X, ad, p, q, s)
-                    : launch_lora<256, false, OutT, false>(W, K, V, X, ad, p, q, s);
+        if constexpr (!SPLIT)  // a split one is at least 256 wide
+            if (!pair)
+                return launch_lora<256, false, OutT, false>(W, K, V, X, ad, p, q, s);
+        return launch_lora<256, false, OutT, true, 1, SPLIT>(W, K, V, X, ad, p, q, s);
     }
 }
 
@@ -407,7 +433,7 @@ int64_t lmhead_lora_workspace_bytes(int64_t M, int64_t K, int64_t V, int64_t R, 
 {
     if (!lora_dims_ok(M, K, V, R, N))
         return -1;
-    const int64_t f = gemm_space(M, K, R, N, pick_bn(M, 16), LMH_F32).bytes;
+    const int64_t f = gemm_space(M, K, R, N, pick_bn(M, 16), LMH_F32).bytes + fwd_split(M, K, V).scratch;
     const int64_t d = gemm_space(M, V, R, N, pick_bn(M, 64), LMH_F32).bytes + dx_split(M, K, V).scratch;
     const int64_t w = grad_space(M, R, N).bytes;
     const int64_t fd = f > d ? f : d;
@@ -429,7 +455,8 @@ lmh_status_t lmhead_fwd_lora(const void *X, const void *W, const void *A, const 
         return LMH_ERR_MISALIGNED;
     const int bn = pick_bn(M, 16);
     const GemmSpace g = gemm_space(M, K, R, N, bn, out_dtype);
-    if (workspace_bytes < g.bytes)
+    const Split split = fwd_split(M, K, V);
+    if (workspace_bytes < g.bytes + split.scratch)
         return LMH_ERR_INVALID_ARG;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
@@ -448,12 +475,19 @@ lmh_status_t lmhead_fwd_lora(const void *X, const void *W, const void *A, const 
     p.l2_out = 1;
     p.status = status;
     const AdapterOperands ad{B, static_cast<uint64_t>(R), static_cast<uint64_t>(V), static_cast<uint64_t>(N),
-                             ws + g.ux, static_cast<uint64_t>(g.tiles * g.stages * bn), nullptr};
-    const LoraParams q = lora_params(ws, g, R, B, u);
+                             ws + g.ux, static_cast<uint64_t>(g.tiles * g.stages * bn),
+                             reinterpret_cast<float *>(ws + g.bytes)};
+    LoraParams q = lora_params(ws, g, R, B, u);
+    q.split_parts = static_cast<int32_t>(split.parts);
+    q.part_kb = static_cast<int32_t>(split.part_kb);
+    q.scratch = ad.scratch;
     const bool pair = V >= 256;
     const uint64_t k = static_cast<uint64_t>(K), v = static_cast<uint64_t>(V);
-    return out_dtype == LMH_F32 ? dispatch_fwd<float>(bn, pair, W, k, v, X, ad, p, q, s)
-                                : dispatch_fwd<__nv_bfloat16>(bn, pair, W, k, v, X, ad, p, q, s);
+    if (split.parts > 0)
+        return out_dtype == LMH_F32 ? dispatch_fwd<float, true>(bn, pair, W, k, v, X, ad, p, q, s)
+                                    : dispatch_fwd<__nv_bfloat16, true>(bn, pair, W, k, v, X, ad, p, q, s);
+    return out_dtype == LMH_F32 ? dispatch_fwd<float, false>(bn, pair, W, k, v, X, ad, p, q, s)
+                                : dispatch_fwd<__nv_bfloat16, false>(bn, pair, W, k, v, X, ad, p, q, s);
 }
 
 lmh_status_t lmhead_bwd_dx_lora(const void *dlogits, const void *W, const void *A, const void *B, const float *scale,
@@ -472,7 +506,7 @@ lmh_status_t lmhead_bwd_dx_lora(const void *dlogits, const void *W, const void *
         return LMH_ERR_MISALIGNED;
     const int bn = pick_bn(M, 64);
     const GemmSpace g = gemm_space(M, V, R, N, bn, out_dtype);
-    const DxSplit split = dx_split(M, K, V);
+    const Split split = dx_split(M, K, V);
     if (workspace_bytes < g.bytes + split.scratch)
         return LMH_ERR_INVALID_ARG;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -499,6 +533,7 @@ lmh_status_t lmhead_bwd_dx_lora(const void *dlogits, const void *W, const void *
     LoraParams q = lora_params(ws, g, R, A, g_out);
     q.split_parts = static_cast<int32_t>(split.parts);
     q.part_kb = static_cast<int32_t>(split.part_kb);
+    q.scratch = ad.scratch;
     const bool pair = K >= 256;
     const uint64_t k = static_cast<uint64_t>(K), v = static_cast<uint64_t>(V);
     return out_dtype == LMH_F32 ? dispatch_dx<float>(bn, pair, W, k, v, dlogits, ad, p, q, s)

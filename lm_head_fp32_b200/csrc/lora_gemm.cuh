@@ -68,6 +68,10 @@ __host__ __device__ constexpr int slot_span(int32_t i) { return (i >> 4 & 15) * 
 __host__ __device__ constexpr int slot_off(int32_t i) { return (i >> 8 & 15) * 32; }
 __host__ __device__ constexpr bool slot_last(int32_t i) { return i >> 12 & 1; }  // of its accumulator
 
+// What a tile split into `parts` puts into scratch: the parts, and the adapters' term
+// where it is formed by itself.
+__host__ __device__ constexpr int split_slabs(int bn, int parts) { return parts + (bn <= 128 ? 1 : 0); }
+
 struct LoraParams {
     const int2 *count;         // per token tile: {slots, accumulators they take; 0: the shared one}
     const int2 *slot;          // [token tile][slot_stride]: {adapter, slot_info}
@@ -79,6 +83,7 @@ struct LoraParams {
     int32_t rank;
     int32_t split_parts;       // dX: parts every tile's reduction is cut into (0: whole tiles)
     int32_t part_kb;           // k-blocks of such a part (the last may have fewer)
+    float *scratch;            // [tile][split_slabs][BN][tile's rows]
     const __nv_bfloat16 *adapters;  // [adapter][Mdim][rank], A_MN: [adapter][rank][Mdim]
     const float *t;                 // u (g): [Ndim][rank]
 };
@@ -97,7 +102,11 @@ __host__ __device__ constexpr uint32_t lora_tmem_cols(int bn)
     return n;
 }
 
-template <int BN, bool A_MN, typename OutT, bool TMA_STORE, bool PAIR, int RES = 1, int EW = lora_epi_warps(BN)>
+// SPLIT: tiles may be split along the reduction (logits: all are, and the parts go to
+// lora_join_kernel).  A parameter of its own, so that the logits' kernels without it
+// keep their registers.
+template <int BN, bool A_MN, typename OutT, bool TMA_STORE, bool PAIR, int RES = 1, int EW = lora_epi_warps(BN),
+          bool SPLIT = A_MN>
 __global__ void __launch_bounds__(64 + 32 * EW, RES)
     lora_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmS,
@@ -134,18 +143,19 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
     const int num_units = PAIR ? static_cast<int>(gridDim.x >> 1) : static_cast<int>(gridDim.x);
     const int num_tiles = p.num_m_tiles * p.num_n_tiles;
     const int num_kb = (p.Kdim + kBlockK - 1) / kBlockK;
-    // dX, split along the reduction, the parts in FP32 to scratch (tmP), where
+    // Split along the reduction, the parts go to scratch (tmP) in FP32, where
     // lora_join_kernel adds them; the last part takes the slots.
-    // - Fewer tiles than units (few tokens, a narrow model): every tile into
+    // - Fewer tiles than units (few tokens; a narrow model, a small vocabulary): every tile into
     //   split_parts parts, so that most units have one.  Where the epilogue warps form
-    //   the adapters' term, each part takes that of its share of the tokens.
-    // - Several waves: the tiles of a last wave that would leave many units idle in
+    //   the adapters' term, each part takes that of its share of the tokens, and it
+    //   goes to scratch as one part more: a token's sums are the same wherever in the
+    //   batch it stands.
+    // - Several waves of dX's tiles: the tiles of a last wave that would leave many units idle in
     //   two, as in gemm_tc_kernel: long part [0, split_kb) on the unit that would have
     //   run the tile, short part on an idle one.
-    constexpr bool SPLIT = A_MN;
     const bool all_split = SPLIT && q.split_parts > 0;
     const int split_first = !SPLIT ? num_tiles : all_split ? 0 : num_tiles - p.split_tiles;
-    constexpr bool ROTATE = !A_MN && BN > 128;  // logits of several token tiles
+    constexpr bool ROTATE = !A_MN && BN > 128 && !SPLIT;  // logits of several token tiles
     const int waves = (num_tiles + num_units - 1) / num_units;
     const int num_items = ROTATE ? waves * num_units
                           : all_split ? num_tiles * q.split_parts
@@ -555,9 +565,9 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
                 }
                 ++ch;
             };
-            // where the adapters' term waits, and for which tokens there is one
+            // where the adapters' term waits, and the tokens that have one
             const uint32_t stash = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + 2 * BN + half * COLS;
-            uint32_t has[MW] = {};
+            uint32_t has[MW] = {}, own[MW];  // (of this part's tokens)
             if constexpr (IN_REGS) {
                 // A piece is 8 ranks of one slot: 16 bytes per lane, its row of the
                 // adapter, through the lane's own places in the staging slots (free
@@ -569,7 +579,6 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
                 const int per_slot = q.rank / 8;
                 const int pieces = ns * per_slot;
                 const bool in = m < p.Mdim;
-                uint32_t own[MW];  // this part's tokens
 #pragma unroll
                 for (int i = 0; i < MW; ++i)
                     own[i] = 0xffffffffu;
@@ -600,7 +609,8 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
                     }
                     asm volatile("cp.async.commit_group;" ::: "memory");
                 };
-                if constexpr (!A_MN)
+                constexpr bool RING = !A_MN && !SPLIT;  // a part has few slots
+                if constexpr (RING)
                     for (int i = 0; i < AHEAD - 1; ++i)
                         fetch();
                 int used = 0;
@@ -619,7 +629,7 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
                         has[i] |= mask[i];
                         any |= mask[i];
                     }
-                    if (A_MN && any == 0)
+                    if (SPLIT && any == 0)
                         continue;
 #pragma unroll 1
                     for (int r0 = 0; r0 < q.rank; r0 += RC) {
@@ -630,9 +640,15 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
                             if (k >= n8)
                                 continue;
                             if constexpr (!A_MN) {
-                                asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 2) : "memory");
-                                const uint4 v = ring[(used++ % AHEAD) * 32 + lane];
-                                fetch();
+                                uint4 v = make_uint4(0, 0, 0, 0);
+                                if constexpr (RING) {
+                                    asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 2) : "memory");
+                                    v = ring[(used++ % AHEAD) * 32 + lane];
+                                    fetch();
+                                } else if (in) {
+                                    v = *reinterpret_cast<const uint4 *>(
+                                        q.adapters + (static_cast<int64_t>(table[s].x) * p.Mdim + m) * q.rank + r0 + 8 * k);
+                                }
                                 const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                                 for (int j = 0; j < 4; ++j) {
@@ -738,7 +754,25 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
             }
             if (!ok)
                 break;
-            if constexpr (IN_REGS) {
+            if (IN_REGS && all_split) {
+                float *slab = q.scratch + quarter * 32 + lane +
+                              (static_cast<int64_t>(t * split_slabs(BN, q.split_parts) + q.split_parts) * BN + half * COLS) *
+                                  C::TILE_M;
+#pragma unroll
+                for (int c = 0; c < COLS; c += 16) {
+                    const uint32_t o16 = (own[c / 32] >> (c & 31)) & 0xffffu;
+                    const uint32_t m16 = (has[c / 32] >> (c & 31)) & 0xffffu;
+                    if (o16 == 0)
+                        continue;
+                    uint32_t r[32];
+                    tmem_ld_chunk<16>(stash + c, r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (o16 >> j & 1u)
+                            slab[(c + j) * C::TILE_M] = m16 >> j & 1u ? __uint_as_float(r[j]) : 0.f;
+                }
+            } else if constexpr (IN_REGS) {
                 // last, whenever the accumulators came, so that the order is always the same
 #pragma unroll
                 for (int c = 0; c < COLS; c += 16) {
@@ -755,8 +789,8 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
                 }
             }
             if (SPLIT && part >= 0) {
-                const int parts = all_split ? q.split_parts : 2;
-                const int y = ((t - split_first) * parts + part) * BN + half * COLS;  // scratch row
+                const int slabs = all_split ? split_slabs(BN, q.split_parts) : 2;
+                const int y = ((t - split_first) * slabs + part) * BN + half * COLS;  // scratch row
                 float *fslots = reinterpret_cast<float *>(slots);
 #pragma unroll
                 for (int c = 0; c < COLS; c += CH) {
@@ -864,8 +898,8 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
         atomicOr(p.status, 2);
 }
 
-// out = the parts of the split tiles added in order.  grid (split tiles, row groups);
-// Mdim is a multiple of 8.  scratch [tile][part][bn][tile_m].
+// out = the parts of the split tiles added in order.  grid (split tiles, row groups).
+// scratch [tile][part][bn][tile_m].
 constexpr int kJoinRows = 8;
 
 template <typename OutT>
@@ -894,10 +928,11 @@ __global__ void __launch_bounds__(256)
             a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
         }
         OutT *o = out + n * p.ldo + m;
-        store_out(o, __float_as_uint(a.x));
-        store_out(o + 1, __float_as_uint(a.y));
-        store_out(o + 2, __float_as_uint(a.z));
-        store_out(o + 3, __float_as_uint(a.w));
+        const float v[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (m + j < p.Mdim)
+                store_out(o + j, __float_as_uint(v[j]));
     }
 }
 

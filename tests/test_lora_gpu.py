@@ -171,6 +171,35 @@ def pick(t, rows):
     return t[rows].double()
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("order", ["random", "runs"])
+@pytest.mark.parametrize("M,K,V,R,N", [  # tiles of the logits cut along K
+    (1, 4096, 129, 8, 1), (2, 4096, 4096, 16, 4), (16, 2056, 1001, 64, 20), (17, 4096, 4097, 24, 5),
+    (32, 1544, 2048, 256, 3), (50, 4096, 3999, 16, 60), (64, 8192, 515, 40, 1), (128, 4096, 2000, 16, 9),
+    (127, 3200, 1023, 136, 40), (200, 4096, 600, 16, 3), (300, 4096, 4099, 64, 30), (700, 8200, 1300, 8, 257),
+])
+def test_forward_cut_along_the_reduction(M, K, V, R, N, order, dtype):
+    X, W, A, B, scale, ids = make(M, K, V, R, N, order=order)
+    logits, u = fwd(X, W, A, B, scale, ids, dtype)
+    ru, tu, ref, tol = ref_fwd(X, W, A, B, scale, ids, dtype)
+    close(u, ru, tu, "u")
+    close(logits, ref, tol, "logits")
+    again, _ = fwd(X, W, A, B, scale, ids, dtype)
+    assert torch.equal(logits, again)
+
+
+@pytest.mark.parametrize("M", [5, 70, 300])
+def test_cut_forward_keeps_bad_values_apart(M):
+    X, W, A, B, scale, ids = make(M, 4096, 700, 16, 3)
+    ids[::3] = 1
+    one, _ = fwd(X, W, A, B, scale, ids)
+    A2, B2 = A.clone(), B.clone()
+    A2[1], B2[1, 5:300] = float("nan"), float("inf")
+    two, _ = fwd(X, W, A2, B2, scale, ids)
+    o = ids != 1
+    assert torch.equal(one[o], two[o]) and torch.isnan(two[~o]).all()
+
+
 @pytest.mark.parametrize("M", [5, 260])
 def test_adapters_beyond_32_bit_offsets(M):
     K, V, R, N = 256, 32776, 128, 600   # B has 2.5e9 elements
