@@ -122,12 +122,14 @@ struct Split {
 };
 // Fewer tiles than units: the number of parts that takes the least time, counted in
 // k-blocks on the busiest unit, each part with what handing it over costs (about 3 us
-// for the 256 KB of a pair's tile, a k-block 0.3 us; narrow tiles a third of that) and
-// `join` for the second kernel.
+// for the 256 KB of a pair's tile, a k-block 0.3 us; narrow tiles less) and `join` for
+// the second kernel.  (Logits of 2 x 4096 x 4096 18 us against 27, 300 x 4096 x 4096 40
+// against 43, 64 x 4096 x 5000 27 against 35; both gradients of 60 x 792 x 73312 71 us
+// against 445, 32 x 2048 x 128256 135 against 735, 256 x 4096 x 128256 310 against 480.)
 Split split_all(int64_t tiles, int64_t units, int64_t num_kb, int64_t bn, int64_t tile_m, int64_t join)
 {
     Split s;
-    const int64_t cost = bn == 256 ? 20 : 8;
+    const int64_t cost = bn == 256 ? 20 : bn == 128 ? 16 : 8;
     int64_t best = num_kb;
     for (int64_t n = 2; n * 8 <= num_kb && n * tiles <= 2 * units; ++n) {
         const int64_t kb = ceil_div(ceil_div(num_kb, n), 8) * 8, parts = ceil_div(num_kb, kb);

@@ -582,12 +582,12 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
 #pragma unroll
                 for (int i = 0; i < MW; ++i)
                     own[i] = 0xffffffffu;
-                if (all_split) {
-                    const int lo = part * BN / q.split_parts, hi = (part + 1) * BN / q.split_parts;
-                    auto below = [](int x) -> uint32_t { return x <= 0 ? 0u : x >= 32 ? 0xffffffffu : (1u << x) - 1u; };
+                if (all_split) {  // every split_parts-th token
 #pragma unroll
-                    for (int i = 0; i < MW; ++i)
-                        own[i] = below(hi - half * COLS - i * 32) & ~below(lo - half * COLS - i * 32);
+                    for (int i = 0; i < MW; ++i) {
+                        const int c = i * 32 + lane;
+                        own[i] = __ballot_sync(0xffffffffu, c < COLS && (half * COLS + c) % q.split_parts == part);
+                    }
                 }
                 int fs = 0, fr = 0, fetched = 0;  // slot and rank block of the next fetch
                 if (lane == 0)
