@@ -80,8 +80,8 @@ GemmSpace gemm_space(int64_t M, int64_t Cdim, int64_t R, int64_t N, int bn, int3
 {
     GemmSpace g;
     g.tiles = ceil_div(M, bn);
-    g.parts = out_dtype == LMH_F32 ? 2 : 1;
-    g.stages = R <= 32 ? 1 : g.parts * ceil_div(R, 64);
+    g.parts = out_dtype == LMH_F32 ? 3 : 1;
+    g.stages = lmh::lora_stages(static_cast<int>(R), static_cast<int>(g.parts));
     g.max_slots = N < bn ? N : bn;
     g.slot_stride = (g.max_slots + 1) / 2 * 2;
     g.partial = 0;

@@ -6,13 +6,14 @@
 //
 // with a = the token's adapter.  The adapters' term goes into the same sums:
 // after the k-blocks of the shared product, each output tile takes one more
-// k-block (one or two per 64 ranks) per adapter that occurs among its tokens
+// k-block (up to three per 64 ranks) per adapter that occurs among its tokens
 // ("slot").  So the delta never travels to memory and back: separate from the
 // product it would read and write all logits once more (4.2 GB at 4096 x
 // 128256).  u is FP32, the tensor cores take BF16: for an FP32 output it is split
-// into u_hi + u_lo (2^-18 relative), B_a entering twice; for a BF16 output it is
-// rounded to BF16 once, as X itself is, which is no more than the output's own
-// rounding and takes half the k-blocks.
+// into three parts (FP32's 24 bits; two, 2^-18 of u, leave an error of 1.1e-6 of the
+// logits' norm where the term is as large as the rest), B_a entering three times; for
+// a BF16 output it is rounded to BF16 once, as X itself is, which is no more than the
+// output's own rounding and takes a third of the k-blocks.
 //
 // A slot's product is formed for the 32-aligned span of its tokens, and the
 // epilogue adds the columns of those tokens alone: an adapter that holds
@@ -49,10 +50,11 @@ namespace lmh {
 // pipe about 0.2 us: 4096 x 4096 x 128256 takes 3163, 3101, 3043 us with 8, 12, 16
 // and 2966 without.  FP32 dX: 8, because dlogits has one large term per row, the
 // target's, after which every MMA loses its share of the whole sum (9.8e-7 with
-// 12).  BF16 outputs round at 2e-3, so 64 (4e-6) do.
-__host__ __device__ constexpr int promote_kblocks(int out_bytes, bool gradient)
+// 12); the logits of up to 64 tokens: 8 too, since they wait for W and lose nothing by
+// it.  BF16 outputs round at 2e-3, so 64 (4e-6) do.
+__host__ __device__ constexpr int promote_kblocks(int out_bytes, bool gradient, int bn)
 {
-    return out_bytes == 4 ? (gradient ? 8 : 12) : 64;
+    return out_bytes == 4 ? (gradient || bn <= 64 ? 8 : 12) : 64;
 }
 
 constexpr int kSlotMaskWords = 8;  // one bit per token of a tile of up to 256
@@ -72,14 +74,22 @@ __host__ __device__ constexpr bool slot_last(int32_t i) { return i >> 12 & 1; } 
 // where it is formed by itself.
 __host__ __device__ constexpr int split_slabs(int bn, int parts) { return parts + (bn <= 128 ? 1 : 0); }
 
+// Ring stages (64 columns of the split u) of one slot.  Three parts: up to 16 ranks
+// {part 0, 1, 2, zeros} of 16 columns in one; up to 32 {part 0, 1} and {part 2, zeros}
+// of 32; above that a stage per part and 64 ranks.
+__host__ __device__ constexpr int lora_stages(int rank, int parts)
+{
+    return parts == 1 || rank > 32 ? parts * ((rank + 63) / 64) : rank <= 16 ? 1 : 2;
+}
+
 struct LoraParams {
     const int2 *count;         // per token tile: {slots, accumulators they take; 0: the shared one}
     const int2 *slot;          // [token tile][slot_stride]: {adapter, slot_info}
     const uint32_t *slot_mask; // [token tile][max_slots][kSlotMaskWords]: their tokens
     int32_t slot_stride;       // even
     int32_t max_slots;
-    int32_t parts;             // BF16 parts of u: 2, or 1 for a BF16 output
-    int32_t stages_per_slot;   // ring stages of one slot: 1 up to 32 ranks, then `parts` per 64
+    int32_t parts;             // BF16 parts of u: 3, or 1 for a BF16 output
+    int32_t stages_per_slot;   // ring stages of one slot: see lora_stages
     int32_t rank;
     int32_t split_parts;       // dX: parts every tile's reduction is cut into (0: whole tiles)
     int32_t part_kb;           // k-blocks of such a part (the last may have fewer)
@@ -119,7 +129,7 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
     constexpr bool IN_REGS = BN <= 128;
     constexpr uint32_t TMEM_COLS = lora_tmem_cols(BN);
     static_assert(RES * TMEM_COLS <= 512, "tensor memory of the resident CTAs");
-    constexpr int kPromote = promote_kblocks(sizeof(OutT), A_MN);
+    constexpr int kPromote = promote_kblocks(sizeof(OutT), A_MN, BN);
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -469,17 +479,19 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
                             ok = false;
                             break;
                         }
-                        if (q.parts == 2 && sps == 1) {
-                            // up to 32 ranks: columns 0..31 of u are its high parts,
-                            // 32..63 the low ones, against the same ranks of B_a
+                        if (q.parts == 3 && q.rank <= 16) {
                             mma(0, 0, joined);
+                            mma(0, 1, 1u);
                             mma(0, 2, 1u);
-                            if (q.rank > 16) {
-                                mma(1, 1, 1u);
+                        } else if (q.parts == 3 && q.rank <= 32) {
+                            mma(0, 0, j != 0 ? 1u : joined);
+                            mma(1, 1, 1u);
+                            if (j == 0) {
+                                mma(0, 2, 1u);
                                 mma(1, 3, 1u);
                             }
                         } else {
-                            // 64 ranks: the high parts, then, if there are two, the low ones
+                            // 64 ranks: one part after the other
                             const int steps = min(4, (q.rank - j / q.parts * 64 + kUmmaK - 1) / kUmmaK);
                             for (int k = 0; k < steps; ++k)
                                 mma(k, k, (j != 0 || k != 0) ? 1u : joined);

@@ -13,7 +13,7 @@
 //                       each adapter among the tokens the product of all 64 is
 //                       formed and the rows of that adapter's tokens are kept.
 //   lora_expand_kernel  sums the partials in a fixed order, scales, and writes
-//                       t (FP32), its split into BF16 high and low parts for the
+//                       t (FP32), its split into BF16 parts for the
 //                       GEMM, and the slots of every token tile
 //   lora_group_kernel   the tokens of each adapter, in order
 //   lora_split_kernel   t in that order as three BF16 parts (FP32's 24 bits)
@@ -312,9 +312,7 @@ __device__ __forceinline__ __nv_bfloat16 split_hi(float x, float &rest)
 
 // grid (token tiles of the GEMM, parts of `tokens` tokens).
 //   t    [M][R] FP32, scaled: u or g (0 for a token without adapter)
-//   ux   (or NULL) [tile][stages][bn][64] BF16.  Of two parts: up to 32 ranks one
-//        stage {high 0..31, low 0..31}, above that per 64 ranks a stage of high and
-//        one of low parts.  Of one part: a stage per 64 ranks
+//   ux   (or NULL) [tile][stages][bn][64] BF16: see lora_stages
 //   count, slot_table, slot_mask: see LoraParams (written by part 0)
 __global__ void __launch_bounds__(256)
     lora_expand_kernel(const float *__restrict__ partial, int32_t ranges, const int32_t *__restrict__ adapter,
@@ -390,16 +388,19 @@ __global__ void __launch_bounds__(256)
         const int tk = tok0 + j;
         if (tk >= bn)
             break;
-        const bool both = parts == 2 && stages == 1;
-        const bool low = both ? c0 >= 32 : parts == 2 && (st & 1);
-        const int r0 = both ? (c0 & 31) : st / parts * 64 + c0;
+        int part = st % parts, r0 = st / parts * 64 + c0;
+        if (parts == 3 && R <= 32) {
+            const int width = R <= 16 ? 16 : 32;  // columns of a part
+            part = st * 2 + c0 / width;
+            r0 = c0 % width;
+        }
         __nv_bfloat16 h[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const float v = r0 + e < Rpad ? val[j * Rpad + r0 + e] : 0.f;
-            float low_part;
-            const __nv_bfloat16 hi = split_hi(v, low_part);
-            h[e] = low ? __float2bfloat16_rn(low_part) : hi;
+            const float v = r0 + e < Rpad && part < 3 ? val[j * Rpad + r0 + e] : 0.f;
+            float rest, rest2;
+            const __nv_bfloat16 hi = split_hi(v, rest), mid = split_hi(rest, rest2);
+            h[e] = part == 0 ? hi : part == 1 ? mid : __float2bfloat16_rn(rest2);
         }
         *reinterpret_cast<uint4 *>(ux + ((tile * stages + st) * bn + tk) * 64 + c0) = *reinterpret_cast<uint4 *>(h);
     }

@@ -9,8 +9,8 @@ Tolerances, per element, with S the sum of the absolute values of the terms:
     MMAs): 2^-23 * (260 + terms / 8192) * S.
   row sums (u, g): the same per 128 terms (8 MMAs), parts added in FP64 or FP32,
     one rounding: 2^-23 * (12 + terms / 256) * S.
-  u in the second product, above 128 tokens: for an FP32 output two BF16 parts,
-    2^-17 of sum |u| |B|, for a BF16 output one, 2^-8 of it; beside u's own
+  u in the second product, above 128 tokens: for an FP32 output three BF16 parts,
+    2^-24 of sum |u| |B|, for a BF16 output one, 2^-8 of it; beside u's own
     tolerance carried through B.
   gradients dA, dB: 256 terms (3 x 16 MMAs) at a time: 2^-23 * (52 + tokens / 512) * S.
   BF16 outputs: half a BF16 step (2^-9 of the value's power of two, so at most
@@ -76,7 +76,7 @@ def gemm_eps(terms, dtype=torch.float32, chunk=768):
 
 
 def split_eps(M, dtype):
-    return 2.0 ** -24 if M <= 128 else 2.0 ** -17 if dtype == torch.float32 else 2.0 ** -8
+    return 2.0 ** -24 if M <= 128 or dtype == torch.float32 else 2.0 ** -8
 
 
 def ref_fwd(X, W, A, B, scale, ids, dtype=torch.float32):
