@@ -25,8 +25,8 @@
 // The sum over the reduction is kept in FP32 as FP32 should be: the tensor
 // cores' own accumulation loses about 2^-24 of the running sum at each MMA,
 // always towards zero, which grows with the length.  Here a tensor-memory
-// accumulator takes promote_kblocks k-blocks and the epilogue warps add it, rounded to nearest, to sums they hold in
-// registers, while the MMAs fill the other accumulator.
+// accumulator takes promote_kblocks k-blocks and the epilogue warps add it, rounded to
+// nearest, to sums they hold in registers, while the MMAs fill the other accumulator.
 //
 // Up to 128 tokens (one token tile, bound by the read of W) there is time to spare
 // on the epilogue warps and none in the handing over of accumulators, each about
@@ -155,8 +155,8 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
     const int num_kb = (p.Kdim + kBlockK - 1) / kBlockK;
     // Split along the reduction, the parts go to scratch (tmP) in FP32, where
     // lora_join_kernel adds them; the last part takes the slots.
-    // - Fewer tiles than units (few tokens; a narrow model, a small vocabulary): every tile into
-    //   split_parts parts, so that most units have one.  Where the epilogue warps form
+    // - Fewer tiles than units (few tokens; a narrow model, a small vocabulary): every
+    //   tile into split_parts parts, so that most units have one.  Where the epilogue warps form
     //   the adapters' term, each part takes that of its share of the tokens, and it
     //   goes to scratch as one part more: a token's sums are the same wherever in the
     //   batch it stands.
