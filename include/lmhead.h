@@ -277,9 +277,9 @@ LMH_API lmh_status_t lmhead_bwd_dw_acc(const void *dlogits, const void *X, float
  *           calls take it.   logits as lmhead_fwd.
  *   One kernel forms both products in the same sums, FP32 rounded to nearest
  *   every 768 terms of K or fewer (4096 for BF16 logits), so the base part is as
- *   lmhead_fwd's but with a smaller error and not bitwise equal to it.  Above 128
- *   tokens u enters the second product as three BF16 parts (FP32's 24 bits), or one
- *   for BF16 logits.  An adapter's values reach the tokens that use it and no
+ *   lmhead_fwd's but with a smaller error and not bitwise equal to it.  u enters the
+ *   second product with FP32's 24 bits (above 128 tokens as three BF16 parts), for
+ *   BF16 logits too.  An adapter's values reach the tokens that use it and no
  *   others, infinities and NaN included (for its own tokens an infinity may come
  *   out as NaN, since the parts of u multiply it one by one).  Any order of the
  *   tokens; those of one adapter next to each other cost least (each 256-token

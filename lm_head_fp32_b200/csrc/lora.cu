@@ -74,14 +74,13 @@ int64_t rank_pad(int64_t R) { return (R + 15) / 16 * 16; }
 // lmhead_bwd_dx_lora (Cdim = V).
 struct GemmSpace {
     int64_t partial, ux, count, slot, slot_mask, start, order, bytes;
-    int64_t tiles, parts, stages, max_slots, slot_stride;
+    int64_t tiles, stages, max_slots, slot_stride;
 };
-GemmSpace gemm_space(int64_t M, int64_t Cdim, int64_t R, int64_t N, int bn, int32_t out_dtype)
+GemmSpace gemm_space(int64_t M, int64_t Cdim, int64_t R, int64_t N, int bn)
 {
     GemmSpace g;
     g.tiles = ceil_div(M, bn);
-    g.parts = out_dtype == LMH_F32 ? 3 : 1;
-    g.stages = lmh::lora_stages(static_cast<int>(R), static_cast<int>(g.parts));
+    g.stages = lmh::lora_stages(static_cast<int>(R));
     g.max_slots = N < bn ? N : bn;
     g.slot_stride = (g.max_slots + 1) / 2 * 2;
     g.partial = 0;
@@ -358,7 +357,7 @@ lmh_status_t run_rows(const void *Y, const void *P, const float *scale, const in
                      reinterpret_cast<int2 *>(ws + g.count), reinterpret_cast<int2 *>(ws + g.slot),
                      reinterpret_cast<uint32_t *>(ws + g.slot_mask),
                      static_cast<int32_t>(bn), static_cast<int32_t>(g.slot_stride), static_cast<int32_t>(g.max_slots),
-                     static_cast<int32_t>(g.stages), static_cast<int32_t>(g.parts), M, static_cast<int32_t>(R), static_cast<int32_t>(rank_pad(R)),
+                     static_cast<int32_t>(g.stages), M, static_cast<int32_t>(R), static_cast<int32_t>(rank_pad(R)),
                      static_cast<int32_t>(N), static_cast<int32_t>(tokens), status);
 }
 
@@ -372,7 +371,6 @@ LoraParams lora_params(uint8_t *ws, const GemmSpace &g, int64_t R, const void *a
     q.slot_mask = reinterpret_cast<const uint32_t *>(ws + g.slot_mask);
     q.slot_stride = static_cast<int32_t>(g.slot_stride);
     q.max_slots = static_cast<int32_t>(g.max_slots);
-    q.parts = static_cast<int32_t>(g.parts);
     q.stages_per_slot = static_cast<int32_t>(g.stages);
     q.rank = static_cast<int32_t>(R);
     return q;
@@ -435,8 +433,8 @@ int64_t lmhead_lora_workspace_bytes(int64_t M, int64_t K, int64_t V, int64_t R, 
 {
     if (!lora_dims_ok(M, K, V, R, N))
         return -1;
-    const int64_t f = gemm_space(M, K, R, N, pick_bn(M, 16), LMH_F32).bytes + fwd_split(M, K, V).scratch;
-    const int64_t d = gemm_space(M, V, R, N, pick_bn(M, 64), LMH_F32).bytes + dx_split(M, K, V).scratch;
+    const int64_t f = gemm_space(M, K, R, N, pick_bn(M, 16)).bytes + fwd_split(M, K, V).scratch;
+    const int64_t d = gemm_space(M, V, R, N, pick_bn(M, 64)).bytes + dx_split(M, K, V).scratch;
     const int64_t w = grad_space(M, R, N).bytes;
     const int64_t fd = f > d ? f : d;
     return fd > w ? fd : w;
@@ -456,7 +454,7 @@ lmh_status_t lmhead_fwd_lora(const void *X, const void *W, const void *A, const 
         !aligned(logits, out_dtype == LMH_F32 ? 4 : 2))
         return LMH_ERR_MISALIGNED;
     const int bn = pick_bn(M, 16);
-    const GemmSpace g = gemm_space(M, K, R, N, bn, out_dtype);
+    const GemmSpace g = gemm_space(M, K, R, N, bn);
     const Split split = fwd_split(M, K, V);
     if (workspace_bytes < g.bytes + split.scratch)
         return LMH_ERR_INVALID_ARG;
@@ -507,7 +505,7 @@ lmh_status_t lmhead_bwd_dx_lora(const void *dlogits, const void *W, const void *
         !aligned(workspace, 256))
         return LMH_ERR_MISALIGNED;
     const int bn = pick_bn(M, 64);
-    const GemmSpace g = gemm_space(M, V, R, N, bn, out_dtype);
+    const GemmSpace g = gemm_space(M, V, R, N, bn);
     const Split split = dx_split(M, K, V);
     if (workspace_bytes < g.bytes + split.scratch)
         return LMH_ERR_INVALID_ARG;

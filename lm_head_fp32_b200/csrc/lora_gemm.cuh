@@ -9,11 +9,11 @@
 // k-block (up to three per 64 ranks) per adapter that occurs among its tokens
 // ("slot").  So the delta never travels to memory and back: separate from the
 // product it would read and write all logits once more (4.2 GB at 4096 x
-// 128256).  u is FP32, the tensor cores take BF16: for an FP32 output it is split
-// into three parts (FP32's 24 bits; two, 2^-18 of u, leave an error of 1.1e-6 of the
-// logits' norm where the term is as large as the rest), B_a entering three times; for
-// a BF16 output it is rounded to BF16 once, as X itself is, which is no more than the
-// output's own rounding and takes a third of the k-blocks.
+// 128256).  u is FP32, the tensor cores take BF16: it is split into three parts (FP32's
+// 24 bits; two, 2^-18 of u, leave an error of 1.1e-6 of the logits' norm where the term
+// is as large as the rest), B_a entering three times.  For a BF16 output too: rounded
+// to BF16, u would lose 2^-9 of the term, many of the output's steps where the term
+// and the rest cancel.
 //
 // A slot's product is formed for the 32-aligned span of its tokens, and the
 // epilogue adds the columns of those tokens alone: an adapter that holds
@@ -74,12 +74,14 @@ __host__ __device__ constexpr bool slot_last(int32_t i) { return i >> 12 & 1; } 
 // where it is formed by itself.
 __host__ __device__ constexpr int split_slabs(int bn, int parts) { return parts + (bn <= 128 ? 1 : 0); }
 
-// Ring stages (64 columns of the split u) of one slot.  Three parts: up to 16 ranks
+constexpr int kSplitParts = 3;  // BF16 parts of u
+
+// Ring stages (64 columns of the split u) of one slot: up to 16 ranks
 // {part 0, 1, 2, zeros} of 16 columns in one; up to 32 {part 0, 1} and {part 2, zeros}
 // of 32; above that a stage per part and 64 ranks.
-__host__ __device__ constexpr int lora_stages(int rank, int parts)
+__host__ __device__ constexpr int lora_stages(int rank)
 {
-    return parts == 1 || rank > 32 ? parts * ((rank + 63) / 64) : rank <= 16 ? 1 : 2;
+    return rank > 32 ? kSplitParts * ((rank + 63) / 64) : rank <= 16 ? 1 : 2;
 }
 
 struct LoraParams {
@@ -88,7 +90,6 @@ struct LoraParams {
     const uint32_t *slot_mask; // [token tile][max_slots][kSlotMaskWords]: their tokens
     int32_t slot_stride;       // even
     int32_t max_slots;
-    int32_t parts;             // BF16 parts of u: 3, or 1 for a BF16 output
     int32_t stages_per_slot;   // ring stages of one slot: see lora_stages
     int32_t rank;
     int32_t split_parts;       // dX: parts every tile's reduction is cut into (0: whole tiles)
@@ -348,7 +349,7 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
                                 ok = false;
                                 break;
                             }
-                            issue_slot(stage, m0, id, j / q.parts * 64, (nt * sps + j) * BN + row);
+                            issue_slot(stage, m0, id, j / kSplitParts * 64, (nt * sps + j) * BN + row);
                             ++issued;
                             if (++stage == S) {
                                 stage = 0;
@@ -479,11 +480,11 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
                             ok = false;
                             break;
                         }
-                        if (q.parts == 3 && q.rank <= 16) {
+                        if (q.rank <= 16) {
                             mma(0, 0, joined);
                             mma(0, 1, 1u);
                             mma(0, 2, 1u);
-                        } else if (q.parts == 3 && q.rank <= 32) {
+                        } else if (q.rank <= 32) {
                             mma(0, 0, j != 0 ? 1u : joined);
                             mma(1, 1, 1u);
                             if (j == 0) {
@@ -492,7 +493,7 @@ __global__ void __launch_bounds__(64 + 32 * EW, RES)
                             }
                         } else {
                             // 64 ranks: one part after the other
-                            const int steps = min(4, (q.rank - j / q.parts * 64 + kUmmaK - 1) / kUmmaK);
+                            const int steps = min(4, (q.rank - j / kSplitParts * 64 + kUmmaK - 1) / kUmmaK);
                             for (int k = 0; k < steps; ++k)
                                 mma(k, k, (j != 0 || k != 0) ? 1u : joined);
                         }

@@ -319,8 +319,8 @@ __global__ void __launch_bounds__(256)
                        const float *__restrict__ scale, float *__restrict__ t_out,
                        __nv_bfloat16 *__restrict__ ux, int2 *__restrict__ tile_count,
                        int2 *__restrict__ slot_table, uint32_t *__restrict__ slot_mask, int32_t bn,
-                       int32_t slot_stride, int32_t max_slots, int32_t stages, int32_t parts, int64_t M,
-                       int32_t R, int32_t Rpad, int32_t N, int32_t tokens, int32_t *status)
+                       int32_t slot_stride, int32_t max_slots, int32_t stages, int64_t M, int32_t R,
+                       int32_t Rpad, int32_t N, int32_t tokens, int32_t *status)
 {
     __shared__ int32_t ids[256];
     __shared__ int32_t warp_n[8];
@@ -388,8 +388,8 @@ __global__ void __launch_bounds__(256)
         const int tk = tok0 + j;
         if (tk >= bn)
             break;
-        int part = st % parts, r0 = st / parts * 64 + c0;
-        if (parts == 3 && R <= 32) {
+        int part = st % kSplitParts, r0 = st / kSplitParts * 64 + c0;
+        if (R <= 32) {
             const int width = R <= 16 ? 16 : 32;  // columns of a part
             part = st * 2 + c0 / width;
             r0 = c0 % width;
@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(256)
         __nv_bfloat16 h[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const float v = r0 + e < Rpad && part < 3 ? val[j * Rpad + r0 + e] : 0.f;
+            const float v = r0 + e < Rpad && part < kSplitParts ? val[j * Rpad + r0 + e] : 0.f;
             float rest, rest2;
             const __nv_bfloat16 hi = split_hi(v, rest), mid = split_hi(rest, rest2);
             h[e] = part == 0 ? hi : part == 1 ? mid : __float2bfloat16_rn(rest2);
