@@ -20,7 +20,8 @@
 // Continuations are compared by the FP64 value of total, ties by the lower beam, then
 // the higher logit (where FP64 cannot tell totals apart that differ), then the lower
 // token: an FP32 total has a step of 1e-6 at -15, which the gaps between
-// candidates of a large batch do meet.
+// candidates of a large batch do meet.  Within a beam the order is exact; between
+// beams it is as good as lse (see beam_scan_kernel).
 #pragma once
 #include <cfloat>
 #include <cstdint>
@@ -50,7 +51,7 @@ constexpr int kBeamDevBadParent = 0x10; // LMH_DEV_BAD_PARENT
 // A part's share of its row.
 struct BeamPartial {
     double sum;     // sum of 2^(x log2(e) - ref)
-    float ref;      // integer-valued: rint(max * log2(e)); -inf if no finite logit;
+    float ref;      // beam_ref(largest logit); -inf if no finite logit;
                     // FLT_MAX, -FLT_MAX beyond kBeamMaxRef: then sum of exp(x - max)
     int32_t count;  // candidates in the part's list
 };
@@ -79,6 +80,12 @@ __device__ __forceinline__ double warp_sum(double v)
         v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
+
+constexpr float kLog2e = 1.44269502162933349609f, kLog2eRest = 1.92596303e-8f;  // together log2(e)
+constexpr double kLog2eF64 = 1.4426950408889634074;
+
+// The integer power of two that sums are held against whose largest logit is x.
+__device__ __forceinline__ float beam_ref(float x) { return fmaxf(rintf(x * kLog2e), -FLT_MAX); }
 
 // 2^d for a whole number d <= 0 (0 below 2^-1022).
 __device__ __forceinline__ double pow2(float d)
@@ -302,9 +309,10 @@ __global__ void __launch_bounds__(kBeamThreads, 6)
                      int32_t batches, int32_t *status)
 {
     __shared__ uint32_t red[kBeamWarps];
-    __shared__ float red_ref[kBeamWarps];
+    __shared__ float red_top[kBeamWarps];
     __shared__ double red_sum[kBeamWarps];
-    __shared__ float noted[kBeamMaxBatches][kBeamThreads];  // maximum of each thread's batch
+    // of each thread's batch: its maximum, and its sum against beam_ref(maximum)
+    __shared__ float2 noted[kBeamMaxBatches][kBeamThreads];
     __shared__ uint16_t listed[kBeamWarps][kBeamHits];  // batch << 5 | lane
     __shared__ uint64_t buf[kBeamBuf];
     __shared__ uint64_t win[kBeamWarps];
@@ -325,14 +333,19 @@ __global__ void __launch_bounds__(kBeamThreads, 6)
     if (tid == 0)
         count = 0;
 
-    // Sum of exponentials against an integer power of two 2^ref: x log2(e) - ref is
-    // then rounded once per term, near its own size (log2(e) as two floats, so that
-    // large logits keep their last places), and a new ref scales the sum exactly.
-    // A new ref is taken only when a term would pass 2^8.  FP32 sums of 16 terms,
-    // joined in FP64, leave lse good to about 1e-8 (for logits up to 1e7).
-    constexpr float kLh = 1.44269502162933349609f, kLl = 1.92596303e-8f, kSlack = 8.f / kLh;
-    float ref = -INFINITY, top = -INFINITY, most = -INFINITY;
-    double sum = 0.0;
+    // Sums of exponentials against an integer power of two 2^ref: x log2(e) - ref is
+    // rounded once per term, near its own size (log2(e) as two floats, so that
+    // large logits keep their last places), and sums of different refs are joined by
+    // exact scaling.  Each sixteen has the ref of its own largest logit, so that the
+    // terms that count have small exponents.  A term is off by up to 2^-20 of itself
+    // (ex2.approx 2^-22, the argument's roundings, FP32 sums of 16), which is too much
+    // for a row that one token dominates: 5e-7 of lse, more than what separates close
+    // beams.  The sixteens looked at again below, which hold the part's best C logits,
+    // are therefore summed in FP64 there, and lse is off by at most 2^-20 of the share
+    // the others hold (for logits up to 1e7).  Measured: 1e-8 and less with 40 likely
+    // tokens (6e-8 with ex2.approx alone), 3.6e-8, the same for every row, with a bulk
+    // of many terms; 512 x 151936 69 us against 66.
+    float most = -INFINITY;
     bool any_bad = false;
     int nb = 0;
     for (int64_t v0 = begin; v0 < end; v0 += kBeamBatch, ++nb) {
@@ -340,25 +353,18 @@ __global__ void __launch_bounds__(kBeamThreads, 6)
         beam_load(x0, v0, V, off, x);
         float best;
         auto add = [&]() -> float {
-            if (best > top) {
-                const float r = fmaxf(rintf(best * kLh), -FLT_MAX);
-                // the first time ref is -inf and the sum 0
-                sum = ref > -INFINITY ? sum * pow2(ref - r) : 0.0;
-                ref = r;
-                top = best + kSlack;
-            }
+            const float ref = beam_ref(best);
             float s4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < kBeamPerThread; ++i) {
-                const float t = fmaf(x[i], kLl, fmaf(x[i], kLh, -ref));
+                const float t = fmaf(x[i], kLog2eRest, fmaf(x[i], kLog2e, -ref));
                 float y;
                 asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(t));
                 s4[i & 3] += y;
             }
             return (s4[0] + s4[1]) + (s4[2] + s4[3]);
         };
-        // A NaN, an infinity or a row that begins with -inf shows in the sum
-        // (fmaxf passes over NaN; -inf against a ref of -inf is NaN): once more then.
+        // A NaN or an infinity shows in the sum (fmaxf passes over NaN): once more then.
         float s;
         bool again = false;
         do {
@@ -370,21 +376,31 @@ __global__ void __launch_bounds__(kBeamThreads, 6)
                 best = fmaxf(best, x[i]);
             s = best < kBeamMaxLogit ? add() : NAN;
             if (again && !(s < INFINITY))
-                s = 0.f;  // nothing but -inf so far
+                s = 0.f;  // logits beyond kBeamMaxRef's: see beam_sum_far
             again = !again && !(s < INFINITY);
         } while (again);
-        sum += static_cast<double>(s);
-        noted[nb][tid] = best;
+        noted[nb][tid] = make_float2(best, s);
         most = fmaxf(most, best);
     }
+    const float warp_top = from_ordered(__reduce_max_sync(0xffffffffu, ordered(most)));
+    if (lane == 0)
+        red_top[warp] = warp_top;
     const float thr = block_threshold(most, C, red);
+    float top = red_top[0];
+#pragma unroll
+    for (int i = 1; i < kBeamWarps; ++i)
+        top = fmaxf(top, red_top[i]);
+    const float ref = top > -INFINITY ? beam_ref(top) : -INFINITY;
+    double sum = 0.0;
     // The sixteens that reach it: listed by the warp, then two at a time, a lane per
-    // logit (the loads are what takes time here).
+    // logit (the loads are what takes time here).  The others' sums are joined.
     static_assert(kBeamPerThread == 16, "half a warp reads one thread's batch");
     int hits = 0;
     for (int b = 0; b < nb; ++b) {
-        const float mine = noted[b][tid];
-        const bool hit = mine >= thr && mine > -INFINITY;
+        const float2 mine = noted[b][tid];
+        const bool hit = mine.x >= thr && mine.x > -INFINITY;
+        if (!hit && mine.x > -INFINITY)
+            sum += static_cast<double>(mine.y) * pow2(beam_ref(mine.x) - ref);
         const unsigned all = __ballot_sync(0xffffffffu, hit);
         const int place = hits + __popc(all & ((1u << lane) - 1u));
         if (hit && place < kBeamHits)
@@ -402,8 +418,10 @@ __global__ void __launch_bounds__(kBeamThreads, 6)
         const int at_hit = mine < hits ? listed[warp][mine] : 0;
         const int64_t v = beam_token<T>(begin + static_cast<int64_t>(at_hit >> 5) * kBeamBatch, lane & 15,
                                         warp * 32 + (at_hit & 31));
-        const float x = mine < hits && v < V ? BeamVec<T>::one(x0 + v) : -INFINITY;
-        const bool in = x >= thr && x < kBeamMaxLogit && x > -INFINITY;
+        float x = mine < hits && v < V ? BeamVec<T>::one(x0 + v) : -INFINITY;
+        x = x < kBeamMaxLogit ? x : -INFINITY;
+        sum += exp2(fma(static_cast<double>(x), kLog2eF64, -static_cast<double>(ref)));
+        const bool in = x >= thr && x > -INFINITY;
         const unsigned put = __ballot_sync(0xffffffffu, in);
         int at = 0;
         if (lane == 0)
@@ -414,13 +432,9 @@ __global__ void __launch_bounds__(kBeamThreads, 6)
     }
     if (__any_sync(0xffffffffu, any_bad) && lane == 0 && status)
         atomicOr(status, kBeamDevBadLogit);
-    // the warp's reference, then the block's; scaling by powers of two is exact
-    const float wref = from_ordered(__reduce_max_sync(0xffffffffu, ordered(ref)));
-    const double ws = warp_sum(ref > -INFINITY ? sum * pow2(ref - wref) : 0.0);
-    if (lane == 0) {
-        red_ref[warp] = wref;
-        red_sum[warp] = ws;
-    }
+    sum = warp_sum(sum);
+    if (lane == 0)
+        red_sum[warp] = sum;
     __syncthreads();
     const int n = count;
     BeamCand *out = cand + (row * parts + pt) * C;
@@ -437,8 +451,22 @@ __global__ void __launch_bounds__(kBeamThreads, 6)
                                      static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(k))};
         }
     } else {
-        // more values at the threshold than fit (many equal logits): the best one
-        // below the last, C times over the part
+        // more values at the threshold than fit (many equal logits, whose terms
+        // all err the same way): the whole sum in FP64, and the best one below the
+        // last, C times over the part
+        sum = 0.0;
+        for (int64_t v0 = begin; v0 < end; v0 += kBeamBatch) {
+#pragma unroll 1
+            for (int i = 0; i < kBeamPerThread; ++i) {
+                const int64_t v = beam_token<T>(v0, i, tid);
+                const float x = v < V ? BeamVec<T>::one(x0 + v) : -INFINITY;
+                if (x < kBeamMaxLogit)
+                    sum += exp2(fma(static_cast<double>(x), kLog2eF64, -static_cast<double>(ref)));
+            }
+        }
+        sum = warp_sum(sum);
+        if (lane == 0)
+            red_sum[warp] = sum;  // read after the barriers below
         uint64_t last = ~0ull;
         for (kept = 0; kept < C; ++kept) {
             uint64_t b = 0;
@@ -474,20 +502,14 @@ __global__ void __launch_bounds__(kBeamThreads, 6)
                                      static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(b))};
         }
     }
-    float r = red_ref[0];
-#pragma unroll
-    for (int i = 1; i < kBeamWarps; ++i)
-        r = fmaxf(r, red_ref[i]);
     if (tid == 0) {
         double s = 0.0;
 #pragma unroll
         for (int i = 0; i < kBeamWarps; ++i)
-            if (red_ref[i] > -INFINITY)
-                s += red_sum[i] * pow2(red_ref[i] - r);
-        part[row * parts + pt] = BeamPartial{s, r, kept};
+            s += red_sum[i];
+        part[row * parts + pt] = BeamPartial{s, ref, kept};
     }
-    // (threads whose logits lie that far below the part's largest added nothing)
-    if (fabsf(r) > kBeamMaxRef && r > -INFINITY)
+    if (fabsf(ref) > kBeamMaxRef && ref > -INFINITY)
         beam_sum_far(logits, cand, part, V, C, parts, batches, red_sum);
 }
 
