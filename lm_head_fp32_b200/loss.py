@@ -158,11 +158,13 @@ def lm_head_lora_cross_entropy(X: torch.Tensor, W: torch.Tensor, A: torch.Tensor
     -log softmax(X . W^T + scale[a] (X . A_a^T) . B_a^T)[target], a = adapter[i].
 
     X, W, target as in lm_head_cross_entropy (V % 8 == 0); A: [N, R, K], B: [N, V, R]
-    bfloat16, scale: [N] float32 (no gradient), adapter: [M] int32, -1 for a token
-    without adapter.  The backward gives X, A, B and, where it asks for one (a frozen
+    bfloat16, scale: [N] float32 (there is no gradient for it: one that asks for a
+    gradient is refused), adapter: [M] int32, -1 for a token without adapter.  The backward gives X, A, B and, where it asks for one (a frozen
     head does not), W bfloat16 gradients; the adapters' are summed in FP32 and
     rounded once.  A backward that accumulates into .grad can be captured into a CUDA
     graph while no eager graph of the same leaves is alive (autograd's own limit)."""
+    if scale.requires_grad and torch.is_grad_enabled():
+        raise ValueError("scale gets no gradient: pass scale.detach()")
     _check_inputs(X, W, target)
     if A.dim() != 3 or B.dim() != 3 or A.dtype != torch.bfloat16 or B.dtype != torch.bfloat16:
         raise ValueError("expected bfloat16 A [N,R,K] and B [N,V,R]")
