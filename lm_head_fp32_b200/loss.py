@@ -43,6 +43,26 @@ def _row_gradients(grad_loss: torch.Tensor) -> torch.Tensor:
     return grad_loss.to(torch.float32).contiguous()
 
 
+class _FirstOrder(torch.autograd.Function):
+    """A gradient as it is; to differentiate it once more is refused.  `on`: what it
+    depends on."""
+    @staticmethod
+    def forward(ctx, grad, *on):
+        return grad.view_as(grad)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("the LM-head loss can be differentiated once only")
+
+
+def _first_order(grads, on):
+    """The gradients of a backward pass.  Under create_graph they come from kernels that
+    autograd does not see; without a mark a second derivative would leave them out."""
+    if not torch.is_grad_enabled():
+        return grads
+    return tuple(g if g is None else _FirstOrder.apply(g, *on) for g in grads)
+
+
 class _LMHeadCrossEntropy(torch.autograd.Function):
     @staticmethod
     def forward(ctx, X, W, target, ignore_index, fused, main_grad, status):
@@ -78,7 +98,7 @@ class _LMHeadCrossEntropy(torch.autograd.Function):
             lmhead.lmhead_bwd_dw_acc(dl, X, ctx.main_grad, status)
         elif ctx.needs_input_grad[1]:
             dW = lmhead.lmhead_bwd_dw(dl, X, torch.empty_like(W), status)
-        return dX, dW, None, None, None, None, None
+        return *_first_order((dX, dW), (X, W, grad_loss)), None, None, None, None, None
 
 
 def lm_head_cross_entropy(X: torch.Tensor, W: torch.Tensor, target: torch.Tensor,
@@ -147,7 +167,8 @@ class _LMHeadLoraCrossEntropy(torch.autograd.Function):
         if need_w:
             with torch.cuda.device(dev):
                 dW = lmhead.lmhead_bwd_dw(dl, X, torch.empty_like(W), status)
-        return dX, dW, dA, dB, None, None, None, None, None
+        grads = _first_order((dX, dW, dA, dB), (X, W, A, B, grad_loss))
+        return *grads, None, None, None, None, None
 
 
 def lm_head_lora_cross_entropy(X: torch.Tensor, W: torch.Tensor, A: torch.Tensor, B: torch.Tensor,

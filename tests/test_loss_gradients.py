@@ -55,3 +55,21 @@ def test_gradients_asked_for_alone_are_those_of_all(wants):
     for k in "XWAB":
         assert (got[k] is None) == (k not in wants)
         assert got[k] is None or torch.equal(got[k], every[k])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lora", [False, True])
+def test_a_second_derivative_is_refused(lora):
+    X, W, A, B, scale, ids, t = inputs()
+    leaves = [p.requires_grad_() for p in ((X, W, A, B) if lora else (X, W))]
+
+    def out():
+        return (loss.lm_head_lora_cross_entropy(X, W, A, B, scale, ids, t) if lora
+                else loss.lm_head_cross_entropy(X, W, t)).sum()
+
+    ref = torch.autograd.grad(out(), leaves)
+    got = torch.autograd.grad(out(), leaves, create_graph=True)
+    for r, g in zip(ref, got):
+        assert torch.equal(r, g)          # the first derivative as ever
+        with pytest.raises(RuntimeError, match="once"):
+            (X.float().sum() + g.float().pow(2).sum()).backward(retain_graph=True)
