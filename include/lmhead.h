@@ -374,8 +374,9 @@ LMH_API int64_t beam_select_workspace_bytes(int64_t N, int64_t W, int64_t V, int
  *            sum_i o_i outer_stride[i] + n entry_stride + w beam_stride and has
  *            run_bytes contiguous bytes; outer and outer_stride are HOST arrays
  *            of num_outer (0..3) extents and strides.  All strides in bytes.
- *            Elements of a state must not overlap (checked from the strides);
- *            different states must not either (equal pointers are refused).
+ *            Elements of a state must not overlap, nor different states: both are
+ *            checked, from the strides and the pointers, and refused
+ *            (LMH_ERR_INVALID_ARG).  States that lie between each other's rows are fine.
  *   parents  [N,W] int32 (beam_select's next_beam).  A parent outside [0, W)
  *            sets LMH_DEV_BAD_PARENT and leaves that beam's state as it was.
  *   Limits: N <= 65535, W <= 64.  Any alignment: 16-byte copies where the

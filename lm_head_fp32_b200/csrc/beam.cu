@@ -84,6 +84,32 @@ lmh_status_t dispatch_reorder(const lmh::ReorderParams &p, int64_t N, int num_st
     return LMH_ERR_UNSUPPORTED;
 }
 
+// The geometry of a state: dimensions from the smallest stride up, each of which steps
+// over all that lies below it (`below` bytes, from the first to the last).
+struct Geometry {
+    int64_t run = 0;
+    int n = 0;
+    int64_t extent[5], stride[5], below[5];
+};
+
+// Whether two states of this geometry share memory, d bytes apart: whether two elements,
+// one of each, come to lie within a run of each other.  In every dimension only the two
+// steps next to d can bring them together, since all that lies below moves them by less.
+bool states_meet(const Geometry &g, int64_t d, int dim)
+{
+    if (dim < 0)
+        return d > -g.run && d < g.run;
+    const int64_t s = g.stride[dim];
+    const int64_t q0 = d >= 0 ? d / s : -((-d + s - 1) / s);  // rounded down
+    for (int64_t q = q0; q <= q0 + 1; ++q) {
+        const int64_t left = d - q * s;
+        if (q > -g.extent[dim] && q < g.extent[dim] && left > -g.below[dim] && left < g.below[dim] &&
+            states_meet(g, left, dim - 1))
+            return true;
+    }
+    return false;
+}
+
 }  // namespace
 
 extern "C" {
@@ -173,12 +199,17 @@ lmh_status_t beam_reorder(void *const *states, int64_t num_states, const int32_t
     if (run_bytes > kMaxSpan)
         return LMH_ERR_INVALID_ARG;
     int64_t span = run_bytes;
+    Geometry geometry;
+    geometry.run = run_bytes;
     uint64_t align = static_cast<uint64_t>(run_bytes) | 16u;
     for (int i = 0; i < nd; ++i) {
         if (ext[i] == 1)
             continue;
         if (str[i] < span || str[i] > kMaxSpan / ext[i])
             return LMH_ERR_INVALID_ARG;
+        geometry.extent[geometry.n] = ext[i];
+        geometry.stride[geometry.n] = str[i];
+        geometry.below[geometry.n++] = span;
         span += (ext[i] - 1) * str[i];
         align |= static_cast<uint64_t>(str[i]);
     }
@@ -186,9 +217,14 @@ lmh_status_t beam_reorder(void *const *states, int64_t num_states, const int32_t
     for (int64_t i = 0; i < num_states; ++i) {
         if (!states[i])
             return LMH_ERR_INVALID_ARG;
-        for (int64_t j = 0; j < i; ++j)
-            if (states[j] == states[i])
-                return LMH_ERR_INVALID_ARG;  // it would be moved twice
+        for (int64_t j = 0; j < i; ++j) {
+            // what two states share would be moved twice, by blocks that do not wait for each other
+            const uintptr_t a = reinterpret_cast<uintptr_t>(states[i]), b = reinterpret_cast<uintptr_t>(states[j]);
+            const uintptr_t apart = a > b ? a - b : b - a;
+            if (apart < static_cast<uintptr_t>(span) &&
+                states_meet(geometry, static_cast<int64_t>(apart), geometry.n - 1))
+                return LMH_ERR_INVALID_ARG;
+        }
         p.state[i] = static_cast<uint8_t *>(states[i]);
         align |= reinterpret_cast<uintptr_t>(states[i]);
     }

@@ -420,7 +420,8 @@ def beam_reorder(states, parents: torch.Tensor, entry_dim: int = 0,
     put in the order of its beams' parents, in place: state[.., n, w, ..] becomes the
     old state[.., n, parents[n, w], ..], with n in dimension entry_dim and w in the
     next.  parents: [N, W] int32, as beam_select's next_beam.  Strided views (the
-    filled part of a cache) are taken as they are."""
+    filled part of a cache) are taken as they are.  States that share memory are
+    refused (among each 128 of the list, one launch's worth)."""
     states = [states] if isinstance(states, torch.Tensor) else list(states)
     if parents.dim() != 2 or not states:
         raise ValueError("expected parents [N,W] and at least one state")
