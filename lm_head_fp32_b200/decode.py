@@ -40,7 +40,7 @@ class BeamDecoder:
         self.W, self.A, self.B, self.scale, self.eos = W, A, B, scale, int(eos)
         self.entries, self.beams = int(entries), int(beams)
         V, K = W.shape
-        M, C = self.entries * self.beams, min(2 * self.beams, self.beams * V)
+        M, C = self.entries * self.beams, 2 * self.beams
         n = lmhead.beam_select_workspace_bytes(self.entries, self.beams, V, C)
         if n < 0:
             raise ValueError(f"{entries} x {beams} beams over {V} tokens are out of range")

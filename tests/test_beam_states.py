@@ -7,7 +7,7 @@ import random
 import pytest
 import torch
 
-from lm_head_fp32_b200 import lmhead
+from lm_head_fp32_b200 import decode, lmhead
 
 P = ctypes.c_void_p
 BASE = 0x10000000
@@ -96,3 +96,54 @@ def test_views_that_share_rows_are_refused():
     with pytest.raises(lmhead.LmhError):
         lmhead.beam_reorder([cache[:, :, :30], cache[:, :, 10:]], par)
     lmhead.beam_reorder([cache[:, :, :20], cache[:, :, 20:]], par)
+
+
+def decoder(V, eos, device, E=2, beams=2, K=16):
+    W = torch.ones((V, K), dtype=torch.bfloat16, device=device)
+    return decode.BeamDecoder(W, E, beams, eos=eos)
+
+
+def test_decoder_buffers_of_a_vocabulary_of_one_token():
+    for eos in (-1, 0):
+        d = decoder(1, eos, "cpu")
+        assert d.cand_score.shape == d.cand_beam.shape == d.cand_token.shape == (2, 4)
+
+
+@pytest.mark.gpu
+def test_decoder_over_a_vocabulary_of_one_token():
+    inf = float("inf")
+    X = torch.ones((4, 16), dtype=torch.bfloat16, device="cuda")
+    d = decoder(1, 0, "cuda")
+    tokens, parents, scores = d.step(X)
+    # its one token ends every sequence
+    assert d.cand_score.tolist() == [[0.0, -inf, -inf, -inf]] * 2
+    assert d.cand_token.tolist() == [[0, -1, -1, -1]] * 2 and scores.tolist() == [[-inf, -inf]] * 2
+    d = decoder(1, -1, "cuda")
+    for _ in range(3):
+        tokens, parents, scores = d.step(X)
+        assert scores.tolist() == [[0.0, -inf]] * 2 and parents.tolist() == [[0, 1]] * 2
+    assert int(d.status.item()) == 0
+
+
+@pytest.mark.gpu
+def test_decoder_leaves_entries_that_are_done():
+    E, beams, K, V = 3, 4, 64, 500
+    gen = torch.Generator().manual_seed(2)
+    W = torch.randn((V, K), generator=gen).to(torch.bfloat16).cuda()
+    a, b = (decode.BeamDecoder(W, E, beams, eos=7) for _ in range(2))
+    hist = [torch.arange(E * beams * 5, device="cuda").view(E, beams, 5).clone() for _ in range(2)]
+    done = torch.tensor([0, 1, 0], dtype=torch.int32, device="cuda")
+    for step in range(3):
+        X = torch.randn((E * beams, K), generator=gen).to(torch.bfloat16).cuda()
+        before, kept = b.scores.clone(), hist[1][1].clone()
+        a.step(X, hist[0])
+        b.step(X, hist[1], done=done if step else None)
+        for e in (0, 2):
+            for f in ("tokens", "parents", "scores", "cand_score", "cand_beam", "cand_token"):
+                assert torch.equal(getattr(a, f)[e], getattr(b, f)[e])
+            assert torch.equal(hist[0][e], hist[1][e])
+        if step:
+            assert torch.equal(b.scores[1], before[1]) and torch.equal(hist[1][1], kept)
+            assert b.parents[1].tolist() == [0, 1, 2, 3] and b.cand_beam[1].tolist() == [-1] * 8
+            assert b.tokens[1].tolist() == [7] * 4
+    assert int(b.status.item()) == 0
