@@ -301,10 +301,11 @@ __global__ void __launch_bounds__(kRowsThreads)
     }
 }
 
-// x as BF16 high part and remainder; an x with no finite remainder has none.
+// x as BF16 high part and remainder, the part towards zero: three of them hold FP32's
+// 24 bits, and the largest x have a finite one.  An infinite x has no remainder.
 __device__ __forceinline__ __nv_bfloat16 split_hi(float x, float &rest)
 {
-    const __nv_bfloat16 h = __float2bfloat16_rn(x);
+    const __nv_bfloat16 h = __float2bfloat16_rz(x);
     const float hf = __bfloat162float(h);
     rest = fabsf(hf) < INFINITY ? x - hf : 0.f;
     return h;

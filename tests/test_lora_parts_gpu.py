@@ -113,3 +113,33 @@ def test_adapter_gradients_keep_every_bit(R):
         if a >= 0:
             rA[a, :, i + 3], rB[a, i] = g[i] * -2.0, u[i] * 0.5
     assert torch.equal(dA, rA) and torch.equal(dB, rB)
+
+
+LARGEST = torch.finfo(torch.float32).max   # 24 bits; rounded to nearest BF16 it would be infinite
+
+
+@pytest.mark.parametrize("M", [5, 140, 300])
+@pytest.mark.parametrize("R", [8, 32, 64])
+def test_the_largest_u_and_g_stay_finite(M, R):
+    K, V, N = 64, 264, 2
+    X, W, A, B = (torch.zeros(s, dtype=B16, device=DEV) for s in ((M, K), (V, K), (N, R, K), (N, V, R)))
+    X[:, 0], A[:, 3, 0], B[:, :, 3] = 1.0, 1.0, 2.0 ** -126
+    scale = torch.tensor([LARGEST, -LARGEST], device=DEV)
+    ids = (torch.arange(M, device=DEV) % 2).int()
+    u, logits = guarded_empty((M, R)), guarded_empty((M, V))
+    ws = guarded_empty((lmhead.lmhead_lora_workspace_bytes(M, K, V, R, N) // 256 * 256 + 256,), torch.uint8)
+    lmhead.lmhead_fwd_lora(X, W, A, B, scale, ids, u, logits, ws)
+    want = scale[ids.long()]
+    torch.cuda.synchronize()
+    assert torch.equal(u[:, 3], want) and not u[:, :3].any() and not u[:, 4:].any()
+    assert torch.equal(logits, (want * 2.0 ** -126)[:, None].expand(M, V))
+    # the gradients' split of the same u, one token per column
+    dl = torch.zeros((M, V), dtype=B16, device=DEV)
+    at = torch.arange(min(M, V), device=DEV)
+    dl[at, at] = 2.0 ** -126
+    dA, dB = guarded_empty((N, R, K)), guarded_empty((N, V, R))
+    lmhead.lmhead_bwd_lora(dl, X, u, torch.zeros_like(u), ids, dA, dB, ws)
+    torch.cuda.synchronize()
+    ref = torch.zeros((N, V, R), device=DEV)
+    ref[ids[at].long(), at, 3] = want[at] * 2.0 ** -126
+    assert torch.equal(dB, ref) and not dA.any()
