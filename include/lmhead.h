@@ -276,7 +276,8 @@ LMH_API lmh_status_t lmhead_bwd_dw_acc(const void *dlogits, const void *X, float
  *   u       [M,R] FP32, written (0 for a token without adapter); the backward
  *           calls take it.   logits as lmhead_fwd.
  *   One kernel forms both products in the same sums, FP32 rounded to nearest
- *   every 768 terms of K or fewer (4096 for BF16 logits), so the base part is as
+ *   every 768 terms of K or fewer (4096 for BF16 logits, where the tiles are not cut
+ *   along K), so the base part is as
  *   lmhead_fwd's but with a smaller error and not bitwise equal to it.  u enters the
  *   second product with FP32's 24 bits (above 128 tokens as three BF16 parts), for
  *   BF16 logits too.  An adapter's values reach the tokens that use it and no
@@ -302,9 +303,9 @@ LMH_API int64_t lmhead_lora_workspace_bytes(int64_t M, int64_t K, int64_t V, int
 /* The input gradient of lmhead_fwd_lora:
  *   g[i,:]  = scale[a] dlogits[i,:] . B_a          (written, [M,R] FP32)
  *   dX[i,:] = dlogits[i,:] . W + g[i,:] . A_a      (FP32 or BF16)
- * summed as in lmhead_fwd_lora (FP32 dX: every 512 terms of V).  Requirements
- * as there, and V % 8 == 0,
- * dlogits, g and dX 16-byte aligned.  Deterministic. */
+ * summed as in lmhead_fwd_lora (FP32 dX: every 512 terms of V, BF16 dX: every 4096),
+ * g with FP32's 24 bits.  Requirements as there, and V % 8 == 0, dlogits, g and dX
+ * 16-byte aligned.  Deterministic. */
 LMH_API lmh_status_t lmhead_bwd_dx_lora(const void *dlogits, const void *W, const void *A,
                                         const void *B, const float *scale, const int32_t *adapter,
                                         float *g, void *dX, int32_t out_dtype, void *workspace,

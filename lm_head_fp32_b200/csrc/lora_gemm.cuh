@@ -51,7 +51,8 @@ namespace lmh {
 // and 2966 without.  FP32 dX: 8, because dlogits has one large term per row, the
 // target's, after which every MMA loses its share of the whole sum (9.8e-7 with
 // 12); the logits of up to 64 tokens: 8 too, since they wait for W and lose nothing by
-// it.  BF16 outputs round at 2e-3, so 64 (4e-6) do.
+// it.  BF16 outputs round at 2e-3, so 64 (4e-6) do; BF16 logits whose tiles are cut along
+// K are summed in FP32 scratch, and as FP32 logits are.
 __host__ __device__ constexpr int promote_kblocks(int out_bytes, bool gradient, int bn)
 {
     return out_bytes == 4 ? (gradient || bn <= 64 ? 8 : 12) : 64;
@@ -92,7 +93,7 @@ struct LoraParams {
     int32_t max_slots;
     int32_t stages_per_slot;   // ring stages of one slot: see lora_stages
     int32_t rank;
-    int32_t split_parts;       // dX: parts every tile's reduction is cut into (0: whole tiles)
+    int32_t split_parts;       // parts every tile's reduction is cut into (0: whole tiles)
     int32_t part_kb;           // k-blocks of such a part (the last may have fewer)
     float *scratch;            // [tile][split_slabs][BN][tile's rows]
     const __nv_bfloat16 *adapters;  // [adapter][Mdim][rank], A_MN: [adapter][rank][Mdim]
