@@ -11,8 +11,8 @@
 //                      logits.  A stream like the cross-entropy forward that also
 //                      notes the maximum of each thread's 16 logits; the maxima
 //                      give a threshold that C logits reach and few others, and
-//                      only the sixteens that reach it are looked at again (62 us at
-//                      512 x 151936, 5.0 TB/s; candidates kept as they stream, against
+//                      only the sixteens that reach it are looked at again (66 us at
+//                      512 x 151936, 4.9 TB/s; candidates kept as they stream, against
 //                      the threshold of the first batch, cost 33 instructions per
 //                      logit and 103 us)
 //   beam_merge_kernel  one CTA per batch entry: lse of every beam, the best C
@@ -342,9 +342,10 @@ __global__ void __launch_bounds__(kBeamThreads, 6)
     // for a row that one token dominates: 5e-7 of lse, more than what separates close
     // beams.  The sixteens looked at again below, which hold the part's best C logits,
     // are therefore summed in FP64 there, and lse is off by at most 2^-20 of the share
-    // the others hold (for logits up to 1e7).  Measured: 1e-8 and less with 40 likely
-    // tokens (6e-8 with ex2.approx alone), 3.6e-8, the same for every row, with a bulk
-    // of many terms; 512 x 151936 69 us against 66.
+    // the others hold (for logits up to 1e7).  Measured with 40 likely tokens:
+    // 1e-9 with 16 candidates, 1.8e-8 with one (6e-8 with ex2.approx alone); with a bulk
+    // of many terms 3.6e-8, nearly the same for every row.  512 x 151936, selection and
+    // merge: 69 us against 66.
     float most = -INFINITY;
     bool any_bad = false;
     int nb = 0;
@@ -804,7 +805,7 @@ struct ReorderParams {
 // is another takes over, and only then writes.  No row that stays is touched,
 // and a row that several beams take is read from memory once (L1 serves the
 // rest), so the traffic is the rows wanted plus the rows changed: bound by HBM (16
-// caches of 16 x 4 beams, 2.8 GB moved: 395 us; 489 us with one column under way
+// caches of 16 x 4 beams, 2.5 GB moved: 388 us, 6.5 TB/s; a quarter more with one column under way
 // per thread instead of two).
 // MAXW bounds W at compile time, so that the column's values stay in registers:
 // vectors of 16 bytes up to 16 beams, 8 up to 32, 4 up to 64.
